@@ -78,7 +78,7 @@ typedef enum {
   LS_ERR_UNSUPPORTED = 2,        /* valid but unsupported shape or dtype */
   LS_ERR_WORKSPACE_TOO_SMALL = 3,
   LS_ERR_CUDA = 4,               /* a CUDA runtime/driver call failed */
-  LS_ERR_DEVICE_BOUNDS = 5,      /* device saw a page id outside the pool */
+  LS_ERR_DEVICE_BOUNDS = 5,      /* device saw a page id, slot, length or target out of range */
   LS_ERR_DEVICE_TIMEOUT = 6      /* a device-side bounded wait ran out */
 } ls_status;
 
@@ -374,6 +374,145 @@ LS_API ls_status ls_replay_fwd_noalloc(const ls_attn_desc* desc, const ls_prompt
 
 /* Bytes of the fixed scratch ls_replay_fwd_noalloc uses (64 MiB). */
 LS_API size_t ls_replay_fwd_noalloc_scratch_bytes(void);
+
+/* ---------------------------------------------------------------------------
+ * Rollout and scoring: the quantised K/V cache, attention of new tokens over
+ * it, and log-probabilities over the vocabulary.  A GRPO step decodes the
+ * group's responses over the captured prompt, scores the sampled tokens and
+ * starts the backward pass from their log-probabilities; the pages name these
+ * stages (the five-stage transaction of the review's mind map, capture to
+ * policy replay) and give no interface, so the interfaces are this library's.
+ * ------------------------------------------------------------------------- */
+
+/* How a cache holds a row (one token's K or V of one KV head).
+ *   LS_CACHE_F32, LS_CACHE_BF16: the values.
+ *   LS_CACHE_E4M3: 8-bit codes (4 exponent bits, 3 of mantissa, no infinity)
+ *     and one exponent e per row, value = code * 2^e.  ls_cache_write takes
+ *     the least e with max|row| <= 448 * 2^e (not below -126; 0 for a row of
+ *     zeros) and rounds to nearest even, so a value keeps a relative error of
+ *     2^-4 down to max|row| / 2^15.  e = -128 marks a row that held an
+ *     infinity or a NaN: all of it reads as NaN. */
+typedef enum { LS_CACHE_F32 = 0, LS_CACHE_BF16 = 1, LS_CACHE_E4M3 = 2 } ls_cache_format;
+
+/* A paged cache of one layer (device pointers).  k, v: [pool_pages][Hkv][S_p][d]
+ * in the format's elements; k_exp, v_exp: int8 [pool_pages][Hkv][S_p], E4M3
+ * only (NULL otherwise).  head_dim in {64, 128, 256}.  A pool in bf16 or
+ * float32 is laid out as ls_prompt_kv's, so a captured prompt is a cache as
+ * it stands.  A slot is a row's place: page * S_p + row in the page. */
+typedef struct {
+  int32_t format;
+  int32_t hkv;
+  int32_t head_dim;
+  int32_t page_size;
+  int64_t pool_pages;
+  void* k;
+  void* v;
+  int8_t* k_exp;
+  int8_t* v_exp;
+} ls_kv_cache;
+
+/* Writes token t's rows of k, v (src_dtype; heads contiguous, token t at
+ * element t * k_stride / t * v_stride, both multiples of 8) into slot
+ * slots[t].  A negative slot skips the token; one past the pool is skipped and
+ * reported through ws's status word (ws may be NULL).  Two tokens of one call
+ * must not share a slot.  n_tok == 0 is a no-op. */
+LS_API ls_status ls_cache_write(const ls_kv_cache* cache, int32_t src_dtype, const void* k,
+                                const void* v, int64_t k_stride, int64_t v_stride,
+                                const int64_t* slots, int64_t n_tok, void* ws, size_t ws_bytes,
+                                void* stream);
+
+/* Reads slots[t] into token t of k, v ([n_tok][Hkv][d], dst_dtype).  E4M3
+ * values are exact in both dtypes (bf16 values below 2^-133 aside).  A negative slot
+ * gives zeros, one past the pool zeros and the status word. */
+LS_API ls_status ls_cache_read(const ls_kv_cache* cache, const int64_t* slots, int64_t n_tok,
+                               int32_t dst_dtype, void* k, void* v, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/* Attention of each sequence's new tokens over its pages, in which the new
+ * tokens' own K/V already are.  Sequence b has query tokens q_start[b] ..
+ * q_start[b+1]-1 of q and keys 0 .. kv_len[b]-1 (key j in page
+ * page_table[b][j / S_p], row j % S_p).  With causal, its token i of n sees
+ * keys up to kv_len[b] - n + i, else all; o is the softmax's mean of V, lse
+ * its natural log-sum-exp (scale included).  A token that sees no key
+ * gives o = 0, lse = -infinity.  Rows of the pages past kv_len may hold
+ * anything; a NaN in a key that a token sees makes that token's rows NaN (in
+ * a bf16 or float32 value row, which weights of 0 multiply too, perhaps also
+ * those of the sequence's earlier tokens in the call).  Without causal, several members' tokens over
+ * a prompt that they share are one sequence; a float32 o and lse are then
+ * parts for ls_lse_merge.
+ *   q_dtype / o_dtype: o_dtype is q_dtype or LS_DTYPE_F32.
+ *   max_q, max_kv: upper bounds of the lengths, for planning and the
+ *     workspace; a longer sequence of queries is refused on the device (its
+ *     o and lse are not written, the status word says so), a longer kv_len is
+ *     computed, more slowly.  kv_len is at most pages_per_seq * S_p (more is
+ *     cut there and reported).
+ *   q_stride: elements from one token of q to the next (a multiple of 8, at
+ *     least Hq * d); o is contiguous. */
+typedef struct {
+  int32_t q_dtype;
+  int32_t o_dtype;
+  int32_t hq;
+  int32_t batch;
+  int64_t total_q;
+  int32_t max_q;
+  int32_t causal;
+  int64_t max_kv;
+  int64_t q_stride;
+  float softmax_scale;
+} ls_cached_attn_desc;
+
+LS_API ls_status ls_cached_attn_workspace_size(const ls_cached_attn_desc* desc,
+                                               const ls_kv_cache* cache, size_t* bytes);
+
+/* q [total_q][Hq][d]; q_start int32 [batch+1] from 0 to total_q; kv_len int64
+ * [batch]; page_table int32 [batch][pages_per_seq]; o [total_q][Hq][d]; lse
+ * float32 [total_q][Hq].  All on the device.  A page id outside the pool that
+ * a length reaches holds no keys and is reported. */
+LS_API ls_status ls_cached_attn(const ls_cached_attn_desc* desc, const ls_kv_cache* cache,
+                                const void* q, const int32_t* q_start, const int64_t* kv_len,
+                                const int32_t* page_table, int64_t pages_per_seq, void* o,
+                                float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Log-probabilities of target tokens over a large vocabulary and their
+ * gradients, without the logits in memory: with x_v = logit_scale * (h_n . w_v),
+ *   lse_n = log sum_v exp(x_v),  logp_n = x_target - lse_n  (minus the softmax
+ *   cross entropy),  d logp_n / d x_v = [v = target] - exp(x_v - lse_n).
+ * h [n_rows][hidden], w [vocab][hidden] in dtype, row strides in elements.
+ * A row whose target is ignore_index has logp 0 and no gradient (its lse is
+ * still written); any other target outside [0, vocab) is treated the same and
+ * reported through the status word.  An ignored row's h and d_logp reach no
+ * other row's results, but dw multiplies its h by 0: it has to be finite there.
+ * Arithmetic is float32; dh and dw are rounded to dtype once.
+ *   piece: vocabulary columns whose gradient is held at a time in the backward
+ *     (0: chosen from n_rows); the workspace grows with it. */
+typedef struct {
+  int32_t dtype;
+  int32_t hidden;
+  int32_t vocab;
+  int32_t piece;
+  int64_t n_rows;
+  int64_t h_stride;
+  int64_t w_stride;
+  int64_t ignore_index;
+  float logit_scale;
+} ls_vocab_desc;
+
+/* with_grad != 0: enough for the backward too (one buffer serves both). */
+LS_API ls_status ls_vocab_logprob_workspace_size(const ls_vocab_desc* desc, int32_t with_grad,
+                                                 size_t* bytes);
+
+/* targets int64 [n_rows]; logp, lse float32 [n_rows]. */
+LS_API ls_status ls_vocab_logprob_fwd(const ls_vocab_desc* desc, const void* h, const void* w,
+                                      const int64_t* targets, float* logp, float* lse, void* ws,
+                                      size_t ws_bytes, void* stream);
+
+/* lse: what the forward wrote for the same inputs; d_logp float32 [n_rows]:
+ * the loss's gradient for logp.  dh [n_rows][hidden], dw [vocab][hidden]
+ * (contiguous, dtype) are overwritten; either may be NULL. */
+LS_API ls_status ls_vocab_logprob_bwd(const ls_vocab_desc* desc, const void* h, const void* w,
+                                      const int64_t* targets, const float* lse,
+                                      const float* d_logp, void* dh, void* dw, void* ws,
+                                      size_t ws_bytes, void* stream);
 
 /* Synchronises the stream, then reports the device status word of ws
  * (LS_OK, LS_ERR_DEVICE_BOUNDS or LS_ERR_DEVICE_TIMEOUT) and clears it. */

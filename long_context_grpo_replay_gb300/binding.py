@@ -23,6 +23,10 @@ __all__ = [
     "ls_replay_fwd_part", "ls_replay_bwd_part", "ls_sum_parts",
     "GdnDesc", "LS_GDN_EXACT", "LS_GDN_TENSOR_CORE", "LS_GDN_BWD_REUSES_FORWARD", "ls_gdn_workspace_size", "ls_gdn_replay_fwd",
     "ls_gdn_replay_bwd", "ls_stage_pages",
+    "LS_CACHE_F32", "LS_CACHE_BF16", "LS_CACHE_E4M3", "KvCache", "CachedAttnDesc", "VocabDesc",
+    "kv_cache_from", "cached_attn_desc", "vocab_desc", "ls_cache_write", "ls_cache_read",
+    "ls_cached_attn_workspace_size", "ls_cached_attn", "ls_vocab_logprob_workspace_size",
+    "ls_vocab_logprob_fwd", "ls_vocab_logprob_bwd",
 ]
 
 LS_DTYPE_F32 = 0
@@ -37,6 +41,8 @@ EXPORTED_SYMBOLS = [
     "ls_replay_fwd_noalloc_scratch_bytes", "ls_prompt_prefill", "ls_prompt_prefill_workspace_size",
     "ls_replay_fwd_part", "ls_replay_bwd_part", "ls_sum_parts",
     "ls_gdn_workspace_size", "ls_gdn_replay_fwd", "ls_gdn_replay_bwd", "ls_stage_pages",
+    "ls_cache_write", "ls_cache_read", "ls_cached_attn_workspace_size", "ls_cached_attn",
+    "ls_vocab_logprob_workspace_size", "ls_vocab_logprob_fwd", "ls_vocab_logprob_bwd",
 ]
 
 
@@ -75,6 +81,32 @@ LS_GDN_BWD_REUSES_FORWARD = 1  # ls_gdn_desc.flags
 class GdnDesc(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("dk", ctypes.c_int32),
                 ("dv", ctypes.c_int32), ("precision", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+LS_CACHE_F32 = 0
+LS_CACHE_BF16 = 1
+LS_CACHE_E4M3 = 2
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("hkv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("pool_pages", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p)]
+
+
+class CachedAttnDesc(ctypes.Structure):
+    _fields_ = [("q_dtype", ctypes.c_int32), ("o_dtype", ctypes.c_int32), ("hq", ctypes.c_int32),
+                ("batch", ctypes.c_int32), ("total_q", ctypes.c_int64), ("max_q", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("max_kv", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("softmax_scale", ctypes.c_float)]
+
+
+class VocabDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("hidden", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("piece", ctypes.c_int32), ("n_rows", ctypes.c_int64), ("h_stride", ctypes.c_int64),
+                ("w_stride", ctypes.c_int64), ("ignore_index", ctypes.c_int64),
+                ("logit_scale", ctypes.c_float)]
 
 
 def library_path() -> Path:
@@ -122,6 +154,15 @@ def lib() -> ctypes.CDLL:
         "ls_gdn_replay_bwd": [ctypes.POINTER(GdnDesc), P, P, P, P, P, P, P, I32, P, P, P, P, P, P,
                               SZ, P],
         "ls_stage_pages": [ctypes.POINTER(AttnDesc), P, P, I64, P, I64, I32, P, P, P, SZ, P],
+        "ls_cache_write": [ctypes.POINTER(KvCache), I32, P, P, I64, I64, P, I64, P, SZ, P],
+        "ls_cache_read": [ctypes.POINTER(KvCache), P, I64, I32, P, P, P, SZ, P],
+        "ls_cached_attn_workspace_size": [ctypes.POINTER(CachedAttnDesc), ctypes.POINTER(KvCache),
+                                          ctypes.POINTER(SZ)],
+        "ls_cached_attn": [ctypes.POINTER(CachedAttnDesc), ctypes.POINTER(KvCache), P, P, P, P, I64,
+                           P, P, P, SZ, P],
+        "ls_vocab_logprob_workspace_size": [ctypes.POINTER(VocabDesc), I32, ctypes.POINTER(SZ)],
+        "ls_vocab_logprob_fwd": [ctypes.POINTER(VocabDesc), P, P, P, P, P, P, SZ, P],
+        "ls_vocab_logprob_bwd": [ctypes.POINTER(VocabDesc), P, P, P, P, P, P, P, P, SZ, P],
         "ls_read_device_status": [P, SZ, P],
         "ls_clear_device_status": [P, SZ, P],
         "ls_trace_enable": [I32],
@@ -386,6 +427,152 @@ def ls_replay_group(desc, prompt, members, ws, stream=None):
                         _ptr(m["dq"]), _ptr(m["dk"]), _ptr(m["dv"]))
     _check(lib().ls_replay_group(ctypes.byref(desc), ctypes.byref(prompt), len(members), arr,
                                  _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def _want(t, dtype, shape, name):
+    """Shape, dtype and contiguity of a tensor the library takes by its address alone."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _token_stride(t, name):
+    """Elements from one token to the next of a [n, heads, d] tensor whose heads are contiguous."""
+    n, heads, d = t.shape
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(0) if n > 1 else heads * d
+
+
+def kv_cache_from(k, v, k_exp=None, v_exp=None) -> KvCache:
+    """A cache over pools [pages, Hkv, S_p, d]: float32, bfloat16, or float8_e4m3fn with
+    int8 exponents [pages, Hkv, S_p].  The cache holds addresses: keep the tensors alive."""
+    import torch
+    fmt = {torch.float32: LS_CACHE_F32, torch.bfloat16: LS_CACHE_BF16,
+           torch.float8_e4m3fn: LS_CACHE_E4M3}.get(k.dtype)
+    if fmt is None or k.dim() != 4:
+        raise TypeError(f"cache pools are 4-D float32, bfloat16 or float8_e4m3fn, got {k.dtype}")
+    _want(k, k.dtype, k.shape, "k")
+    _want(v, k.dtype, k.shape, "v")
+    if fmt == LS_CACHE_E4M3:
+        if k_exp is None or v_exp is None:
+            raise ValueError("an e4m3 cache needs k_exp and v_exp")
+        _want(k_exp, torch.int8, k.shape[:3], "k_exp")
+        _want(v_exp, torch.int8, k.shape[:3], "v_exp")
+    pages, hkv, page, d = k.shape
+    return KvCache(fmt, hkv, d, page, pages, _ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp))
+
+
+def _cache_rows(cache, slots, k, v):
+    import torch
+    _want(slots, torch.int64, (k.shape[0],), "slots")
+    want = (k.shape[0], cache.hkv, cache.head_dim)
+    if tuple(k.shape) != want or tuple(v.shape) != want or v.dtype != k.dtype:
+        raise ValueError(f"k and v must be {want} of one dtype")
+
+
+def ls_cache_write(cache, k, v, slots, ws=None, stream=None):
+    """Token t's rows of k, v [n, Hkv, d] (any token stride) into slot slots[t] (see ls.h)."""
+    _cache_rows(cache, slots, k, v)
+    _check(lib().ls_cache_write(ctypes.byref(cache), _dtype_code(k.dtype), _ptr(k), _ptr(v),
+                                _token_stride(k, "k"), _token_stride(v, "v"), _ptr(slots),
+                                k.shape[0], _ptr(ws), 0 if ws is None else _nbytes(ws),
+                                _stream(stream)))
+
+
+def ls_cache_read(cache, slots, k, v, ws=None, stream=None):
+    """Slot slots[t] into token t of k, v [n, Hkv, d] (see ls.h)."""
+    _cache_rows(cache, slots, k, v)
+    _want(k, k.dtype, k.shape, "k")
+    _want(v, k.dtype, k.shape, "v")
+    _check(lib().ls_cache_read(ctypes.byref(cache), _ptr(slots), k.shape[0], _dtype_code(k.dtype),
+                               _ptr(k), _ptr(v), _ptr(ws), 0 if ws is None else _nbytes(ws),
+                               _stream(stream)))
+
+
+def cached_attn_desc(q, o, batch, max_q, max_kv, causal=True, softmax_scale=None) -> CachedAttnDesc:
+    """Desc of ls_cached_attn for q [total_q, Hq, d] and o of q's dtype or float32."""
+    total, hq, d = q.shape
+    scale = softmax_scale if softmax_scale is not None else d ** -0.5
+    return CachedAttnDesc(_dtype_code(q.dtype), _dtype_code(o.dtype), hq, batch, total, max_q,
+                          1 if causal else 0, max_kv, _token_stride(q, "q"), scale)
+
+
+def ls_cached_attn_workspace_size(desc, cache) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ls_cached_attn_workspace_size(ctypes.byref(desc), ctypes.byref(cache),
+                                               ctypes.byref(out)))
+    return out.value
+
+
+def ls_cached_attn(desc, cache, q, q_start, kv_len, page_table, o, lse, ws, stream=None):
+    """Attention of each sequence's new tokens over its pages (see ls.h)."""
+    import torch
+    shape = (desc.total_q, desc.hq, cache.head_dim)
+    if tuple(q.shape) != shape or _dtype_code(q.dtype) != desc.q_dtype or \
+            _token_stride(q, "q") != desc.q_stride:
+        raise ValueError(f"q is not the {shape} tensor of the desc")
+    _want(o, torch.float32 if desc.o_dtype == LS_DTYPE_F32 else torch.bfloat16, shape, "o")
+    _want(lse, torch.float32, shape[:2], "lse")
+    _want(q_start, torch.int32, (desc.batch + 1,), "q_start")
+    _want(kv_len, torch.int64, (desc.batch,), "kv_len")
+    _want(page_table, torch.int32, (desc.batch, page_table.shape[-1]), "page_table")
+    _check(lib().ls_cached_attn(ctypes.byref(desc), ctypes.byref(cache), _ptr(q), _ptr(q_start),
+                                _ptr(kv_len), _ptr(page_table), page_table.shape[1], _ptr(o),
+                                _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def _rows(t, name):
+    if t.dim() != 2 or (t.numel() and t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def vocab_desc(h, w, logit_scale=1.0, ignore_index=-100, piece=0) -> VocabDesc:
+    """Desc of ls_vocab_logprob_* for h [n, hidden] and w [vocab, hidden] of one dtype."""
+    if h.dtype != w.dtype or h.shape[1] != w.shape[1]:
+        raise ValueError("h and w must share dtype and hidden")
+    return VocabDesc(_dtype_code(h.dtype), h.shape[1], w.shape[0], piece, h.shape[0], _rows(h, "h"),
+                     _rows(w, "w"), ignore_index, logit_scale)
+
+
+def ls_vocab_logprob_workspace_size(desc, with_grad=True) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ls_vocab_logprob_workspace_size(ctypes.byref(desc), 1 if with_grad else 0,
+                                                 ctypes.byref(out)))
+    return out.value
+
+
+def _vocab_check(desc, h, w, targets, *rows):
+    import torch
+    for t, n, stride, name in ((h, desc.n_rows, desc.h_stride, "h"), (w, desc.vocab, desc.w_stride, "w")):
+        if tuple(t.shape) != (n, desc.hidden) or _dtype_code(t.dtype) != desc.dtype or \
+                _rows(t, name) != stride:
+            raise ValueError(f"{name} is not the tensor of the desc")
+    _want(targets, torch.int64, (desc.n_rows,), "targets")
+    for t in rows:
+        _want(t, torch.float32, (desc.n_rows,), "a per-row tensor")
+
+
+def ls_vocab_logprob_fwd(desc, h, w, targets, logp, lse, ws, stream=None):
+    """logp of targets [n] and the rows' lse, without the logits (see ls.h)."""
+    _vocab_check(desc, h, w, targets, logp, lse)
+    _check(lib().ls_vocab_logprob_fwd(ctypes.byref(desc), _ptr(h), _ptr(w), _ptr(targets), _ptr(logp),
+                                      _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def ls_vocab_logprob_bwd(desc, h, w, targets, lse, d_logp, dh, dw, ws, stream=None):
+    """dh, dw (either may be None) from d_logp [n] (see ls.h)."""
+    _vocab_check(desc, h, w, targets, lse, d_logp)
+    for t, like, name in ((dh, h, "dh"), (dw, w, "dw")):
+        if t is not None:
+            _want(t, like.dtype, like.shape, name)
+    _check(lib().ls_vocab_logprob_bwd(ctypes.byref(desc), _ptr(h), _ptr(w), _ptr(targets), _ptr(lse),
+                                      _ptr(d_logp), _ptr(dh), _ptr(dw), _ptr(ws), _nbytes(ws),
+                                      _stream(stream)))
 
 
 def ls_read_device_status(ws, stream=None):

@@ -19,8 +19,8 @@ namespace ls {
 namespace {
 
 thread_local char g_err[512] = "";
+}  // namespace
 
-ls_status fail(ls_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 ls_status fail(ls_status st, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -28,6 +28,8 @@ ls_status fail(ls_status st, const char* fmt, ...) {
   va_end(ap);
   return st;
 }
+
+namespace {
 
 ls_status cuda_fail(cudaError_t e, const char* what) {
   return fail(LS_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
@@ -63,7 +65,10 @@ cudaEvent_t take_event() {
 const char* kKernelNames[kNumKernelIds] = {
     "page_write",  "simt_fwd",   "tc_fwd",     "lse_merge", "bwd_preprocess",
     "simt_bwd_dq", "tc_bwd_dq",  "simt_dkdv",  "tc_dkdv",   "dq_reduce",
-    "gdn_fwd",     "gdn_bwd",    "stage_pages"};
+    "gdn_fwd",     "gdn_bwd",    "stage_pages", "cache_write", "cache_read",
+    "cached_simt", "cached_mma", "cached_join", "vocab_simt", "vocab_reduce"};
+
+}  // namespace
 
 // ------------------------------------------------------------------ devices
 int device_sms() {
@@ -90,6 +95,7 @@ bool force_simt() {
   return v != 0;
 }
 
+namespace {
 bool tc_shape(const ls_attn_desc& d) {
   return d.dtype == LS_DTYPE_BF16 && d.head_dim == 256 && d.page_size % kTcSpanQuantum == 0;
 }
@@ -191,6 +197,7 @@ ls_status check_prompt(const ls_attn_desc* d, const ls_prompt_kv* p) {
   return LS_OK;
 }
 
+}  // namespace
 ls_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
   if (!ws) return fail(LS_ERR_INVALID_ARGUMENT, "workspace is NULL");
   if (!aligned(ws, 256)) return fail(LS_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
@@ -198,6 +205,7 @@ ls_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
     return fail(LS_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, need);
   return LS_OK;
 }
+namespace {
 
 #define LS_CHECK(expr)               \
   do {                               \
@@ -795,6 +803,9 @@ ls_status ls_read_device_status(void* ws, size_t ws_bytes, void* stream) {
   }
   if (word & kStatusBadPage)
     return fail(LS_ERR_DEVICE_BOUNDS, "a page-table entry was outside the pool (status 0x%x)",
+                word);
+  if (word & kStatusBadIndex)
+    return fail(LS_ERR_DEVICE_BOUNDS, "a slot, length or target was out of range (status 0x%x)",
                 word);
   return LS_OK;
 }

@@ -1,0 +1,233 @@
+// The quantised K/V cache: rows written into page slots as e4m3 codes with a
+// power-of-two scale per row and KV head, and read back by slot.
+//
+//   e = min { e >= -126 : max|x| <= 448 * 2^e },  code = rne_e4m3(x * 2^-e),
+//   value = code * 2^e.
+//
+// A power of two costs nothing in precision, because e4m3 keeps its relative
+// precision over 15 binades, and makes both directions exact but for the one
+// rounding of the code: x * 2^-e never rounds in float32 where the code is
+// not zero, and code * 2^e is a bf16 number.  The scale is one byte a row.
+//
+// Both kernels only move bytes: one group of d/8 lanes takes a token's K and
+// V row of one head, eight elements a lane, so that a row is read in 16-byte
+// (bf16) pieces, its maximum needs log2(d/8) shuffles, and no shared memory.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "ls_internal.h"
+
+namespace ls {
+namespace {
+
+constexpr int8_t kNanRow = -128;  // exponent of a row that held an infinity or a NaN
+
+struct Row8 {
+  float x[8];
+};
+
+__device__ __forceinline__ Row8 load8(const float* p) {
+  Row8 r;
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  r.x[0] = a.x, r.x[1] = a.y, r.x[2] = a.z, r.x[3] = a.w;
+  r.x[4] = b.x, r.x[5] = b.y, r.x[6] = b.z, r.x[7] = b.w;
+  return r;
+}
+__device__ __forceinline__ Row8 load8(const __nv_bfloat16* p) {
+  Row8 r;
+  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.x[2 * i] = __uint_as_float(w[i] << 16);
+    r.x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  return r;
+}
+__device__ __forceinline__ void store8(float* p, const Row8& r) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(r.x[0], r.x[1], r.x[2], r.x[3]));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(r.x[4], r.x[5], r.x[6], r.x[7]));
+}
+__device__ __forceinline__ uint32_t bf2(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const Row8& r) {
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(bf2(r.x[0], r.x[1]), bf2(r.x[2], r.x[3]),
+                                                 bf2(r.x[4], r.x[5]), bf2(r.x[6], r.x[7])));
+}
+
+// Exponent of a row from the bits of its largest magnitude.
+__device__ __forceinline__ int row_exp(uint32_t amax) {
+  if (amax >= 0x7f800000u) return kNanRow;
+  if (amax == 0u) return 0;
+  // amax = 1.m * 2^(E-127), 448 = 1.75 * 2^8
+  const int e = (int)(amax >> 23) - ((amax & 0x7fffffu) <= 0x600000u ? 135 : 134);
+  return e < -126 ? -126 : e;
+}
+
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126..127
+
+template <int LANES>
+__device__ __forceinline__ void quant_row(const Row8& r, unsigned mask, bool first, uint8_t* dst,
+                                          int8_t* exp_dst) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(r.x[i]) & 0x7fffffffu);
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
+  const int e = row_exp(m);
+  uint2 code = make_uint2(0u, 0u);
+  if (e != kNanRow) {
+    const float s = pow2(-e);
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c[i] = __nv_cvt_float2_to_fp8x2(make_float2(r.x[2 * i] * s, r.x[2 * i + 1] * s), __NV_SATFINITE,
+                                      __NV_E4M3);
+    code = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  }
+  *reinterpret_cast<uint2*>(dst) = code;
+  if (first) *exp_dst = (int8_t)e;
+}
+
+// One group of D/8 lanes per (token, head): its K row and its V row.
+template <typename T, int FMT, int D>
+__global__ void __launch_bounds__(256) cache_write_kernel(
+    const ls_kv_cache c, const T* __restrict__ k, const T* __restrict__ v, int64_t k_stride,
+    int64_t v_stride, const int64_t* __restrict__ slots, int64_t n_rows, uint32_t* status) {
+  constexpr int LANES = D / 8;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LANES;
+  const int part = threadIdx.x % LANES;
+  const unsigned mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << (lane / LANES * LANES);
+  if (row >= n_rows) return;  // a whole group leaves
+  const int64_t t = row / c.hkv;
+  const int head = (int)(row - t * c.hkv);
+  const int64_t slot = __ldg(slots + t);
+  if (slot < 0) return;
+  const int64_t page = slot / c.page_size;
+  if (page >= c.pool_pages) {
+    if (part == 0 && status) atomicOr(status, kStatusBadIndex);
+    return;
+  }
+  const int64_t dst = (page * c.hkv + head) * c.page_size + (slot - page * c.page_size);
+  const Row8 rk = load8(k + t * k_stride + head * D + part * 8);
+  const Row8 rv = load8(v + t * v_stride + head * D + part * 8);
+  if constexpr (FMT == LS_CACHE_E4M3) {
+    quant_row<LANES>(rk, mask, part == 0, static_cast<uint8_t*>(c.k) + dst * D + part * 8, c.k_exp + dst);
+    quant_row<LANES>(rv, mask, part == 0, static_cast<uint8_t*>(c.v) + dst * D + part * 8, c.v_exp + dst);
+  } else if constexpr (FMT == LS_CACHE_BF16) {
+    store8(static_cast<__nv_bfloat16*>(c.k) + dst * D + part * 8, rk);
+    store8(static_cast<__nv_bfloat16*>(c.v) + dst * D + part * 8, rv);
+  } else {
+    store8(static_cast<float*>(c.k) + dst * D + part * 8, rk);
+    store8(static_cast<float*>(c.v) + dst * D + part * 8, rv);
+  }
+}
+
+__device__ __forceinline__ Row8 load_codes(const uint8_t* p, int e) {
+  Row8 r;
+  const uint2 w = __ldcs(reinterpret_cast<const uint2*>(p));
+  const float s = e == kNanRow ? __int_as_float(0x7fffffff) : pow2(e);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = (i < 2 ? w.x : w.y) >> (16 * (i & 1));
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u & 0xffffu), __NV_E4M3);
+    r.x[2 * i] = __half2float(__half(__half_raw{h.x})) * s;
+    r.x[2 * i + 1] = __half2float(__half(__half_raw{h.y})) * s;
+  }
+  return r;
+}
+
+template <typename T, int FMT, int D>
+__global__ void __launch_bounds__(256) cache_read_kernel(
+    const ls_kv_cache c, T* __restrict__ k, T* __restrict__ v, const int64_t* __restrict__ slots,
+    int64_t n_rows, uint32_t* status) {
+  constexpr int LANES = D / 8;
+  const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LANES;
+  const int part = threadIdx.x % LANES;
+  if (row >= n_rows) return;
+  const int64_t t = row / c.hkv;
+  const int head = (int)(row - t * c.hkv);
+  const int64_t slot = __ldg(slots + t);
+  const int64_t page = slot >= 0 ? slot / c.page_size : 0;
+  Row8 rk, rv;
+  if (slot < 0 || page >= c.pool_pages) {
+    if (slot >= 0 && part == 0 && status) atomicOr(status, kStatusBadIndex);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rk.x[i] = rv.x[i] = 0.f;
+  } else {
+    const int64_t src = (page * c.hkv + head) * c.page_size + (slot - page * c.page_size);
+    if constexpr (FMT == LS_CACHE_E4M3) {
+      rk = load_codes(static_cast<const uint8_t*>(c.k) + src * D + part * 8, __ldg(c.k_exp + src));
+      rv = load_codes(static_cast<const uint8_t*>(c.v) + src * D + part * 8, __ldg(c.v_exp + src));
+    } else if constexpr (FMT == LS_CACHE_BF16) {
+      rk = load8(static_cast<const __nv_bfloat16*>(c.k) + src * D + part * 8);
+      rv = load8(static_cast<const __nv_bfloat16*>(c.v) + src * D + part * 8);
+    } else {
+      rk = load8(static_cast<const float*>(c.k) + src * D + part * 8);
+      rv = load8(static_cast<const float*>(c.v) + src * D + part * 8);
+    }
+  }
+  store8(k + row * D + part * 8, rk);
+  store8(v + row * D + part * 8, rv);
+}
+
+// Calls f with the format and the head dimension as constants.
+template <typename F>
+cudaError_t with_shape(const ls_kv_cache& c, F f) {
+  auto by_d = [&](auto fmt) {
+    switch (c.head_dim) {
+      case 64: return f(fmt, std::integral_constant<int, 64>{});
+      case 128: return f(fmt, std::integral_constant<int, 128>{});
+      default: return f(fmt, std::integral_constant<int, 256>{});
+    }
+  };
+  switch (c.format) {
+    case LS_CACHE_E4M3: return by_d(std::integral_constant<int, LS_CACHE_E4M3>{});
+    case LS_CACHE_BF16: return by_d(std::integral_constant<int, LS_CACHE_BF16>{});
+    default: return by_d(std::integral_constant<int, LS_CACHE_F32>{});
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const ls_kv_cache& c, int src_dtype, const void* k, const void* v,
+                               int64_t k_stride, int64_t v_stride, const int64_t* slots,
+                               int64_t n_tok, uint32_t* status, cudaStream_t s) {
+  const int64_t rows = n_tok * c.hkv;
+  const int64_t blocks = (rows * (c.head_dim / 8) + 255) / 256;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  return with_shape(c, [&](auto fmt, auto d) {
+    LaunchScope ls(kKCacheWrite, s);
+    if (src_dtype == LS_DTYPE_F32)
+      cache_write_kernel<float, fmt.value, d.value><<<(unsigned)blocks, 256, 0, s>>>(
+          c, static_cast<const float*>(k), static_cast<const float*>(v), k_stride, v_stride, slots, rows, status);
+    else
+      cache_write_kernel<__nv_bfloat16, fmt.value, d.value><<<(unsigned)blocks, 256, 0, s>>>(
+          c, static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), k_stride, v_stride, slots,
+          rows, status);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_cache_read(const ls_kv_cache& c, const int64_t* slots, int64_t n_tok,
+                              int dst_dtype, void* k, void* v, uint32_t* status, cudaStream_t s) {
+  const int64_t rows = n_tok * c.hkv;
+  const int64_t blocks = (rows * (c.head_dim / 8) + 255) / 256;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  return with_shape(c, [&](auto fmt, auto d) {
+    LaunchScope ls(kKCacheRead, s);
+    if (dst_dtype == LS_DTYPE_F32)
+      cache_read_kernel<float, fmt.value, d.value><<<(unsigned)blocks, 256, 0, s>>>(
+          c, static_cast<float*>(k), static_cast<float*>(v), slots, rows, status);
+    else
+      cache_read_kernel<__nv_bfloat16, fmt.value, d.value><<<(unsigned)blocks, 256, 0, s>>>(
+          c, static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v), slots, rows, status);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace ls

@@ -14,6 +14,7 @@ namespace ls {
 enum : uint32_t {
   kStatusBadPage = 1u,   // a page-table entry pointed outside the pool
   kStatusTimeout = 2u,   // a bounded device wait gave up
+  kStatusBadIndex = 4u,  // a slot, length or target was out of range
 };
 
 // Bytes at the head of the workspace reserved for the status word.
@@ -41,6 +42,13 @@ enum KernelId : int32_t {
   kKGdnFwd,
   kKGdnBwd,
   kKStagePages,
+  kKCacheWrite,
+  kKCacheRead,
+  kKCachedSimt,
+  kKCachedMma,
+  kKCachedJoin,
+  kKVocabSimt,
+  kKVocabReduce,
   kNumKernelIds
 };
 
@@ -145,6 +153,12 @@ cudaError_t launch_tc_bwd_dq(const BwdParams& p, cudaStream_t s);
 // Sets the message ls_last_error() returns on this thread.
 void set_last_error(const char* msg);
 
+ls_status fail(ls_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+ls_status check_ws(const void* ws, size_t ws_bytes, size_t need);
+int device_sms();
+bool device_is_sm100_family();
+bool force_simt();  // LS_FORCE_SIMT is set
+
 bool encode_pool_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows);
 // 3-D TMA map over a bf16 tensor [rows][heads][256] with [box_rows x 1 x 64]
 // boxes and the 128-byte swizzle (response K/V, Q, dO); rows past the end
@@ -179,5 +193,63 @@ cudaError_t launch_gdn_bwd(int B, int H, int R, const float* s0, const float* q,
                            const float* v, const float* g, const float* beta, const float* d_o,
                            float* dq, float* dk, float* dv, float* dg, float* dbeta, float* ws,
                            cudaStream_t st);
+
+// Quantised cache (ls_cache.cu).
+cudaError_t launch_cache_write(const ls_kv_cache& c, int src_dtype, const void* k, const void* v,
+                               int64_t k_stride, int64_t v_stride, const int64_t* slots,
+                               int64_t n_tok, uint32_t* status, cudaStream_t s);
+cudaError_t launch_cache_read(const ls_kv_cache& c, const int64_t* slots, int64_t n_tok,
+                              int dst_dtype, void* k, void* v, uint32_t* status, cudaStream_t s);
+
+// Cached attention.  The keys of a sequence are cut into parts of `span`
+// keys; part ns-1 takes whatever lies beyond.  Row t of a (sequence, KV head)
+// is token t / gq, head t % gq of the group, so that a tile's rows are
+// neighbours in time.
+struct CachedParams {
+  ls_kv_cache c;
+  int32_t hq, gq, batch, max_q, causal;
+  int32_t q_dtype, o_dtype;
+  int64_t total_q, q_stride, pages_per_seq;
+  float scale, scale_log2;
+  int32_t ns;
+  int64_t span;
+  const void* q;
+  const int32_t* q_start;
+  const int64_t* kv_len;
+  const int32_t* page_table;
+  void* o;           // [total_q][hq][d], o_dtype (ns == 1)
+  float* lse;
+  float* o_parts;    // [ns][total_q * hq][d] (ns > 1)
+  float* lse_parts;  // [ns][total_q * hq]
+  uint32_t* status;
+};
+cudaError_t launch_cached_simt(const CachedParams& p, cudaStream_t s);
+cudaError_t launch_cached_mma(const CachedParams& p, cudaStream_t s);
+// Joins the ns parts (at most kCachedMaxParts) of every row.
+constexpr int kCachedMaxParts = 128;
+cudaError_t launch_cached_join(const CachedParams& p, cudaStream_t s);
+int cached_mma_rows(int d);  // rows of one tile of launch_cached_mma, at most
+
+// Vocabulary log-probabilities (ls_vocab.cu, ls_vocab_tc.cu).
+struct VocabParams {
+  ls_vocab_desc d;
+  const void* h;
+  const void* w;
+  const int64_t* targets;
+  const float* lse_in;
+  const float* d_logp;
+  float* logp;
+  float* lse;
+  void* dh;
+  void* dw;
+  void* scratch;  // after the status header
+  uint32_t* status;
+};
+size_t vocab_simt_scratch(const ls_vocab_desc& d, bool with_grad);
+// lse and logp from n_tiles (maximum, sum) pairs per row, [tile][row], in base 2.
+cudaError_t launch_vocab_join(int n_tiles, const VocabParams& p, const float2* parts, const float* hit,
+                              cudaStream_t s);
+cudaError_t launch_vocab_simt_fwd(const VocabParams& p, cudaStream_t s);
+cudaError_t launch_vocab_simt_bwd(const VocabParams& p, cudaStream_t s);
 
 }  // namespace ls

@@ -1,0 +1,336 @@
+// Vocabulary log-probabilities on the CUDA cores: float32 arithmetic for any
+// dtype, row stride and alignment, and what both routes share (joining the
+// pieces' softmax statistics).
+//
+//   x_nv = s * h_n . w_v,  lse_n = log sum_v exp(x_nv),  logp_n = x_nt - lse_n,
+//   D_nv = s * dlogp_n * ([v = t_n] - exp(x_nv - lse_n)),  dh = D w,  dw = D^T h.
+//
+// The logits are never in memory: the forward's product keeps, per row and
+// tile of the vocabulary, the tile's maximum and its sum of exponentials; the
+// backward forms them again, a piece of the vocabulary at a time, turns them
+// into D in the product's epilogue, and uses D in two products.
+//
+// One tiled product serves all three: TILE x TILE outputs for 256 threads,
+// 16 of the inner dimension at a time through shared memory, 8 x 8 (or, where
+// 128 x 128 tiles would leave SMs idle, 4 x 4) outputs a thread.  It is bound
+// by FMA issue; its rate is near that of a library float32 product.
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include "ls_internal.h"
+
+namespace ls {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kBK = 16;
+
+__device__ __forceinline__ float ldf(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float ldf(const __nv_bfloat16* p) {
+  return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p)) << 16);
+}
+__device__ __forceinline__ void stf(float* p, float v) { *p = v; }
+__device__ __forceinline__ void stf(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// An operand of the product: element (i, k), i the output's index.
+template <typename T>
+struct Operand {
+  const T* p;
+  int64_t si, sk;  // strides of i and k; one of them is 1
+  int64_t n;       // extent of i
+};
+
+// C tile = sum_k A(m, k) B(n, k); epi(m, n, value) for each output of the tile.
+template <int TM, typename TA, typename TB>
+struct Product {
+  static constexpr int TILE = 16 * TM;
+  float a[kBK][TILE + 4], b[kBK][TILE + 4];
+
+  template <typename T>
+  __device__ __forceinline__ static void load(float (&dst)[kBK][TILE + 4], const Operand<T>& o,
+                                              int64_t i0, int64_t k0, int64_t K) {
+#pragma unroll
+    for (int x = threadIdx.x; x < TILE * kBK; x += 256) {
+      // neighbouring threads follow the contiguous index
+      const int i = o.sk == 1 ? x / kBK : x % TILE, k = o.sk == 1 ? x % kBK : x / TILE;
+      dst[k][i] = i0 + i < o.n && k0 + k < K ? ldf(o.p + (i0 + i) * o.si + (k0 + k) * o.sk) : 0.f;
+    }
+  }
+
+  // acc[i][j]: rows (i / 4) * TILE/2 + ty * 4 + i % 4 (TM 8) or ty * 4 + i (TM 4)
+  __device__ __forceinline__ static int at(int t, int i) { return TM == 8 ? (i / 4) * 64 + t * 4 + (i & 3) : t * 4 + i; }
+
+  __device__ __forceinline__ void run(const Operand<TA>& A, const Operand<TB>& B, int64_t m0, int64_t n0,
+                                      int64_t K, float (&acc)[TM][TM]) {
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] = 0.f;
+    for (int64_t k0 = 0; k0 < K; k0 += kBK) {
+      __syncthreads();
+      load(a, A, m0, k0, K);
+      load(b, B, n0, k0, K);
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kBK; ++k) {
+        float x[TM], y[TM];
+#pragma unroll
+        for (int i = 0; i < TM; i += 4) {
+          *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(&a[k][at(ty, i)]);
+          *reinterpret_cast<float4*>(y + i) = *reinterpret_cast<const float4*>(&b[k][at(tx, i)]);
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int j = 0; j < TM; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+      }
+    }
+  }
+};
+
+// Forward: per row of a 16*TM-column tile of the vocabulary, (maximum, sum of
+// 2^(x - maximum)) of the logits in base 2, and the target's logit.
+template <int TM, typename T>
+__global__ void __launch_bounds__(256) vocab_fwd_kernel(const ls_vocab_desc d, const T* h, const T* w,
+                                                        const int64_t* targets, float2* parts, float* hit) {
+  using P = Product<TM, T, T>;
+  __shared__ __align__(16) P sm;
+  const int64_t m0 = (int64_t)blockIdx.x * P::TILE, n0 = (int64_t)blockIdx.y * P::TILE;
+  float acc[TM][TM];
+  sm.run({h, d.h_stride, 1, d.n_rows}, {w, d.w_stride, 1, d.vocab}, m0, n0, d.hidden, acc);
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int64_t row = m0 + P::at(ty, i);
+    const int64_t target = row < d.n_rows ? __ldg(targets + row) : -1;
+    float top = -CUDART_INF_F;
+    float y[TM];
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const int64_t v = n0 + P::at(tx, j);
+      const float x = acc[i][j] * d.logit_scale;
+      if (v == target && v < d.vocab) hit[row] = x;
+      y[j] = v < d.vocab ? x * kLog2e : -CUDART_INF_F;
+      top = fmaxf(top, y[j]);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = top == -CUDART_INF_F ? 0.f : top;
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < TM; ++j) sum += exp2f(y[j] - ref);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (tx == 0 && row < d.n_rows) parts[(int64_t)blockIdx.y * d.n_rows + row] = make_float2(top, sum);
+  }
+}
+
+// lse and logp of 32 rows from their tiles' statistics: lane = row, eight
+// warps share the tiles.
+__global__ void __launch_bounds__(256) vocab_join_kernel(int n_tiles, int64_t n_rows, int64_t vocab,
+                                                         int64_t ignore, const float2* __restrict__ parts,
+                                                         const float* __restrict__ hit,
+                                                         const int64_t* __restrict__ targets,
+                                                         float* __restrict__ logp, float* __restrict__ lse,
+                                                         uint32_t* status) {
+  __shared__ float2 sm[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+  float m = -CUDART_INF_F, l = 0.f;
+  if (row < n_rows)
+    for (int t = warp; t < n_tiles; t += 8) {
+      const float2 a = __ldg(parts + (int64_t)t * n_rows + row);
+      const float mn = fmaxf(m, a.x);
+      const float ref = mn == -CUDART_INF_F ? 0.f : mn;
+      l = l * exp2f(m - ref) + a.y * exp2f(a.x - ref);
+      m = mn;
+    }
+  sm[warp][lane] = make_float2(m, l);
+  __syncthreads();
+  if (warp == 0 && row < n_rows) {
+    for (int i = 1; i < 8; ++i) {
+      const float2 a = sm[i][lane];
+      const float mn = fmaxf(m, a.x);
+      const float ref = mn == -CUDART_INF_F ? 0.f : mn;
+      l = l * exp2f(m - ref) + a.y * exp2f(a.x - ref);
+      m = mn;
+    }
+    const float z = ((m == -CUDART_INF_F ? 0.f : m) + log2f(l)) * kLn2;
+    lse[row] = z;
+    const int64_t target = __ldg(targets + row);
+    const bool in = target >= 0 && target < vocab;
+    if (!in && target != ignore) atomicOr(status, kStatusBadIndex);
+    logp[row] = in ? hit[row] - z : 0.f;
+  }
+}
+
+// D of a piece of the vocabulary: columns v0 .. v0 + np of the logits.
+template <int TM, typename T>
+__global__ void __launch_bounds__(256) vocab_slope_kernel(const ls_vocab_desc d, const T* h, const T* w,
+                                                          const int64_t* targets, const float* lse,
+                                                          const float* d_logp, int64_t v0, int64_t np, float* out) {
+  using P = Product<TM, T, T>;
+  __shared__ __align__(16) P sm;
+  const int64_t m0 = (int64_t)blockIdx.x * P::TILE, n0 = (int64_t)blockIdx.y * P::TILE;
+  float acc[TM][TM];
+  sm.run({h, d.h_stride, 1, d.n_rows}, {w + v0 * d.w_stride, d.w_stride, 1, np}, m0, n0, d.hidden, acc);
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int64_t row = m0 + P::at(ty, i);
+    if (row >= d.n_rows) continue;
+    const int64_t target = __ldg(targets + row);
+    const float c = target >= 0 && target < d.vocab ? __ldg(d_logp + row) * d.logit_scale : 0.f;
+    const float z = __ldg(lse + row);
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const int64_t n = n0 + P::at(tx, j);
+      if (n >= np) continue;
+      const float p = exp2f((acc[i][j] * d.logit_scale - z) * kLog2e);
+      // a row that takes no part has no gradient even where its logits are not finite
+      out[row * np + n] = c == 0.f ? 0.f : c * ((v0 + n == target ? 1.f : 0.f) - p);
+    }
+  }
+}
+
+// out[m][n] (row stride n) = A B^T (+ add), rounded to TO once.
+template <int TM, typename TA, typename TB, typename TO>
+__global__ void __launch_bounds__(256) vocab_product_kernel(Operand<TA> A, Operand<TB> B, int64_t K,
+                                                            const float* add, TO* out) {
+  using P = Product<TM, TA, TB>;
+  __shared__ __align__(16) P sm;
+  const int64_t m0 = (int64_t)blockIdx.x * P::TILE, n0 = (int64_t)blockIdx.y * P::TILE;
+  float acc[TM][TM];
+  sm.run(A, B, m0, n0, K, acc);
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int64_t m = m0 + P::at(ty, i);
+    if (m >= A.n) continue;
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const int64_t n = n0 + P::at(tx, j);
+      if (n >= B.n) continue;
+      float v = acc[i][j];
+      if (add) v += add[m * B.n + n];
+      stf(out + m * B.n + n, v);
+    }
+  }
+}
+
+size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Columns of a piece on the CUDA cores: D of a piece within 256 MB.
+int64_t simt_piece(const ls_vocab_desc& d) {
+  int64_t np = d.piece > 0 ? d.piece : (64ll << 20) / (d.n_rows > 0 ? d.n_rows : 1) / 128 * 128;
+  if (np < 128 && d.piece == 0) np = 128;
+  return np < d.vocab ? np : d.vocab;
+}
+
+// Smaller tiles where 128 x 128 ones would not give every SM a CTA.
+bool small_tiles(int64_t m, int64_t n) {
+  return ((m + 127) / 128) * ((n + 127) / 128) < device_sms();
+}
+template <typename F>
+cudaError_t with_tile(int64_t m, int64_t n, F f) {
+  const bool small = small_tiles(m, n);
+  const int64_t tile = small ? 64 : 128;
+  const dim3 grid((unsigned)((m + tile - 1) / tile), (unsigned)((n + tile - 1) / tile));
+  if ((n + tile - 1) / tile > 65535) return cudaErrorInvalidConfiguration;
+  if (small)
+    f(std::integral_constant<int, 4>{}, grid);
+  else
+    f(std::integral_constant<int, 8>{}, grid);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t simt_fwd(const VocabParams& p, cudaStream_t s) {
+  const ls_vocab_desc& d = p.d;
+  float2* parts = static_cast<float2*>(p.scratch);
+  const int64_t tiles64 = (d.vocab + 63) / 64;
+  float* hit = reinterpret_cast<float*>(parts + tiles64 * d.n_rows);
+  int n_tiles = 0;
+  {
+    LaunchScope ls(kKVocabSimt, s);
+    const cudaError_t e = with_tile(d.n_rows, d.vocab, [&](auto tm, dim3 grid) {
+      n_tiles = (int)grid.y;
+      vocab_fwd_kernel<tm.value, T><<<grid, 256, 0, s>>>(d, static_cast<const T*>(p.h), static_cast<const T*>(p.w), p.targets, parts, hit);
+    });
+    if (e != cudaSuccess) return e;
+  }
+  return launch_vocab_join(n_tiles, p, parts, hit, s);
+}
+
+template <typename T>
+cudaError_t simt_bwd(const VocabParams& p, cudaStream_t s) {
+  const ls_vocab_desc& d = p.d;
+  const T* h = static_cast<const T*>(p.h);
+  const T* w = static_cast<const T*>(p.w);
+  const int64_t piece = simt_piece(d);
+  float* slope = static_cast<float*>(p.scratch);
+  float* dh32 = slope + round_up((size_t)d.n_rows * piece, 64);
+  for (int64_t v0 = 0; v0 < d.vocab; v0 += piece) {
+    const int64_t np = d.vocab - v0 < piece ? d.vocab - v0 : piece;
+    LaunchScope ls(kKVocabSimt, s);
+    cudaError_t e = with_tile(d.n_rows, np, [&](auto tm, dim3 grid) {
+      vocab_slope_kernel<tm.value, T><<<grid, 256, 0, s>>>(d, h, w, p.targets, p.lse_in, p.d_logp, v0, np, slope);
+    });
+    if (e != cudaSuccess) return e;
+    if (p.dh) {
+      const Operand<float> A{slope, np, 1, d.n_rows};
+      const Operand<T> B{w + v0 * d.w_stride, 1, d.w_stride, d.hidden};
+      const float* add = v0 > 0 ? dh32 : nullptr;
+      e = with_tile(d.n_rows, d.hidden, [&](auto tm, dim3 grid) {
+        ls.more_kernels(1);
+        if (v0 + np == d.vocab)
+          vocab_product_kernel<tm.value, float, T, T><<<grid, 256, 0, s>>>(A, B, np, add, static_cast<T*>(p.dh));
+        else
+          vocab_product_kernel<tm.value, float, T, float><<<grid, 256, 0, s>>>(A, B, np, add, dh32);
+      });
+      if (e != cudaSuccess) return e;
+    }
+    if (p.dw) {
+      const Operand<float> A{slope, 1, np, np};
+      const Operand<T> B{h, 1, d.h_stride, d.hidden};
+      e = with_tile(np, d.hidden, [&](auto tm, dim3 grid) {
+        ls.more_kernels(1);
+        vocab_product_kernel<tm.value, float, T, T><<<grid, 256, 0, s>>>(A, B, d.n_rows, nullptr, static_cast<T*>(p.dw) + v0 * d.hidden);
+      });
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_vocab_join(int n_tiles, const VocabParams& p, const float2* parts, const float* hit,
+                              cudaStream_t s) {
+  LaunchScope ls(kKVocabReduce, s);
+  vocab_join_kernel<<<(unsigned)((p.d.n_rows + 31) / 32), 256, 0, s>>>(
+      n_tiles, p.d.n_rows, p.d.vocab, p.d.ignore_index, parts, hit, p.targets, p.logp, p.lse, p.status);
+  return cudaGetLastError();
+}
+
+size_t vocab_simt_scratch(const ls_vocab_desc& d, bool with_grad) {
+  const size_t n = (size_t)d.n_rows;
+  size_t need = (size_t)((d.vocab + 63) / 64) * n * sizeof(float2) + n * sizeof(float);
+  if (with_grad) {
+    const size_t g = (round_up(n * (size_t)simt_piece(d), 64) +
+                      (simt_piece(d) < d.vocab ? n * (size_t)d.hidden : 0)) * sizeof(float);
+    need = g > need ? g : need;
+  }
+  return round_up(need, 256);
+}
+
+cudaError_t launch_vocab_simt_fwd(const VocabParams& p, cudaStream_t s) {
+  return p.d.dtype == LS_DTYPE_F32 ? simt_fwd<float>(p, s) : simt_fwd<__nv_bfloat16>(p, s);
+}
+cudaError_t launch_vocab_simt_bwd(const VocabParams& p, cudaStream_t s) {
+  return p.d.dtype == LS_DTYPE_F32 ? simt_bwd<float>(p, s) : simt_bwd<__nv_bfloat16>(p, s);
+}
+
+}  // namespace ls
