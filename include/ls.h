@@ -482,7 +482,11 @@ LS_API ls_status ls_cached_attn(const ls_cached_attn_desc* desc, const ls_kv_cac
  * still written); any other target outside [0, vocab) is treated the same and
  * reported through the status word.  An ignored row's h and d_logp reach no
  * other row's results, but dw multiplies its h by 0: it has to be finite there.
- * Arithmetic is float32; dh and dw are rounded to dtype once.
+ * Sums are float32; dh and dw are rounded to dtype once.  bf16 with hidden,
+ * strides and addresses in multiples of 16 bytes runs on the tensor cores,
+ * where the backward also rounds the logits' gradient to bf16, once, as the
+ * operand of its two products; float32 and other layouts run on the CUDA
+ * cores.
  *   piece: vocabulary columns whose gradient is held at a time in the backward
  *     (0: chosen from n_rows); the workspace grows with it. */
 typedef struct {

@@ -66,7 +66,7 @@ const char* kKernelNames[kNumKernelIds] = {
     "page_write",  "simt_fwd",   "tc_fwd",     "lse_merge", "bwd_preprocess",
     "simt_bwd_dq", "tc_bwd_dq",  "simt_dkdv",  "tc_dkdv",   "dq_reduce",
     "gdn_fwd",     "gdn_bwd",    "stage_pages", "cache_write", "cache_read",
-    "cached_simt", "cached_mma", "cached_join", "vocab_simt", "vocab_reduce"};
+    "cached_simt", "cached_mma", "cached_join", "vocab_simt", "vocab_tc", "vocab_reduce"};
 
 }  // namespace
 
@@ -415,6 +415,19 @@ EncodeTiledFn encoder() {
   return enc;
 }
 }  // namespace
+
+bool encode_matrix_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t stride,
+                       int box_rows, int blocks) {
+  EncodeTiledFn enc = encoder();
+  if (!enc) return false;
+  cuuint64_t gdim[3] = {(cuuint64_t)(blocks == 1 ? cols : 64), (cuuint64_t)rows, (cuuint64_t)(cols / 64)};
+  cuuint64_t gstr[2] = {(cuuint64_t)stride * 2u, 64u * 2u};
+  cuuint32_t box[3] = {64u, (cuuint32_t)box_rows, (cuuint32_t)blocks};
+  cuuint32_t es[3] = {1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, blocks == 1 ? 2 : 3, const_cast<void*>(base), gdim, gstr,
+             box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 bool encode_pool_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows) {
   EncodeTiledFn enc = encoder();

@@ -48,6 +48,7 @@ enum KernelId : int32_t {
   kKCachedMma,
   kKCachedJoin,
   kKVocabSimt,
+  kKVocabTc,
   kKVocabReduce,
   kNumKernelIds
 };
@@ -168,6 +169,12 @@ bool encode_rows_map(CUtensorMap* m, const void* base, int heads, int64_t rows, 
 // swizzled [box_rows x 64] column boxes (pool rows; token-major rows).
 bool encode_pool_tile_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows,
                           int box_blocks = 4);
+// A bf16 matrix [rows][cols] of any row stride (16-byte multiple): blocks == 1
+// gives a 2-D map with boxes of 64 columns x box_rows (any cols, zeros past the
+// end), blocks > 1 a 3-D one (64, rows, cols / 64) whose box lands `blocks`
+// column boxes one after the other (cols a multiple of 64).
+bool encode_matrix_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t stride,
+                       int box_rows, int blocks);
 bool encode_rows_tile_map(CUtensorMap* m, const void* base, int heads, int64_t rows, int box_rows,
                           int box_blocks = 4);
 cudaError_t launch_tc_dkdv(const BwdParams& p, cudaStream_t s);
@@ -251,5 +258,9 @@ cudaError_t launch_vocab_join(int n_tiles, const VocabParams& p, const float2* p
                               cudaStream_t s);
 cudaError_t launch_vocab_simt_fwd(const VocabParams& p, cudaStream_t s);
 cudaError_t launch_vocab_simt_bwd(const VocabParams& p, cudaStream_t s);
+// bf16; hidden, the row strides and the addresses multiples of 16 bytes.
+size_t vocab_tc_scratch(const ls_vocab_desc& d, bool with_grad);
+cudaError_t launch_vocab_tc_fwd(const VocabParams& p, cudaStream_t s);
+cudaError_t launch_vocab_tc_bwd(const VocabParams& p, cudaStream_t s);
 
 }  // namespace ls

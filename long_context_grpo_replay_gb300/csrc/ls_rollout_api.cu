@@ -1,7 +1,7 @@
 // Host side of the rollout and scoring entry points: the quantised cache,
 // cached attention and vocabulary log-probabilities.  Validation, planning
-// and dispatch; the kernels are in ls_cache.cu, ls_cached_attn.cu and
-// ls_vocab.cu.
+// and dispatch; the kernels are in ls_cache.cu, ls_cached_attn.cu,
+// ls_vocab.cu and ls_vocab_tc.cu.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -143,8 +143,21 @@ ls_status check_vocab(const ls_vocab_desc* d) {
   return LS_OK;
 }
 
+// The tensor-core route by the desc alone, so that the workspace's size does
+// not depend on addresses; a call whose addresses do not suit it takes the
+// CUDA-core route in the same workspace.
+bool vocab_tc_shape(const ls_vocab_desc& d) {
+  return d.dtype == LS_DTYPE_BF16 && d.hidden % 8 == 0 && d.h_stride % 8 == 0 &&
+         d.w_stride % 8 == 0 && !force_simt() && device_is_sm100_family();
+}
+
 size_t vocab_need(const ls_vocab_desc& d, bool with_grad) {
-  return kWsHeader + vocab_simt_scratch(d, with_grad);
+  size_t need = vocab_simt_scratch(d, with_grad);
+  if (vocab_tc_shape(d)) {
+    const size_t t = vocab_tc_scratch(d, with_grad);
+    need = t > need ? t : need;
+  }
+  return kWsHeader + need;
 }
 
 }  // namespace
@@ -288,7 +301,10 @@ ls_status ls_vocab_logprob_fwd(const ls_vocab_desc* desc, const void* h, const v
   p.lse = lse;
   p.scratch = static_cast<char*>(ws) + kWsHeader;
   p.status = static_cast<uint32_t*>(ws);
-  LS_CUDA(launch_vocab_simt_fwd(p, s), "vocabulary forward launch");
+  if (vocab_tc_shape(*desc) && aligned(h, 16) && aligned(w, 16))
+    LS_CUDA(launch_vocab_tc_fwd(p, s), "vocabulary forward launch");
+  else
+    LS_CUDA(launch_vocab_simt_fwd(p, s), "vocabulary forward launch");
   return LS_OK;
 }
 
@@ -322,7 +338,10 @@ ls_status ls_vocab_logprob_bwd(const ls_vocab_desc* desc, const void* h, const v
   p.dw = dw;
   p.scratch = static_cast<char*>(ws) + kWsHeader;
   p.status = static_cast<uint32_t*>(ws);
-  LS_CUDA(launch_vocab_simt_bwd(p, s), "vocabulary backward launch");
+  if (vocab_tc_shape(*desc) && aligned(h, 16) && aligned(w, 16))
+    LS_CUDA(launch_vocab_tc_bwd(p, s), "vocabulary backward launch");
+  else
+    LS_CUDA(launch_vocab_simt_bwd(p, s), "vocabulary backward launch");
   return LS_OK;
 }
 
