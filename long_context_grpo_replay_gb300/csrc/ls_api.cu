@@ -66,7 +66,7 @@ const char* kKernelNames[kNumKernelIds] = {
     "page_write",  "simt_fwd",   "tc_fwd",     "lse_merge", "bwd_preprocess",
     "simt_bwd_dq", "tc_bwd_dq",  "simt_dkdv",  "tc_dkdv",   "dq_reduce",
     "gdn_fwd",     "gdn_bwd",    "stage_pages", "cache_write", "cache_read",
-    "cached_simt", "cached_mma", "cached_join", "vocab_simt", "vocab_tc", "vocab_reduce"};
+    "cached_simt", "cached_mma", "cached_tc", "cached_join", "vocab_simt", "vocab_tc", "vocab_reduce"};
 
 }  // namespace
 

@@ -1,0 +1,660 @@
+// Tensor-core (tcgen05) attention of a chunk of new tokens over a paged cache,
+// bf16 or e4m3, head dim 64, 128 or 256.
+//
+// A CTA has 128 query rows of one (sequence, KV head) -- tokens x the group's
+// heads -- and one part of the keys, 128 keys at a time: S = Q K^T into one of
+// two tensor-memory buffers, the softmax of a row by two threads, P back into
+// S's columns as the tensor-memory operand of O += P V.  With 24/4 heads and
+// d = 256, 128 rows do 256 flop for a cached e4m3 byte, about the device's
+// ratio, so one tile serves both ends: many tokens are bound by the products,
+// few (a group's members over their shared prompt) by the memory stream.
+//
+// K and V tiles are [128 keys x 128 columns] chunks of a ring of four or five
+// slots in shared memory, in the order of use K0 K1 V0 K2 V1 ...  Four warps fill them:
+// bf16 rows by asynchronous copies, e4m3 rows through registers, as f16 (exact:
+// e4m3 is a subset), two chunks loaded ahead.  Rows are found per key, so any
+// page size works; a missing key's row is zeros.
+//
+// e4m3 scales stay out of the products: y = x 2^ek + ev (base 2) is the score
+// and the exponent of the value row, w = 2^(y - m) the weight that multiplies
+// codes, l = sum w 2^-ev, o = sum w code / l.  Weights are f16, held 2^11 times
+// their value and at most 2^15: 11 bits down to 2^-25 of the largest, so a sum
+// of many small weights beside a large one is not lost.  bf16: P in bf16, as in
+// the replay kernels.  Each row's maximum only moves when exceeded by 2^4
+// (e4m3) or 2^8 (bf16), so that O is rarely rescaled.
+//
+// Warp roles (512 threads): 0 finds the keys' rows, scales and presence;
+// 1 issues the products; 2 owns tensor memory; 4-7 fill chunks; 8-15 softmax.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math_constants.h>
+
+#include "ls_cached.cuh"
+#include "ls_internal.h"
+#include "ls_tc.cuh"
+
+namespace ls {
+namespace {
+using namespace tc;
+
+constexpr int kBM = 128, kBN = 128, kThreads = 512;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kBar = 8;   // barriers per ring (more than chunks), and tiles of key tables
+constexpr int kAhead = 2; // tiles whose tables are found at a time
+
+template <int D>
+struct TcShape {
+  static constexpr int CW = D < 128 ? D : 128;         // columns of a chunk
+  static constexpr int NCH = D / CW;                   // chunks of a K or V tile
+  static constexpr int NC = D == 256 ? 4 : 5;          // chunks of the ring
+  static constexpr uint32_t kBox = kBN * 128;          // [128 keys x 64 columns] of 16-bit values
+  static constexpr uint32_t kChunk = kBN * CW * 2;
+  static constexpr uint32_t kQ = kBM * D * 2;
+  static constexpr uint32_t kSmem = kQ + NC * kChunk + 1024;
+  static_assert(kSmem + 20480 <= 227 * 1024, "shared memory, with 20 KB of tables");
+  static_assert(NC < kBar, "a chunk's barriers are free before its slot is");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Two pairs of e4m3 codes as two f16 pairs.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Position of K_j / V_j in the order of use, and what stands at position u.
+__device__ __forceinline__ int unit_of_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int unit_of_v(int j, int n) { return j < n - 1 ? 2 * j + 2 : 2 * n - 1; }
+__device__ __forceinline__ void unit_at(int u, int n, int& j, bool& is_v) {
+  if (u == 0) {
+    j = 0, is_v = false;
+  } else if (u & 1) {
+    j = (u + 1) / 2;
+    is_v = j >= n;
+    if (is_v) j = n - 1;
+  } else {
+    j = (u - 2) / 2, is_v = true;
+  }
+}
+
+template <int D, bool E4>
+__global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedParams p) {
+  using L = TcShape<D>;
+  constexpr float kOff = E4 ? 11.f : 0.f;
+  constexpr float kSlack = E4 ? 4.f : 8.f;
+  // registers: 128 a thread at launch, 65,536 in all; 40 + 104 + 2 x 168 per
+  // group of 128 threads make 61,440
+  constexpr int kRegsControl = 40, kRegsFill = 104, kRegsSoftmax = 168;
+  static_assert(128 * (kRegsControl + kRegsFill + 2 * kRegsSoftmax) <= 65536, "register split");
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t bar_q, bar_full[kBar], bar_done[kBar], bar_rows[kBar], bar_tile[kBar], bar_s[2], bar_p[2], bar_o,
+      bar_last, bar_pair[4], bar_drain;
+  __shared__ uint32_t tmem_base_s, abort_s;
+  __shared__ int row_s[kBar][kBN];
+  __shared__ __align__(16) float kf_s[E4 ? kBar : 1][kBN], ev_s[E4 ? kBar : 1][kBN], vi_s[E4 ? kBar : 1][kBN];
+  __shared__ uint32_t there_s[kBar][4];
+  __shared__ float top_s[2][2][kBM], back_s[kBM];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u, sRing = sQ + L::kQ;
+  const int b = blockIdx.z, kvh = blockIdx.y;
+  const int part = blockIdx.x % p.ns, tile = blockIdx.x / p.ns;
+  const Seq s = load_seq(p, b, tid == 0 && kvh == 0 && blockIdx.x == 0);
+  const int nrows = s.n * p.gq, r0 = tile * kBM;
+  if (r0 >= nrows) return;
+  const int r1 = r0 + kBM < nrows ? r0 + kBM : nrows;
+  int kb, ke;
+  part_range(p, s, part, (r1 - 1) / p.gq, kb, ke);
+  const int ntiles = ke > kb ? (ke - kb + kBN - 1) / kBN : 0;
+  const int nchunks = 2 * ntiles * L::NCH;
+
+  if (tid == 0) {
+    abort_s = 0;
+    mbar_init(smem_u32(&bar_q), 8);
+    for (int i = 0; i < kBar; ++i) {
+      mbar_init(smem_u32(&bar_full[i]), 4);
+      mbar_init(smem_u32(&bar_done[i]), 1);
+      mbar_init(smem_u32(&bar_rows[i]), 1);
+      mbar_init(smem_u32(&bar_tile[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bar_s[i]), 1);
+      mbar_init(smem_u32(&bar_p[i]), 8);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bar_pair[i]), 64);
+    mbar_init(smem_u32(&bar_o), 1);
+    mbar_init(smem_u32(&bar_last), 1);
+    mbar_init(smem_u32(&bar_drain), 1);
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(&tmem_base_s), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = tmem_base_s;
+  const uint32_t tS = tbase + 256;
+  const volatile uint32_t* abortp = &abort_s;
+  auto fail = [&](int line) {
+    atomicOr(p.status, kStatusTimeout);
+    atomicCAS(p.status + 1, 0u, ((uint32_t)kKCachedTc << 16) | (uint32_t)line);
+    abort_s = 1;
+  };
+
+  if (warp < 4) {
+    fewer_registers<kRegsControl>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- key tables
+      // kAhead tiles at a time, so that their page ids, then their scales, are
+      // in flight together
+      bool ok = true;
+      for (int j0 = 0; ok && j0 < ntiles; j0 += kAhead) {
+        int row[kAhead][4];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int key = kb + (j0 + a) * kBN + x * 32 + lane;
+            row[a][x] = key < ke ? pool_row(p, b, kvh, key) : -1;
+          }
+        int ek[kAhead][4], ev[kAhead][4];
+        if constexpr (E4) {
+#pragma unroll
+          for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              ek[a][x] = row[a][x] >= 0 ? __ldg(p.c.k_exp + row[a][x]) : 0;
+              ev[a][x] = row[a][x] >= 0 ? __ldg(p.c.v_exp + row[a][x]) : 0;
+            }
+        }
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          const int j = j0 + a, sl = j % kBar;
+          if (!ok || j >= ntiles) break;
+          // the tables of tile j - kBar are used up once its O is done
+          if (j >= kBar && !mbar_wait_warp(smem_u32(&bar_tile[sl]), (j / kBar - 1) & 1, abortp)) {
+            if (lane == 0) fail(__LINE__);
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            row_s[sl][x * 32 + lane] = row[a][x];
+            const uint32_t m = __ballot_sync(0xffffffffu, row[a][x] >= 0);
+            if (lane == 0) there_s[sl][x] = m;
+            if constexpr (E4) {
+              kf_s[sl][x * 32 + lane] = exp_scale(ek[a][x]);
+              // a NaN row reaches only the rows that see it: through the exponent
+              const bool nan = ev[a][x] == -128;
+              ev_s[sl][x * 32 + lane] = nan ? exp_scale(-128) : (float)ev[a][x];
+              vi_s[sl][x * 32 + lane] = nan ? 1.f : exp_scale(-ev[a][x]);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bar_rows[sl]));
+        }
+      }
+    } else if (warp == 1 && lane == 0 && ntiles > 0) {
+      // ---------------------------------------------------------- products
+      constexpr uint32_t kF16 = (1u << 7) | (1u << 10);  // the operands' type bits: bf16, cleared for f16
+      constexpr uint32_t idesc_s = idesc_bf16(kBM, kBN, false) & ~(E4 ? kF16 : 0u);
+      constexpr uint32_t idesc_o = idesc_bf16(kBM, L::CW, true) & ~(E4 ? kF16 : 0u);
+      auto wait_full = [&](int c) { return mbar_wait(smem_u32(&bar_full[c % kBar]), (c / kBar) & 1, abortp); };
+      auto issue_s = [&](int j) -> bool {
+        const uint32_t dS = tS + (j & 1) * kBN;
+#pragma unroll
+        for (int h = 0; h < L::NCH; ++h) {
+          const int c = unit_of_k(j) * L::NCH + h;
+          if (!wait_full(c)) {
+            fail(__LINE__);
+            return false;
+          }
+          tc_fence_after();
+          const uint32_t kc = sRing + (c % L::NC) * L::kChunk;
+#pragma unroll
+          for (int kk = 0; kk < L::CW / 16; ++kk)
+            mma_ss(dS, sdesc_sw128(sQ + (h * 2 + (kk >> 2)) * (kBM * 128) + (kk & 3) * 32, 16, 1024),
+                   sdesc_sw128(kc + (kk >> 2) * L::kBox + (kk & 3) * 32, 16, 1024), idesc_s, (h > 0 || kk > 0) ? 1u : 0u);
+          if (h == L::NCH - 1) mma_commit(smem_u32(&bar_s[j & 1]));
+          mma_commit(smem_u32(&bar_done[c % kBar]));
+        }
+        return true;
+      };
+      bool ok = mbar_wait(smem_u32(&bar_q), 0, abortp);
+      if (!ok) fail(__LINE__);
+      tc_fence_after();
+      if (ok) ok = issue_s(0);
+      for (int j = 0; ok && j < ntiles; ++j) {
+        // the other S buffer held P_{j-1}, read by the products issued before
+        if (j + 1 < ntiles && !issue_s(j + 1)) break;
+        if (!mbar_wait(smem_u32(&bar_p[j & 1]), (j >> 1) & 1, abortp)) {
+          fail(__LINE__);
+          break;
+        }
+#pragma unroll
+        for (int h = 0; h < L::NCH; ++h) {
+          const int c = unit_of_v(j, ntiles) * L::NCH + h;
+          if (!wait_full(c)) {
+            fail(__LINE__);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t vc = sRing + (c % L::NC) * L::kChunk;
+#pragma unroll
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            mma_ts(tbase + h * L::CW, tS + (j & 1) * kBN + kk * 8, sdesc_sw128(vc + kk * 2048, L::kBox, 1024), idesc_o,
+                   (j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(smem_u32(&bar_done[c % kBar]));
+        }
+        if (!ok) break;
+        mma_commit(smem_u32(&bar_tile[j % kBar]));
+        mma_commit(smem_u32(&bar_o));
+        if (j == ntiles - 1) mma_commit(smem_u32(&bar_last));
+      }
+      mma_commit(smem_u32(&bar_drain));
+      mbar_wait(smem_u32(&bar_drain), 0, abortp);
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ chunks
+    fewer_registers<kRegsFill>();
+    const int w = tid - 128;
+    bool ok = true;
+    auto where = [&](int c, int& j, const char*& pool, int& h) {
+      bool is_v;
+      unit_at(c / L::NCH, ntiles, j, is_v);
+      pool = static_cast<const char*>(is_v ? p.c.v : p.c.k);
+      h = c % L::NCH;
+    };
+    auto rows_ready = [&](int j) -> bool {
+      if (mbar_wait_warp(smem_u32(&bar_rows[j % kBar]), (j / kBar) & 1, abortp)) return true;
+      if (lane == 0) fail(__LINE__);
+      return false;
+    };
+    auto slot_free = [&](int c) -> bool {
+      if (c < L::NC || mbar_wait_warp(smem_u32(&bar_done[(c - L::NC) % kBar]), ((c - L::NC) / kBar) & 1, abortp)) return true;
+      if (lane == 0) fail(__LINE__);
+      return false;
+    };
+    auto filled = [&](int c) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bar_full[c % kBar]));
+    };
+    if constexpr (E4) {
+      // a thread's pieces: 16 codes of column piece pc in rows tid / PR + i * RS
+      constexpr int PR = L::CW / 16, RS = 128 / PR, NP = kBN / RS;
+      const int pc = w % PR, rr = w / PR;
+      uint4 buf[2][NP];
+      auto load = [&](int c, uint4 (&v)[NP]) -> bool {
+        int j, h;
+        const char* pool;
+        where(c, j, pool, h);
+        if (!rows_ready(j)) return false;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const int row = row_s[j % kBar][rr + i * RS];
+          v[i] = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool + (int64_t)row * D + h * L::CW + pc * 16))
+                          : make_uint4(0u, 0u, 0u, 0u);
+        }
+        return true;
+      };
+      auto store = [&](int c, const uint4 (&v)[NP]) -> bool {
+        if (!slot_free(c)) return false;
+        // pieces 4-7 write their halves in the other order: the eight threads
+        // of a row then cover all banks with each store
+        const uint32_t dst = sRing + (c % L::NC) * L::kChunk + (pc >> 2) * L::kBox;
+        const int flip = pc >> 2;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          uint4 x, y;
+          codes_f16(v[i].x, x.x, x.y);
+          codes_f16(v[i].y, x.z, x.w);
+          codes_f16(v[i].z, y.x, y.y);
+          codes_f16(v[i].w, y.z, y.w);
+          const int r = rr + i * RS, at = (pc & 3) * 2;
+          st_shared_v4(dst + sw128_offset(r, at + flip), flip ? y : x);
+          st_shared_v4(dst + sw128_offset(r, at + 1 - flip), flip ? x : y);
+        }
+        filled(c);
+        return true;
+      };
+      if (nchunks > 0) ok = load(0, buf[0]);
+      if (ok && nchunks > 1) ok = load(1, buf[1]);
+      for (int c = 0; ok && c < nchunks; c += 2) {
+        ok = store(c, buf[0]);
+        if (ok && c + 2 < nchunks) ok = load(c + 2, buf[0]);
+        if (ok && c + 1 < nchunks) ok = store(c + 1, buf[1]);
+        if (ok && c + 3 < nchunks) ok = load(c + 3, buf[1]);
+      }
+    } else {
+      constexpr int PR = L::CW / 8, RS = 128 / PR, NP = kBN / RS;
+      const int pc = w % PR, rr = w / PR;
+      int c = 0;
+      for (; ok && c < nchunks; ++c) {
+        int j, h;
+        const char* pool;
+        where(c, j, pool, h);
+        ok = rows_ready(j) && slot_free(c);
+        if (!ok) break;
+        const uint32_t dst = sRing + (c % L::NC) * L::kChunk + (pc >> 3) * L::kBox;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const int r = rr + i * RS, row = row_s[j % kBar][r];
+          copy16(dst + sw128_offset(r, pc & 7), pool + ((int64_t)(row < 0 ? 0 : row) * D + h * L::CW + pc * 8) * 2, row >= 0);
+        }
+        copy_commit();
+        if (c >= 2) {
+          copy_wait<2>();
+          filled(c - 2);
+        }
+      }
+      copy_wait<0>();
+      if (ok)
+        for (int x = nchunks < 2 ? 0 : nchunks - 2; x < nchunks; ++x) filled(x);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    more_registers<kRegsSoftmax>();
+    const int sw = warp - 8, q4 = sw & 3, hf = sw >> 2;
+    const int i = q4 * 32 + lane;
+    const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+    // queries: a warp takes 16 rows, eight columns a lane
+    for (int x = 0; x < 16; ++x) {
+      const int r = sw * 16 + x, t = r0 + r;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (t < r1 && lane < D / 8) {
+        const int tok = t / p.gq, hh = t - tok * p.gq;
+        v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(s.q0 + tok) * p.q_stride +
+                                                 (int64_t)(kvh * p.gq + hh) * D) + lane);
+      }
+      if constexpr (E4) {
+        // f16 with the row's power of two taken out: its largest element in [1, 4)
+        uint32_t e[4] = {v.x, v.y, v.z, v.w}, top = 0;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) top = max(top, max((e[y] << 16) & 0x7fffffffu, e[y] & 0x7fff0000u));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        int f = 254 - (int)(top >> 23);
+        f = f < 1 ? 1 : f > 253 ? 253 : f;
+        const float to = __int_as_float(f << 23);
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          e[y] = pack_f16x2(__uint_as_float(e[y] << 16) * to, __uint_as_float(e[y] & 0xffff0000u) * to);
+        v = make_uint4(e[0], e[1], e[2], e[3]);
+        if (lane == 0) back_s[r] = __int_as_float((254 - f) << 23) * p.scale_log2;
+      }
+      if (lane < D / 8) st_shared_v4(sQ + (lane >> 3) * (kBM * 128) + sw128_offset(r, lane & 7), v);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bar_q));
+
+    bool ok = mbar_wait_warp(smem_u32(&bar_q), 0, abortp);  // back_s of rows that other warps wrote
+    if (!ok && lane == 0) fail(__LINE__);
+    const bool row_ok = r0 + i < r1;
+    const int tok = row_ok ? (r0 + i) / p.gq : 0, hh = row_ok ? r0 + i - tok * p.gq : 0;
+    // a row past the end has zero queries; seeing every key keeps its warp on the short path
+    const int lim = row_ok ? row_limit(p, s, tok) : INT32_MAX;
+    const float crow = E4 ? back_s[i] : p.scale_log2;
+    float m_run = -CUDART_INF_F, l_run = 0.f;
+    for (int j = 0; ok && j < ntiles; ++j) {
+      const int bf = j & 1, sl = j % kBar, key0 = kb + j * kBN + hf * 64;
+      if (!mbar_wait_warp(smem_u32(&bar_rows[sl]), (j / kBar) & 1, abortp) ||
+          !mbar_wait_warp(smem_u32(&bar_s[bf]), (j >> 1) & 1, abortp)) {
+        if (lane == 0) fail(__LINE__);
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint64_t y[32];  // scores of this half's 64 keys, two by two
+      {
+        uint32_t a0[32], a1[32];
+        const uint32_t sa = tS + lanes + bf * kBN + hf * 64;
+        tmem_ld32(sa, a0);
+        tmem_ld32(sa + 32, a1);
+        tmem_wait_ld_r(a0);
+        reg_dep(a1);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          y[c] = f2(__uint_as_float(a0[2 * c]), __uint_as_float(a0[2 * c + 1]));
+          y[16 + c] = f2(__uint_as_float(a1[2 * c]), __uint_as_float(a1[2 * c + 1]));
+        }
+      }
+      if constexpr (E4) {
+        const uint64_t c2 = f2(crow, crow);
+        const ulonglong2* kf = reinterpret_cast<const ulonglong2*>(&kf_s[sl][hf * 64]);
+        const ulonglong2* ev = reinterpret_cast<const ulonglong2*>(&ev_s[sl][hf * 64]);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const ulonglong2 f = kf[c], e = ev[c];
+          y[2 * c] = f2_fma(f2_mul(y[2 * c], f.x), c2, e.x);
+          y[2 * c + 1] = f2_fma(f2_mul(y[2 * c + 1], f.y), c2, e.y);
+        }
+      }
+      // keys that exist and that this row sees
+      const int nv = lim - key0;
+      uint64_t see = (uint64_t)there_s[sl][hf * 2] | (uint64_t)there_s[sl][hf * 2 + 1] << 32;
+      if (nv < 64) see &= nv > 0 ? ~0ull >> (64 - nv) : 0ull;
+      float mq[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+      if (!__all_sync(0xffffffffu, see == ~0ull)) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          float a, bb;
+          f2_split(y[c], a, bb);
+          y[c] = f2(see >> (2 * c) & 1 ? a : -CUDART_INF_F, see >> (2 * c + 1) & 1 ? bb : -CUDART_INF_F);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        float a, bb;
+        f2_split(y[c], a, bb);
+        mq[c & 3] = fmaxf(mq[c & 3], fmaxf(a, bb));
+      }
+      float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+      // both halves of a row meet: they exchange their maxima, and each has
+      // read its half of S before P overwrites it
+      top_s[bf][hf][i] = mx;
+      tc_fence_before();
+      mbar_arrive(smem_u32(&bar_pair[q4]));
+      if (!mbar_wait_warp(smem_u32(&bar_pair[q4]), j & 1, abortp)) {
+        if (lane == 0) fail(__LINE__);
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      mx = fmaxf(mx, top_s[bf][hf ^ 1][i]);
+      if constexpr (!E4) mx *= crow;
+      float alpha = 1.f;
+      bool rescale = false;
+      if (mx > m_run + kSlack) {
+        if (m_run != -CUDART_INF_F) {
+          alpha = ex2(m_run - mx);
+          rescale = true;
+        }
+        l_run *= alpha;
+        m_run = mx;
+      }
+      if (__any_sync(0xffffffffu, rescale)) {
+        // S_j done means PV_{j-2} done, so bar_o has completed j-1 or j phases
+        if (!mbar_wait_warp(smem_u32(&bar_o), (j - 1) & 1, abortp)) {
+          if (lane == 0) fail(__LINE__);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll 1
+        for (int c0 = hf * (D / 2); c0 < (hf + 1) * (D / 2); c0 += 32) {
+          uint32_t rr[32];
+          tmem_ld32(tbase + lanes + c0, rr);
+          tmem_wait_ld_r(rr);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) rr[c] = __float_as_uint(__uint_as_float(rr[c]) * alpha);
+          tmem_st32(tbase + lanes + c0, rr);
+        }
+        tmem_wait_st();
+      }
+      // a row that has seen no key keeps its reference at 0: -infinity gives a
+      // weight of 0, and a NaN stays one
+      const float ref = (m_run == -CUDART_INF_F ? 0.f : m_run) - kOff;
+      const uint64_t nref = f2(-ref, -ref), sc2 = f2(crow, crow);
+      uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+      const ulonglong2* vi = reinterpret_cast<const ulonglong2*>(&vi_s[E4 ? sl : 0][hf * 64]);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int x = half * 16 + 2 * c;
+          float e[4];
+          if constexpr (E4) {
+            f2_split(f2_add(y[x], nref), e[0], e[1]);
+            f2_split(f2_add(y[x + 1], nref), e[2], e[3]);
+          } else {
+            f2_split(f2_fma(y[x], sc2, nref), e[0], e[1]);
+            f2_split(f2_fma(y[x + 1], sc2, nref), e[2], e[3]);
+          }
+#pragma unroll
+          for (int z = 0; z < 4; ++z) e[z] = ex2(e[z]);
+          if constexpr (E4) {
+            const ulonglong2 f = vi[half * 8 + c];
+            acc[0] = f2_fma(f2(e[0], e[1]), f.x, acc[0]);
+            acc[1] = f2_fma(f2(e[2], e[3]), f.y, acc[1]);
+            pk[2 * c] = pack_f16x2(e[0], e[1]);
+            pk[2 * c + 1] = pack_f16x2(e[2], e[3]);
+          } else {
+            acc[0] = f2_add(acc[0], f2(e[0], e[1]));
+            acc[1] = f2_add(acc[1], f2(e[2], e[3]));
+            pk[2 * c] = pack_bf16x2(e[0], e[1]);
+            pk[2 * c + 1] = pack_bf16x2(e[2], e[3]);
+          }
+        }
+        tmem_st16(tS + lanes + bf * kBN + hf * 32 + half * 16, pk);
+      }
+      float p0, p1, p2, p3;
+      f2_split(acc[0], p0, p1);
+      f2_split(acc[1], p2, p3);
+      l_run += (p0 + p1) + (p2 + p3);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bar_p[bf]));
+    }
+    // ---- the row sums of both halves, then this half of O's columns
+    float l = 0.f;
+    if (ok && ntiles > 0) {
+      if (!mbar_wait_warp(smem_u32(&bar_last), 0, abortp)) {
+        if (lane == 0) fail(__LINE__);
+        ok = false;
+      }
+      tc_fence_after();
+      if (ok) {
+        top_s[ntiles & 1][hf][i] = l_run;
+        mbar_arrive(smem_u32(&bar_pair[q4]));
+        if (!mbar_wait_warp(smem_u32(&bar_pair[q4]), ntiles & 1, abortp)) {
+          if (lane == 0) fail(__LINE__);
+          ok = false;
+        }
+      }
+      if (ok) l = top_s[ntiles & 1][0][i] + top_s[ntiles & 1][1][i];
+    }
+    const int64_t out = (int64_t)(s.q0 + tok) * p.hq + kvh * p.gq + hh;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+    for (int c0 = hf * (D / 2); c0 < (hf + 1) * (D / 2); c0 += 32) {
+      uint32_t rr[32];
+      __syncwarp();
+      if (ok && ntiles > 0) {
+        tmem_ld32(tbase + lanes + c0, rr);
+        tmem_wait_ld_r(rr);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) rr[c] = 0u;
+      }
+      if (!row_ok) continue;
+      // a row without keys: its O was never weighted, and 0 times it is 0
+      float v[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) v[c] = l == 0.f ? 0.f : __uint_as_float(rr[c]) * inv;
+      if (p.ns > 1 || p.o_dtype == LS_DTYPE_F32) {
+        float* dst = (p.ns > 1 ? p.o_parts + (int64_t)part * p.total_q * p.hq * D : static_cast<float*>(p.o)) + out * D + c0;
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+      } else {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + out * D + c0;
+#pragma unroll
+        for (int c = 0; c < 32; c += 8)
+          *reinterpret_cast<uint4*>(dst + c) = make_uint4(pack_bf16x2(v[c], v[c + 1]), pack_bf16x2(v[c + 2], v[c + 3]),
+                                                          pack_bf16x2(v[c + 4], v[c + 5]), pack_bf16x2(v[c + 6], v[c + 7]));
+      }
+    }
+    if (row_ok && hf == 0) {
+      const float z = l == 0.f ? -CUDART_INF_F : ((m_run == -CUDART_INF_F ? 0.f : m_run) - kOff + __log2f(l)) * kLn2;
+      if (p.ns > 1)
+        p.lse_parts[(int64_t)part * p.total_q * p.hq + out] = z;
+      else
+        p.lse[out] = z;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+template <int D, bool E4>
+cudaError_t run_tc(const CachedParams& p, cudaStream_t s) {
+  using L = TcShape<D>;
+  auto* kernel = cached_tc_kernel<D, E4>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ((int64_t)p.max_q * p.gq + kBM - 1) / kBM;
+  if (tiles * p.ns > INT32_MAX) return cudaErrorInvalidConfiguration;
+  LaunchScope ls(kKCachedTc, s);
+  kernel<<<dim3((unsigned)(tiles * p.ns), p.c.hkv, p.batch), kThreads, L::kSmem, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cached_tc(const CachedParams& p, cudaStream_t s) {
+  const bool e4 = p.c.format == LS_CACHE_E4M3;
+  switch (p.c.head_dim) {
+    case 64: return e4 ? run_tc<64, true>(p, s) : run_tc<64, false>(p, s);
+    case 128: return e4 ? run_tc<128, true>(p, s) : run_tc<128, false>(p, s);
+    default: return e4 ? run_tc<256, true>(p, s) : run_tc<256, false>(p, s);
+  }
+}
+
+}  // namespace ls

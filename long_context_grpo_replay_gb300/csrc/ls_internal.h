@@ -46,6 +46,7 @@ enum KernelId : int32_t {
   kKCacheRead,
   kKCachedSimt,
   kKCachedMma,
+  kKCachedTc,
   kKCachedJoin,
   kKVocabSimt,
   kKVocabTc,
@@ -232,6 +233,7 @@ struct CachedParams {
 };
 cudaError_t launch_cached_simt(const CachedParams& p, cudaStream_t s);
 cudaError_t launch_cached_mma(const CachedParams& p, cudaStream_t s);
+cudaError_t launch_cached_tc(const CachedParams& p, cudaStream_t s);  // tiles of 128 rows
 // Joins the ns parts (at most kCachedMaxParts) of every row.
 constexpr int kCachedMaxParts = 128;
 cudaError_t launch_cached_join(const CachedParams& p, cudaStream_t s);

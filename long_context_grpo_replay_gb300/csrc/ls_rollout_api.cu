@@ -1,7 +1,7 @@
 // Host side of the rollout and scoring entry points: the quantised cache,
 // cached attention and vocabulary log-probabilities.  Validation, planning
 // and dispatch; the kernels are in ls_cache.cu, ls_cached_attn.cu,
-// ls_vocab.cu and ls_vocab_tc.cu.
+// ls_cached_tc.cu, ls_vocab.cu and ls_vocab_tc.cu.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -58,7 +58,7 @@ ls_status status_word(void* ws, size_t ws_bytes, uint32_t** status) {
 }
 
 // ------------------------------------------------------------ cached attention
-enum Route { kRouteSimt, kRouteMma };
+enum Route { kRouteSimt, kRouteMma, kRouteTc };
 
 struct CachedPlan {
   Route route;
@@ -93,30 +93,47 @@ ls_status check_cached(const ls_cached_attn_desc* d, const ls_kv_cache* c) {
 
 CachedPlan plan_cached(const ls_cached_attn_desc& d, const ls_kv_cache& c) {
   CachedPlan pl{};
-  const int gq = d.hq / c.hkv;
+  const int gq = d.hq / c.hkv, sms = device_sms();
   const int64_t rows = (int64_t)d.max_q * gq;
+  const double key_bytes = 2.0 * c.head_dim * (c.format == LS_CACHE_F32 ? 4 : c.format == LS_CACHE_BF16 ? 2 : 1);
+  // A CTA's tile of rows, the keys that parts are counted in, and about how
+  // long a CTA takes for them and for its start and end (microseconds).
   int64_t tile, quantum;
+  double per_quantum, fixed;
   if (d.q_dtype != LS_DTYPE_BF16 || c.format == LS_CACHE_F32 || force_simt()) {
     pl.route = kRouteSimt;
-    tile = 16;
-    quantum = 32;
-  } else {
+    tile = 16, quantum = 32;
+    per_quantum = 1.5, fixed = 2.0;
+  } else if (rows <= cached_mma_rows(c.head_dim) || !device_is_sm100_family()) {
     pl.route = kRouteMma;
-    tile = rows < cached_mma_rows(c.head_dim) ? rows : cached_mma_rows(c.head_dim);
+    tile = rows < 8 ? 8 : rows < cached_mma_rows(c.head_dim) ? rows : cached_mma_rows(c.head_dim);
     quantum = 128;
+    per_quantum = quantum * key_bytes / 44e3, fixed = 4.0;
+  } else {
+    pl.route = kRouteTc;
+    tile = 128, quantum = 128;
+    per_quantum = 1.3 * c.head_dim / 256.0 + 0.2, fixed = 5.0;
   }
-  const int64_t units = (int64_t)d.batch * c.hkv * ((rows + tile - 1) / (tile > 0 ? tile : 1));
+  const int64_t units = (int64_t)d.batch * c.hkv * ((rows + tile - 1) / tile);
   const int64_t quanta = d.max_kv > 0 ? (d.max_kv + quantum - 1) / quantum : 1;
-  // One sequence: parts for one CTA on each SM.  Several sequences end at
-  // different lengths, and several smaller rounds even them out.
-  const int64_t want = (int64_t)device_sms() * (d.batch > 1 ? 4 : 1);
-  int64_t ns = units > 0 ? want / units : 1;
-  if (ns > quanta) ns = quanta;
-  if (ns > kCachedMaxParts) ns = kCachedMaxParts;
-  if (ns < 1) ns = 1;
-  pl.span = (quanta + ns - 1) / ns * quantum;
-  pl.ns = (int32_t)((quanta * quantum + pl.span - 1) / pl.span);
   const size_t out_rows = (size_t)d.total_q * d.hq;
+  // Rounds of CTAs (one to an SM) against the parts' float32 results, written
+  // and read once.  Several sequences end at different lengths: the model
+  // takes them for half as long as the longest on average, and asks for a few
+  // rounds, which even them out.
+  int64_t best = 1;
+  double best_cost = 1e300;
+  for (int64_t ns = 1; ns <= kCachedMaxParts && ns <= quanta && units > 0; ++ns) {
+    const int64_t span = (quanta + ns - 1) / ns;
+    if ((quanta + span - 1) / span != ns) continue;
+    double rounds = (double)((units * ns + sms - 1) / sms);
+    if (d.batch > 1) rounds = 0.5 * (double)(units * ns) / sms + 1.0;
+    const double cost = rounds * (span * per_quantum + fixed) +
+                        (ns > 1 ? 3.0 + ns * (double)out_rows * c.head_dim * 8.0 / 6.0e6 : 0.0);
+    if (cost < best_cost * 0.99) best_cost = cost, best = ns;
+  }
+  pl.span = (quanta + best - 1) / best * quantum;
+  pl.ns = (int32_t)((quanta * quantum + pl.span - 1) / pl.span);
   pl.o_bytes = pl.ns > 1 ? round_up((size_t)pl.ns * out_rows * c.head_dim * sizeof(float), 256) : 0;
   pl.ws_bytes = kWsHeader + pl.o_bytes +
                 (pl.ns > 1 ? round_up((size_t)pl.ns * out_rows * sizeof(float), 256) : 0);
@@ -264,8 +281,10 @@ ls_status ls_cached_attn(const ls_cached_attn_desc* desc, const ls_kv_cache* cac
   p.status = static_cast<uint32_t*>(ws);
   if (pl.route == kRouteSimt)
     LS_CUDA(launch_cached_simt(p, s), "cached attention launch");
-  else
+  else if (pl.route == kRouteMma)
     LS_CUDA(launch_cached_mma(p, s), "cached attention launch");
+  else
+    LS_CUDA(launch_cached_tc(p, s), "cached attention launch");
   if (pl.ns > 1)
     LS_CUDA(launch_cached_join(p, s), "part join launch");
   return LS_OK;
