@@ -50,7 +50,8 @@ __device__ __forceinline__ int row_limit(const CachedParams& p, const Seq& s, in
 // The pool row of key j of sequence b, or -1 where the page id lies outside
 // the pool (such a page holds no keys).
 __device__ __forceinline__ int pool_row(const CachedParams& p, int b, int kvh, int j) {
-  const int page = (int)((unsigned)j / (unsigned)p.c.page_size);
+  // j / page_size
+  const int page = p.page_mul ? (int)(__umulhi((unsigned)j, p.page_mul) >> p.page_shift) : j;
   const int slot = __ldg(p.page_table + (int64_t)b * p.pages_per_seq + page);
   if (slot < 0 || slot >= p.c.pool_pages) {
     atomicOr(p.status, kStatusBadPage);

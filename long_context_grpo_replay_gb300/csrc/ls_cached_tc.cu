@@ -10,9 +10,9 @@
 // few (a group's members over their shared prompt) by the memory stream.
 //
 // K and V tiles are [128 keys x 128 columns] chunks of a ring of four or five
-// slots in shared memory, in the order of use K0 K1 V0 K2 V1 ...  Four warps fill them:
-// bf16 rows by asynchronous copies, e4m3 rows through registers, as f16 (exact:
-// e4m3 is a subset), two chunks loaded ahead.  Rows are found per key, so any
+// slots in shared memory, in the order of use K0 K1 V0 K2 V1 ...  Two groups of four
+// warps fill them in turn: bf16 rows by asynchronous copies, e4m3 rows through
+// registers, as f16 (exact: e4m3 is a subset).  Rows are found per key, so any
 // page size works; a missing key's row is zeros.
 //
 // e4m3 scales stay out of the products: y = x 2^ek + ev (base 2) is the score
@@ -23,8 +23,12 @@
 // the replay kernels.  Each row's maximum only moves when exceeded by 2^4
 // (e4m3) or 2^8 (bf16), so that O is rarely rescaled.
 //
-// Warp roles (512 threads): 0 finds the keys' rows, scales and presence;
-// 1 issues the products; 2 owns tensor memory; 4-7 fill chunks; 8-15 softmax.
+// Warp roles (640 threads): 0 and 2 find the keys' rows, scales and presence;
+// 1 issues the products; 2 also owns tensor memory; 4-11 fill chunks, 12-19
+// softmax.  The roles' loops are kept short (one copy of each, waits of six
+// instructions): together they have to stay in the instruction cache.  With
+// unrolled loops and inlined timers a tile of e4m3 keys took 11,500 cycles,
+// most of them the issuing thread's misses (61 % hits).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -38,10 +42,9 @@ namespace ls {
 namespace {
 using namespace tc;
 
-constexpr int kBM = 128, kBN = 128, kThreads = 512;
+constexpr int kBM = 128, kBN = 128, kThreads = 640;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kBar = 8;   // barriers per ring (more than chunks), and tiles of key tables
-constexpr int kAhead = 2; // tiles whose tables are found at a time
+constexpr int kBar = 8;  // barriers per ring (more than chunks), and tiles of key tables
 
 template <int D>
 struct TcShape {
@@ -71,6 +74,12 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi
       "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(w));
+}
+// 16 bytes that are read once: past L1.
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
 }
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -109,14 +118,14 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
   using L = TcShape<D>;
   constexpr float kOff = E4 ? 11.f : 0.f;
   constexpr float kSlack = E4 ? 4.f : 8.f;
-  // registers: 128 a thread at launch, 65,536 in all; 40 + 104 + 2 x 168 per
-  // group of 128 threads make 61,440
-  constexpr int kRegsControl = 40, kRegsFill = 104, kRegsSoftmax = 168;
-  static_assert(128 * (kRegsControl + kRegsFill + 2 * kRegsSoftmax) <= 65536, "register split");
+  // registers: 96 a thread at launch, 61,440 in all; 56 + 2 x 64 + 2 x 144 per
+  // group of 128 threads make 60,416, and no role spills
+  constexpr int kRegsControl = 56, kRegsFill = 64, kRegsSoftmax = 144;
+  static_assert(128 * (kRegsControl + 2 * kRegsFill + 2 * kRegsSoftmax) <= kThreads * 96, "register split");
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bar_q, bar_full[kBar], bar_done[kBar], bar_rows[kBar], bar_tile[kBar], bar_s[2], bar_p[2], bar_o,
       bar_last, bar_pair[4], bar_drain;
-  __shared__ uint32_t tmem_base_s, abort_s;
+  __shared__ uint32_t tmem_base_s;
   __shared__ int row_s[kBar][kBN];
   __shared__ __align__(16) float kf_s[E4 ? kBar : 1][kBN], ev_s[E4 ? kBar : 1][kBN], vi_s[E4 ? kBar : 1][kBN];
   __shared__ uint32_t there_s[kBar][4];
@@ -136,7 +145,6 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
   const int nchunks = 2 * ntiles * L::NCH;
 
   if (tid == 0) {
-    abort_s = 0;
     mbar_init(smem_u32(&bar_q), 8);
     for (int i = 0; i < kBar; ++i) {
       mbar_init(smem_u32(&bar_full[i]), 4);
@@ -163,177 +171,140 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
   tc_fence_after();
   const uint32_t tbase = tmem_base_s;
   const uint32_t tS = tbase + 256;
-  const volatile uint32_t* abortp = &abort_s;
-  auto fail = [&](int line) {
-    atomicOr(p.status, kStatusTimeout);
-    atomicCAS(p.status + 1, 0u, ((uint32_t)kKCachedTc << 16) | (uint32_t)line);
-    abort_s = 1;
+  // where a role's wait gave up; it then leaves, and the others' waits end likewise
+  int gave_up = 0;
+  auto wait = [&](uint64_t& bar, int parity, int line) -> bool {  // whole warps
+    if (mbar_wait_short_warp(smem_u32(&bar), parity)) return true;
+    gave_up = line;
+    return false;
   };
 
   if (warp < 4) {
     fewer_registers<kRegsControl>();
-    if (warp == 0) {
+    if (warp == 0 || warp == 2) {
       // ---------------------------------------------------------- key tables
-      // kAhead tiles at a time, so that their page ids, then their scales, are
-      // in flight together
-      bool ok = true;
-      for (int j0 = 0; ok && j0 < ntiles; j0 += kAhead) {
-        int row[kAhead][4];
+      // two warps, every other tile each: a tile takes two loads that depend
+      // on one another (page id, scales), about as long as its products
+      for (int j = warp >> 1; j < ntiles; j += 2) {
+        const int sl = j % kBar;
+        int row[4], ek[4], ev[4];
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int key = kb + (j0 + a) * kBN + x * 32 + lane;
-            row[a][x] = key < ke ? pool_row(p, b, kvh, key) : -1;
-          }
-        int ek[kAhead][4], ev[kAhead][4];
+        for (int x = 0; x < 4; ++x) {
+          const int key = kb + j * kBN + x * 32 + lane;
+          row[x] = key < ke ? pool_row(p, b, kvh, key) : -1;
+        }
         if constexpr (E4) {
 #pragma unroll
-          for (int a = 0; a < kAhead; ++a)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              ek[a][x] = row[a][x] >= 0 ? __ldg(p.c.k_exp + row[a][x]) : 0;
-              ev[a][x] = row[a][x] >= 0 ? __ldg(p.c.v_exp + row[a][x]) : 0;
-            }
-        }
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-          const int j = j0 + a, sl = j % kBar;
-          if (!ok || j >= ntiles) break;
-          // the tables of tile j - kBar are used up once its O is done
-          if (j >= kBar && !mbar_wait_warp(smem_u32(&bar_tile[sl]), (j / kBar - 1) & 1, abortp)) {
-            if (lane == 0) fail(__LINE__);
-            ok = false;
-            break;
-          }
-#pragma unroll
           for (int x = 0; x < 4; ++x) {
-            row_s[sl][x * 32 + lane] = row[a][x];
-            const uint32_t m = __ballot_sync(0xffffffffu, row[a][x] >= 0);
-            if (lane == 0) there_s[sl][x] = m;
-            if constexpr (E4) {
-              kf_s[sl][x * 32 + lane] = exp_scale(ek[a][x]);
-              // a NaN row reaches only the rows that see it: through the exponent
-              const bool nan = ev[a][x] == -128;
-              ev_s[sl][x * 32 + lane] = nan ? exp_scale(-128) : (float)ev[a][x];
-              vi_s[sl][x * 32 + lane] = nan ? 1.f : exp_scale(-ev[a][x]);
-            }
+            ek[x] = row[x] >= 0 ? __ldg(p.c.k_exp + row[x]) : 0;
+            ev[x] = row[x] >= 0 ? __ldg(p.c.v_exp + row[x]) : 0;
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bar_rows[sl]));
         }
+        // the tables of tile j - kBar are used up once its O is done
+        if (j >= kBar && !wait(bar_tile[sl], (j / kBar - 1) & 1, __LINE__)) break;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          row_s[sl][x * 32 + lane] = row[x];
+          const uint32_t m = __ballot_sync(0xffffffffu, row[x] >= 0);
+          if (lane == 0) there_s[sl][x] = m;
+          if constexpr (E4) {
+            kf_s[sl][x * 32 + lane] = exp_scale(ek[x]);
+            // a NaN row reaches only the rows that see it: through the exponent
+            const bool nan = ev[x] == -128;
+            ev_s[sl][x * 32 + lane] = nan ? exp_scale(-128) : (float)ev[x];
+            vi_s[sl][x * 32 + lane] = nan ? 1.f : exp_scale(-ev[x]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_rows[sl]));
       }
     } else if (warp == 1 && lane == 0 && ntiles > 0) {
       // ---------------------------------------------------------- products
       constexpr uint32_t kF16 = (1u << 7) | (1u << 10);  // the operands' type bits: bf16, cleared for f16
       constexpr uint32_t idesc_s = idesc_bf16(kBM, kBN, false) & ~(E4 ? kF16 : 0u);
       constexpr uint32_t idesc_o = idesc_bf16(kBM, L::CW, true) & ~(E4 ? kF16 : 0u);
-      auto wait_full = [&](int c) { return mbar_wait(smem_u32(&bar_full[c % kBar]), (c / kBar) & 1, abortp); };
-      auto issue_s = [&](int j) -> bool {
-        const uint32_t dS = tS + (j & 1) * kBN;
+      // descriptors count in 16 bytes: a tile's differ by constants
+      const uint64_t qd = sdesc_sw128(sQ, 16, 1024);
+      bool ok = mbar_wait_short(smem_u32(&bar_q), 0);
+      for (int j = -1; ok && j < ntiles; ++j) {
+        // S_{j+1} goes to the buffer that held P_{j-1}, read by products issued before
+        if (j + 1 < ntiles) {
+#pragma unroll 1
+          for (int h = 0; h < L::NCH; ++h) {
+            const int c = unit_of_k(j + 1) * L::NCH + h;
+            ok = mbar_wait_short(smem_u32(&bar_full[c % kBar]), (c / kBar) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t kd = sdesc_sw128(sRing + (c % L::NC) * L::kChunk, 16, 1024);
+            const uint64_t qh = qd + (h * 2 * (kBM * 128) >> 4);
 #pragma unroll
-        for (int h = 0; h < L::NCH; ++h) {
-          const int c = unit_of_k(j) * L::NCH + h;
-          if (!wait_full(c)) {
-            fail(__LINE__);
-            return false;
+            for (int kk = 0; kk < L::CW / 16; ++kk)
+              mma_ss(tS + ((j + 1) & 1) * kBN, qh + (((kk >> 2) * (kBM * 128) + (kk & 3) * 32) >> 4),
+                     kd + (((kk >> 2) * L::kBox + (kk & 3) * 32) >> 4), idesc_s, (h > 0 || kk > 0) ? 1u : 0u);
+            if (h == L::NCH - 1) mma_commit(smem_u32(&bar_s[(j + 1) & 1]));
+            mma_commit(smem_u32(&bar_done[c % kBar]));
           }
-          tc_fence_after();
-          const uint32_t kc = sRing + (c % L::NC) * L::kChunk;
-#pragma unroll
-          for (int kk = 0; kk < L::CW / 16; ++kk)
-            mma_ss(dS, sdesc_sw128(sQ + (h * 2 + (kk >> 2)) * (kBM * 128) + (kk & 3) * 32, 16, 1024),
-                   sdesc_sw128(kc + (kk >> 2) * L::kBox + (kk & 3) * 32, 16, 1024), idesc_s, (h > 0 || kk > 0) ? 1u : 0u);
-          if (h == L::NCH - 1) mma_commit(smem_u32(&bar_s[j & 1]));
-          mma_commit(smem_u32(&bar_done[c % kBar]));
         }
-        return true;
-      };
-      bool ok = mbar_wait(smem_u32(&bar_q), 0, abortp);
-      if (!ok) fail(__LINE__);
-      tc_fence_after();
-      if (ok) ok = issue_s(0);
-      for (int j = 0; ok && j < ntiles; ++j) {
-        // the other S buffer held P_{j-1}, read by the products issued before
-        if (j + 1 < ntiles && !issue_s(j + 1)) break;
-        if (!mbar_wait(smem_u32(&bar_p[j & 1]), (j >> 1) & 1, abortp)) {
-          fail(__LINE__);
-          break;
-        }
-#pragma unroll
-        for (int h = 0; h < L::NCH; ++h) {
+        if (!ok) gave_up = __LINE__;
+        if (j < 0 || !ok) continue;
+        ok = mbar_wait_short(smem_u32(&bar_p[j & 1]), (j >> 1) & 1);
+#pragma unroll 1
+        for (int h = 0; ok && h < L::NCH; ++h) {
           const int c = unit_of_v(j, ntiles) * L::NCH + h;
-          if (!wait_full(c)) {
-            fail(__LINE__);
-            ok = false;
-            break;
-          }
+          ok = mbar_wait_short(smem_u32(&bar_full[c % kBar]), (c / kBar) & 1);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t vc = sRing + (c % L::NC) * L::kChunk;
+          const uint64_t vd = sdesc_sw128(sRing + (c % L::NC) * L::kChunk, L::kBox, 1024);
 #pragma unroll
           for (int kk = 0; kk < kBN / 16; ++kk)
-            mma_ts(tbase + h * L::CW, tS + (j & 1) * kBN + kk * 8, sdesc_sw128(vc + kk * 2048, L::kBox, 1024), idesc_o,
-                   (j > 0 || kk > 0) ? 1u : 0u);
+            mma_ts(tbase + h * L::CW, tS + (j & 1) * kBN + kk * 8, vd + (kk * 2048 >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
           mma_commit(smem_u32(&bar_done[c % kBar]));
         }
-        if (!ok) break;
+        if (!ok) {
+          gave_up = __LINE__;
+          break;
+        }
         mma_commit(smem_u32(&bar_tile[j % kBar]));
         mma_commit(smem_u32(&bar_o));
         if (j == ntiles - 1) mma_commit(smem_u32(&bar_last));
       }
       mma_commit(smem_u32(&bar_drain));
-      mbar_wait(smem_u32(&bar_drain), 0, abortp);
+      mbar_wait_short(smem_u32(&bar_drain), 0);
     }
-  } else if (warp < 8) {
+  } else if (warp < 12) {
     // ------------------------------------------------------------ chunks
+    // four warps take the even chunks, four the odd ones
     fewer_registers<kRegsFill>();
-    const int w = tid - 128;
-    bool ok = true;
-    auto where = [&](int c, int& j, const char*& pool, int& h) {
-      bool is_v;
-      unit_at(c / L::NCH, ntiles, j, is_v);
-      pool = static_cast<const char*>(is_v ? p.c.v : p.c.k);
-      h = c % L::NCH;
-    };
-    auto rows_ready = [&](int j) -> bool {
-      if (mbar_wait_warp(smem_u32(&bar_rows[j % kBar]), (j / kBar) & 1, abortp)) return true;
-      if (lane == 0) fail(__LINE__);
-      return false;
-    };
-    auto slot_free = [&](int c) -> bool {
-      if (c < L::NC || mbar_wait_warp(smem_u32(&bar_done[(c - L::NC) % kBar]), ((c - L::NC) / kBar) & 1, abortp)) return true;
-      if (lane == 0) fail(__LINE__);
-      return false;
-    };
+    const int w = tid & 127, group = (warp - 4) >> 2;
+    const int sh = E4 ? 4 : 3;                                     // a thread's piece: 16 codes or 8 bf16 columns
+    constexpr int PR = L::CW / (E4 ? 16 : 8), RS = 128 / PR, NP = kBN / RS;
+    const int pc = w % PR, rr = w / PR;
+    int copied = -1;  // bf16: the chunk whose copies are under way
     auto filled = [&](int c) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bar_full[c % kBar]));
     };
-    if constexpr (E4) {
-      // a thread's pieces: 16 codes of column piece pc in rows tid / PR + i * RS
-      constexpr int PR = L::CW / 16, RS = 128 / PR, NP = kBN / RS;
-      const int pc = w % PR, rr = w / PR;
-      uint4 buf[2][NP];
-      auto load = [&](int c, uint4 (&v)[NP]) -> bool {
-        int j, h;
-        const char* pool;
-        where(c, j, pool, h);
-        if (!rows_ready(j)) return false;
+#pragma unroll 1
+    for (int c = group; c < nchunks; c += 2) {
+      int j;
+      bool is_v;
+      unit_at(c / L::NCH, ntiles, j, is_v);
+      if (!wait(bar_rows[j % kBar], (j / kBar) & 1, __LINE__)) break;
+      const char* src = static_cast<const char*>(is_v ? p.c.v : p.c.k) + ((c % L::NCH) * L::CW + (pc << sh)) * (E4 ? 1 : 2);
+      const int* rows = &row_s[j % kBar][rr];
+      const uint32_t dst = sRing + (c % L::NC) * L::kChunk + (pc >> (E4 ? 2 : 3)) * L::kBox;
+      if constexpr (E4) {
+        uint4 v[NP];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          const int row = row_s[j % kBar][rr + i * RS];
-          v[i] = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool + (int64_t)row * D + h * L::CW + pc * 16))
-                          : make_uint4(0u, 0u, 0u, 0u);
+          const int row = rows[i * RS];
+          v[i] = row >= 0 ? load_once(reinterpret_cast<const uint4*>(src + (int64_t)row * D)) : make_uint4(0u, 0u, 0u, 0u);
         }
-        return true;
-      };
-      auto store = [&](int c, const uint4 (&v)[NP]) -> bool {
-        if (!slot_free(c)) return false;
+        if (c >= L::NC && !wait(bar_done[(c - L::NC) % kBar], ((c - L::NC) / kBar) & 1, __LINE__)) break;
         // pieces 4-7 write their halves in the other order: the eight threads
         // of a row then cover all banks with each store
-        const uint32_t dst = sRing + (c % L::NC) * L::kChunk + (pc >> 2) * L::kBox;
-        const int flip = pc >> 2;
+        const int flip = pc >> 2, at = (pc & 3) * 2;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           uint4 x, y;
@@ -341,54 +312,38 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
           codes_f16(v[i].y, x.z, x.w);
           codes_f16(v[i].z, y.x, y.y);
           codes_f16(v[i].w, y.z, y.w);
-          const int r = rr + i * RS, at = (pc & 3) * 2;
+          const int r = rr + i * RS;
           st_shared_v4(dst + sw128_offset(r, at + flip), flip ? y : x);
           st_shared_v4(dst + sw128_offset(r, at + 1 - flip), flip ? x : y);
         }
         filled(c);
-        return true;
-      };
-      if (nchunks > 0) ok = load(0, buf[0]);
-      if (ok && nchunks > 1) ok = load(1, buf[1]);
-      for (int c = 0; ok && c < nchunks; c += 2) {
-        ok = store(c, buf[0]);
-        if (ok && c + 2 < nchunks) ok = load(c + 2, buf[0]);
-        if (ok && c + 1 < nchunks) ok = store(c + 1, buf[1]);
-        if (ok && c + 3 < nchunks) ok = load(c + 3, buf[1]);
-      }
-    } else {
-      constexpr int PR = L::CW / 8, RS = 128 / PR, NP = kBN / RS;
-      const int pc = w % PR, rr = w / PR;
-      int c = 0;
-      for (; ok && c < nchunks; ++c) {
-        int j, h;
-        const char* pool;
-        where(c, j, pool, h);
-        ok = rows_ready(j) && slot_free(c);
-        if (!ok) break;
-        const uint32_t dst = sRing + (c % L::NC) * L::kChunk + (pc >> 3) * L::kBox;
+      } else {
+        if (c >= L::NC && !wait(bar_done[(c - L::NC) % kBar], ((c - L::NC) / kBar) & 1, __LINE__)) break;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          const int r = rr + i * RS, row = row_s[j % kBar][r];
-          copy16(dst + sw128_offset(r, pc & 7), pool + ((int64_t)(row < 0 ? 0 : row) * D + h * L::CW + pc * 8) * 2, row >= 0);
+          const int r = rr + i * RS, row = rows[i * RS];
+          copy16(dst + sw128_offset(r, pc & 7), src + (int64_t)(row < 0 ? 0 : row) * D * 2, row >= 0);
         }
         copy_commit();
-        if (c >= 2) {
-          copy_wait<2>();
-          filled(c - 2);
+        if (copied >= 0) {
+          copy_wait<1>();
+          filled(copied);
         }
+        copied = c;
       }
+    }
+    if constexpr (!E4) {
       copy_wait<0>();
-      if (ok)
-        for (int x = nchunks < 2 ? 0 : nchunks - 2; x < nchunks; ++x) filled(x);
+      if (copied >= 0) filled(copied);
     }
   } else {
     // ------------------------------------------------------------ softmax
     more_registers<kRegsSoftmax>();
-    const int sw = warp - 8, q4 = sw & 3, hf = sw >> 2;
+    const int sw = warp - 12, q4 = sw & 3, hf = sw >> 2;
     const int i = q4 * 32 + lane;
     const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
     // queries: a warp takes 16 rows, eight columns a lane
+#pragma unroll 2
     for (int x = 0; x < 16; ++x) {
       const int r = sw * 16 + x, t = r0 + r;
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -419,8 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bar_q));
 
-    bool ok = mbar_wait_warp(smem_u32(&bar_q), 0, abortp);  // back_s of rows that other warps wrote
-    if (!ok && lane == 0) fail(__LINE__);
+    bool ok = wait(bar_q, 0, __LINE__);  // back_s of rows that other warps wrote
     const bool row_ok = r0 + i < r1;
     const int tok = row_ok ? (r0 + i) / p.gq : 0, hh = row_ok ? r0 + i - tok * p.gq : 0;
     // a row past the end has zero queries; seeing every key keeps its warp on the short path
@@ -429,12 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     float m_run = -CUDART_INF_F, l_run = 0.f;
     for (int j = 0; ok && j < ntiles; ++j) {
       const int bf = j & 1, sl = j % kBar, key0 = kb + j * kBN + hf * 64;
-      if (!mbar_wait_warp(smem_u32(&bar_rows[sl]), (j / kBar) & 1, abortp) ||
-          !mbar_wait_warp(smem_u32(&bar_s[bf]), (j >> 1) & 1, abortp)) {
-        if (lane == 0) fail(__LINE__);
-        ok = false;
-        break;
-      }
+      ok = wait(bar_rows[sl], (j / kBar) & 1, __LINE__) && wait(bar_s[bf], (j >> 1) & 1, __LINE__);
+      if (!ok) break;
       tc_fence_after();
       uint64_t y[32];  // scores of this half's 64 keys, two by two
       {
@@ -486,11 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       top_s[bf][hf][i] = mx;
       tc_fence_before();
       mbar_arrive(smem_u32(&bar_pair[q4]));
-      if (!mbar_wait_warp(smem_u32(&bar_pair[q4]), j & 1, abortp)) {
-        if (lane == 0) fail(__LINE__);
-        ok = false;
-        break;
-      }
+      ok = wait(bar_pair[q4], j & 1, __LINE__);
+      if (!ok) break;
       tc_fence_after();
       mx = fmaxf(mx, top_s[bf][hf ^ 1][i]);
       if constexpr (!E4) mx *= crow;
@@ -506,11 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       }
       if (__any_sync(0xffffffffu, rescale)) {
         // S_j done means PV_{j-2} done, so bar_o has completed j-1 or j phases
-        if (!mbar_wait_warp(smem_u32(&bar_o), (j - 1) & 1, abortp)) {
-          if (lane == 0) fail(__LINE__);
-          ok = false;
-          break;
-        }
+        ok = wait(bar_o, (j - 1) & 1, __LINE__);
+        if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
         for (int c0 = hf * (D / 2); c0 < (hf + 1) * (D / 2); c0 += 32) {
@@ -572,18 +516,12 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     // ---- the row sums of both halves, then this half of O's columns
     float l = 0.f;
     if (ok && ntiles > 0) {
-      if (!mbar_wait_warp(smem_u32(&bar_last), 0, abortp)) {
-        if (lane == 0) fail(__LINE__);
-        ok = false;
-      }
+      ok = wait(bar_last, 0, __LINE__);
       tc_fence_after();
       if (ok) {
         top_s[ntiles & 1][hf][i] = l_run;
         mbar_arrive(smem_u32(&bar_pair[q4]));
-        if (!mbar_wait_warp(smem_u32(&bar_pair[q4]), ntiles & 1, abortp)) {
-          if (lane == 0) fail(__LINE__);
-          ok = false;
-        }
+        ok = wait(bar_pair[q4], ntiles & 1, __LINE__);
       }
       if (ok) l = top_s[ntiles & 1][0][i] + top_s[ntiles & 1][1][i];
     }
@@ -624,6 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       else
         p.lse[out] = z;
     }
+  }
+  if (gave_up && (lane == 0 || warp == 1)) {
+    atomicOr(p.status, kStatusTimeout);
+    atomicCAS(p.status + 1, 0u, ((uint32_t)kKCachedTc << 16) | (uint32_t)gave_up);
   }
   tc_fence_before();
   __syncthreads();

@@ -218,6 +218,8 @@ struct CachedParams {
   int32_t hq, gq, batch, max_q, causal;
   int32_t q_dtype, o_dtype;
   int64_t total_q, q_stride, pages_per_seq;
+  // j / page_size = umulhi(j, page_mul) >> page_shift for 0 <= j < 2^31 (page_mul 0: page_size 1)
+  uint32_t page_mul, page_shift;
   float scale, scale_log2;
   int32_t ns;
   int64_t span;

@@ -91,6 +91,21 @@ ls_status check_cached(const ls_cached_attn_desc* d, const ls_kv_cache* c) {
   return LS_OK;
 }
 
+// Multiplier and shift of j / d for 0 <= j < 2^31 (d >= 1): with 2^(s-1) < d <=
+// 2^s, m = ceil(2^(31+s) / d) is below 2^32 and off by e < d <= 2^s, so j m /
+// 2^(31+s) exceeds j / d by j e / (d 2^(31+s)) < 1 / d.  umulhi takes 2^32 of
+// the divisor; d = 1 has no such pair, and a multiplier of 0 stands for it.
+void page_divisor(uint32_t d, uint32_t* mul, uint32_t* shift) {
+  uint32_t s = 0;
+  while ((1ull << s) < d) ++s;
+  if (s == 0) {
+    *mul = 0, *shift = 0;
+    return;
+  }
+  *mul = (uint32_t)(((1ull << (31 + s)) + d - 1) / d);
+  *shift = s - 1;
+}
+
 CachedPlan plan_cached(const ls_cached_attn_desc& d, const ls_kv_cache& c) {
   CachedPlan pl{};
   const int gq = d.hq / c.hkv, sms = device_sms();
@@ -266,6 +281,7 @@ ls_status ls_cached_attn(const ls_cached_attn_desc* desc, const ls_kv_cache* cac
   p.total_q = desc->total_q;
   p.q_stride = desc->q_stride;
   p.pages_per_seq = pages_per_seq;
+  page_divisor(cache->page_size, &p.page_mul, &p.page_shift);
   p.scale = desc->softmax_scale;
   p.scale_log2 = desc->softmax_scale * 1.4426950408889634f;
   p.ns = pl.ns;

@@ -81,6 +81,31 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
   return __all_sync(0xffffffffu, ok);
 }
 
+// The same wait in six instructions, for kernels whose roles' loops together
+// press on the instruction cache (mbar_wait's timers and abort flag are about
+// forty).  Bounded by polls alone: each returns at once or is suspended for at
+// most about the hinted 20 us, so 2^17 of them take between a few milliseconds
+// (far beyond any wait between the warps of a CTA) and 2.6 s.
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 131072;\n"
+      "W_%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.and.u32 q, n, 0, !p;\n\t"
+      "@q bra W_%=;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_short_warp(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_short(bar, parity));
+}
+
 // ---------------------------------------------------------------- proxies
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
