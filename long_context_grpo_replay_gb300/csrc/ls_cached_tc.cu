@@ -285,23 +285,44 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bar_full[c % kBar]));
     };
-#pragma unroll 1
-    for (int c = group; c < nchunks; c += 2) {
-      int j;
+    auto source = [&](int c, int& j) -> const char* {
       bool is_v;
       unit_at(c / L::NCH, ntiles, j, is_v);
-      if (!wait(bar_rows[j % kBar], (j / kBar) & 1, __LINE__)) break;
-      const char* src = static_cast<const char*>(is_v ? p.c.v : p.c.k) + ((c % L::NCH) * L::CW + (pc << sh)) * (E4 ? 1 : 2);
-      const int* rows = &row_s[j % kBar][rr];
+      return static_cast<const char*>(is_v ? p.c.v : p.c.k) + ((c % L::NCH) * L::CW + (pc << sh)) * (E4 ? 1 : 2);
+    };
+    // e4m3: a thread's pieces of its next chunk; each is loaded as soon as its
+    // place is converted, so that a group always has about a chunk in flight
+    uint4 v[E4 ? NP : 1];
+    const char* src = nullptr;
+    const int* rows = nullptr;
+    auto fetch = [&](int i) {
+      const int row = rows[i * RS];
+      v[i] = row >= 0 ? load_once(reinterpret_cast<const uint4*>(src + (int64_t)row * D)) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    bool ok = true;
+    if (E4 && group < nchunks) {
+      int j;
+      src = source(group, j);
+      rows = &row_s[j % kBar][rr];
+      ok = wait(bar_rows[j % kBar], (j / kBar) & 1, __LINE__);
+      if (ok)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) fetch(i);
+    }
+#pragma unroll 1
+    for (int c = group; ok && c < nchunks; c += 2) {
+      const int next = E4 ? c + 2 : c;
+      int j = 0;
+      if (next < nchunks) {
+        src = source(next, j);
+        rows = &row_s[j % kBar][rr];
+        ok = wait(bar_rows[j % kBar], (j / kBar) & 1, __LINE__);
+        if (!ok) break;
+      }
+      if (c >= L::NC) ok = wait(bar_done[(c - L::NC) % kBar], ((c - L::NC) / kBar) & 1, __LINE__);
+      if (!ok) break;
       const uint32_t dst = sRing + (c % L::NC) * L::kChunk + (pc >> (E4 ? 2 : 3)) * L::kBox;
       if constexpr (E4) {
-        uint4 v[NP];
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const int row = rows[i * RS];
-          v[i] = row >= 0 ? load_once(reinterpret_cast<const uint4*>(src + (int64_t)row * D)) : make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (c >= L::NC && !wait(bar_done[(c - L::NC) % kBar], ((c - L::NC) / kBar) & 1, __LINE__)) break;
         // pieces 4-7 write their halves in the other order: the eight threads
         // of a row then cover all banks with each store
         const int flip = pc >> 2, at = (pc & 3) * 2;
@@ -315,10 +336,10 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
           const int r = rr + i * RS;
           st_shared_v4(dst + sw128_offset(r, at + flip), flip ? y : x);
           st_shared_v4(dst + sw128_offset(r, at + 1 - flip), flip ? x : y);
+          if (next < nchunks) fetch(i);
         }
         filled(c);
       } else {
-        if (c >= L::NC && !wait(bar_done[(c - L::NC) % kBar], ((c - L::NC) / kBar) & 1, __LINE__)) break;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           const int r = rr + i * RS, row = rows[i * RS];
