@@ -96,25 +96,25 @@ __device__ __forceinline__ void quant_row(const Row8& r, unsigned mask, bool fir
 template <typename T, int FMT, int D>
 __global__ void __launch_bounds__(256) cache_write_kernel(
     const ls_kv_cache c, const T* __restrict__ k, const T* __restrict__ v, int64_t k_stride,
-    int64_t v_stride, const int64_t* __restrict__ slots, int64_t n_rows, uint32_t* status) {
+    int64_t v_stride, const int64_t* __restrict__ slots, uint32_t n_rows, int64_t pool_slots, uint32_t* status) {
   constexpr int LANES = D / 8;
   const int lane = threadIdx.x & 31;
-  const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LANES;
+  const uint32_t row = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
   const int part = threadIdx.x % LANES;
   const unsigned mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << (lane / LANES * LANES);
   if (row >= n_rows) return;  // a whole group leaves
-  const int64_t t = row / c.hkv;
+  const uint32_t t = row / (uint32_t)c.hkv;
   const int head = (int)(row - t * c.hkv);
   const int64_t slot = __ldg(slots + t);
   if (slot < 0) return;
-  const int64_t page = slot / c.page_size;
-  if (page >= c.pool_pages) {
+  if (slot >= pool_slots) {
     if (part == 0 && status) atomicOr(status, kStatusBadIndex);
     return;
   }
-  const int64_t dst = (page * c.hkv + head) * c.page_size + (slot - page * c.page_size);
-  const Row8 rk = load8(k + t * k_stride + head * D + part * 8);
-  const Row8 rv = load8(v + t * v_stride + head * D + part * 8);
+  const uint32_t page = (uint32_t)slot / (uint32_t)c.page_size;  // rows of the pool number below 2^31
+  const int64_t dst = (int64_t)((page * c.hkv + head) * c.page_size + ((uint32_t)slot - page * c.page_size));
+  const Row8 rk = load8(k + (int64_t)t * k_stride + head * D + part * 8);
+  const Row8 rv = load8(v + (int64_t)t * v_stride + head * D + part * 8);
   if constexpr (FMT == LS_CACHE_E4M3) {
     quant_row<LANES>(rk, mask, part == 0, static_cast<uint8_t*>(c.k) + dst * D + part * 8, c.k_exp + dst);
     quant_row<LANES>(rv, mask, part == 0, static_cast<uint8_t*>(c.v) + dst * D + part * 8, c.v_exp + dst);
@@ -144,22 +144,22 @@ __device__ __forceinline__ Row8 load_codes(const uint8_t* p, int e) {
 template <typename T, int FMT, int D>
 __global__ void __launch_bounds__(256) cache_read_kernel(
     const ls_kv_cache c, T* __restrict__ k, T* __restrict__ v, const int64_t* __restrict__ slots,
-    int64_t n_rows, uint32_t* status) {
+    uint32_t n_rows, int64_t pool_slots, uint32_t* status) {
   constexpr int LANES = D / 8;
-  const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LANES;
+  const uint32_t row = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
   const int part = threadIdx.x % LANES;
   if (row >= n_rows) return;
-  const int64_t t = row / c.hkv;
+  const uint32_t t = row / (uint32_t)c.hkv;
   const int head = (int)(row - t * c.hkv);
   const int64_t slot = __ldg(slots + t);
-  const int64_t page = slot >= 0 ? slot / c.page_size : 0;
   Row8 rk, rv;
-  if (slot < 0 || page >= c.pool_pages) {
+  if (slot < 0 || slot >= pool_slots) {
     if (slot >= 0 && part == 0 && status) atomicOr(status, kStatusBadIndex);
 #pragma unroll
     for (int i = 0; i < 8; ++i) rk.x[i] = rv.x[i] = 0.f;
   } else {
-    const int64_t src = (page * c.hkv + head) * c.page_size + (slot - page * c.page_size);
+    const uint32_t page = (uint32_t)slot / (uint32_t)c.page_size;
+    const int64_t src = (int64_t)((page * c.hkv + head) * c.page_size + ((uint32_t)slot - page * c.page_size));
     if constexpr (FMT == LS_CACHE_E4M3) {
       rk = load_codes(static_cast<const uint8_t*>(c.k) + src * D + part * 8, __ldg(c.k_exp + src));
       rv = load_codes(static_cast<const uint8_t*>(c.v) + src * D + part * 8, __ldg(c.v_exp + src));
@@ -171,8 +171,8 @@ __global__ void __launch_bounds__(256) cache_read_kernel(
       rv = load8(static_cast<const float*>(c.v) + src * D + part * 8);
     }
   }
-  store8(k + row * D + part * 8, rk);
-  store8(v + row * D + part * 8, rv);
+  store8(k + (int64_t)row * D + part * 8, rk);
+  store8(v + (int64_t)row * D + part * 8, rv);
 }
 
 // Calls f with the format and the head dimension as constants.
@@ -199,16 +199,17 @@ cudaError_t launch_cache_write(const ls_kv_cache& c, int src_dtype, const void* 
                                int64_t n_tok, uint32_t* status, cudaStream_t s) {
   const int64_t rows = n_tok * c.hkv;
   const int64_t blocks = (rows * (c.head_dim / 8) + 255) / 256;
-  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (rows > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int64_t pool_slots = c.pool_pages * c.page_size;
   return with_shape(c, [&](auto fmt, auto d) {
     LaunchScope ls(kKCacheWrite, s);
     if (src_dtype == LS_DTYPE_F32)
       cache_write_kernel<float, fmt.value, d.value><<<(unsigned)blocks, 256, 0, s>>>(
-          c, static_cast<const float*>(k), static_cast<const float*>(v), k_stride, v_stride, slots, rows, status);
+          c, static_cast<const float*>(k), static_cast<const float*>(v), k_stride, v_stride, slots, (uint32_t)rows, pool_slots, status);
     else
       cache_write_kernel<__nv_bfloat16, fmt.value, d.value><<<(unsigned)blocks, 256, 0, s>>>(
           c, static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), k_stride, v_stride, slots,
-          rows, status);
+          (uint32_t)rows, pool_slots, status);
     return cudaGetLastError();
   });
 }
@@ -217,15 +218,16 @@ cudaError_t launch_cache_read(const ls_kv_cache& c, const int64_t* slots, int64_
                               int dst_dtype, void* k, void* v, uint32_t* status, cudaStream_t s) {
   const int64_t rows = n_tok * c.hkv;
   const int64_t blocks = (rows * (c.head_dim / 8) + 255) / 256;
-  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (rows > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int64_t pool_slots = c.pool_pages * c.page_size;
   return with_shape(c, [&](auto fmt, auto d) {
     LaunchScope ls(kKCacheRead, s);
     if (dst_dtype == LS_DTYPE_F32)
       cache_read_kernel<float, fmt.value, d.value><<<(unsigned)blocks, 256, 0, s>>>(
-          c, static_cast<float*>(k), static_cast<float*>(v), slots, rows, status);
+          c, static_cast<float*>(k), static_cast<float*>(v), slots, (uint32_t)rows, pool_slots, status);
     else
       cache_read_kernel<__nv_bfloat16, fmt.value, d.value><<<(unsigned)blocks, 256, 0, s>>>(
-          c, static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v), slots, rows, status);
+          c, static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v), slots, (uint32_t)rows, pool_slots, status);
     return cudaGetLastError();
   });
 }

@@ -308,15 +308,17 @@ struct MmaShape {
   static constexpr int kRowBytes = D * (E4 ? 1 : 2);
   static constexpr int kChunks = kRowBytes / 16;      // 16-byte pieces of a row
   static constexpr int kStage = 2 * 16 * kRowBytes;   // K and V of 16 keys
-  static constexpr int NW = kStage > 8192 ? 4 : 8;
-  static constexpr int ST = kStage * NW * 6 <= 192 * 1024 ? 6 : 3;
+  // two CTAs to an SM, so that one streams while the other starts or ends:
+  // about 96 KB of ring each
+  static constexpr int NW = kStage > 8192 ? 2 : 4;
+  static constexpr int ST = kStage * NW * 6 <= 96 * 1024 ? 6 : 3;
   static constexpr int kRing = NW * ST * kStage;
   static constexpr int VD = E4 && D >= 128 ? 16 : 8;  // V columns of a lane's piece
   static constexpr int NU = D / (8 * VD);
 };
 
 template <int D, bool E4, int NT>
-__global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 1) cached_mma_kernel(const CachedParams p) {
+__global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 2) cached_mma_kernel(const CachedParams p) {
   using L = MmaShape<D, E4>;
   constexpr int NW = L::NW, ST = L::ST, RB = L::kRowBytes, CPR = L::kChunks, VD = L::VD;
   constexpr int KS = D / 16;                 // products per score block, and m-tiles of O^T
@@ -628,8 +630,10 @@ __global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 1) cached_mma_kernel
 __global__ void __launch_bounds__(256) cached_join_kernel(int ns, int64_t n_rows, int d, const float* __restrict__ o_parts,
                                                           const float* __restrict__ lse_parts, int o_dtype, void* o,
                                                           float* lse) {
-  __shared__ float w[128], total_s;
+  __shared__ float w[kCachedMaxParts], total_s;
   __shared__ float4 acc_s[256];
+  // launched while the parts' kernel still runs: wait for its results
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, cols = d >> 2, groups = 256 / cols;
   if (tid < 32) {
@@ -705,13 +709,13 @@ cudaError_t run_mma_d(const CachedParams& p, cudaStream_t s) {
   const int64_t rows = (int64_t)p.max_q * p.gq;
   if (rows <= 8) return e4 ? run_mma<D, true, 1>(p, s) : run_mma<D, false, 1>(p, s);
   if (rows <= 16 || D == 256) return e4 ? run_mma<D, true, 2>(p, s) : run_mma<D, false, 2>(p, s);
-  if constexpr (D < 256) return e4 ? run_mma<D, true, 4>(p, s) : run_mma<D, false, 4>(p, s);
+  if constexpr (D < 256) return e4 ? run_mma<D, true, D == 128 ? 3 : 4>(p, s) : run_mma<D, false, D == 128 ? 3 : 4>(p, s);
   return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-int cached_mma_rows(int d) { return d == 256 ? 16 : 32; }
+int cached_mma_rows(int d) { return d == 256 ? 16 : d == 128 ? 24 : 32; }
 
 cudaError_t launch_cached_mma(const CachedParams& p, cudaStream_t s) {
   switch (p.c.head_dim) {
@@ -724,8 +728,17 @@ cudaError_t launch_cached_mma(const CachedParams& p, cudaStream_t s) {
 cudaError_t launch_cached_join(const CachedParams& p, cudaStream_t s) {
   LaunchScope ls(kKCachedJoin, s);
   const int64_t rows = p.total_q * p.hq;
-  cached_join_kernel<<<(unsigned)rows, 256, 0, s>>>(p.ns, rows, p.c.head_dim, p.o_parts, p.lse_parts, p.o_dtype, p.o, p.lse);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)rows);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cached_join_kernel, (int)p.ns, rows, (int)p.c.head_dim, (const float*)p.o_parts,
+                            (const float*)p.lse_parts, (int)p.o_dtype, p.o, p.lse);
 }
 
 cudaError_t launch_cached_simt(const CachedParams& p, cudaStream_t s) {

@@ -113,7 +113,7 @@ CachedPlan plan_cached(const ls_cached_attn_desc& d, const ls_kv_cache& c) {
   const double key_bytes = 2.0 * c.head_dim * (c.format == LS_CACHE_F32 ? 4 : c.format == LS_CACHE_BF16 ? 2 : 1);
   // A CTA's tile of rows, the keys that parts are counted in, and about how
   // long a CTA takes for them and for its start and end (microseconds).
-  int64_t tile, quantum;
+  int64_t tile, quantum, ctas = sms;
   double per_quantum, fixed;
   if (d.q_dtype != LS_DTYPE_BF16 || c.format == LS_CACHE_F32 || force_simt()) {
     pl.route = kRouteSimt;
@@ -122,8 +122,8 @@ CachedPlan plan_cached(const ls_cached_attn_desc& d, const ls_kv_cache& c) {
   } else if (rows <= cached_mma_rows(c.head_dim) || !device_is_sm100_family()) {
     pl.route = kRouteMma;
     tile = rows < 8 ? 8 : rows < cached_mma_rows(c.head_dim) ? rows : cached_mma_rows(c.head_dim);
-    quantum = 128;
-    per_quantum = quantum * key_bytes / 44e3, fixed = 4.0;
+    quantum = 128, ctas = 2 * sms;
+    per_quantum = quantum * key_bytes / 22e3, fixed = 6.0;
   } else {
     pl.route = kRouteTc;
     tile = 128, quantum = 128;
@@ -132,7 +132,7 @@ CachedPlan plan_cached(const ls_cached_attn_desc& d, const ls_kv_cache& c) {
   const int64_t units = (int64_t)d.batch * c.hkv * ((rows + tile - 1) / tile);
   const int64_t quanta = d.max_kv > 0 ? (d.max_kv + quantum - 1) / quantum : 1;
   const size_t out_rows = (size_t)d.total_q * d.hq;
-  // Rounds of CTAs (one to an SM) against the parts' float32 results, written
+  // Rounds of CTAs against the parts' float32 results, written
   // and read once.  Several sequences end at different lengths: the model
   // takes them for half as long as the longest on average, and asks for a few
   // rounds, which even them out.
@@ -141,8 +141,8 @@ CachedPlan plan_cached(const ls_cached_attn_desc& d, const ls_kv_cache& c) {
   for (int64_t ns = 1; ns <= kCachedMaxParts && ns <= quanta && units > 0; ++ns) {
     const int64_t span = (quanta + ns - 1) / ns;
     if ((quanta + span - 1) / span != ns) continue;
-    double rounds = (double)((units * ns + sms - 1) / sms);
-    if (d.batch > 1) rounds = 0.5 * (double)(units * ns) / sms + 1.0;
+    double rounds = (double)((units * ns + ctas - 1) / ctas);
+    if (d.batch > 1) rounds = 0.5 * (double)(units * ns) / ctas + 1.0;
     const double cost = rounds * (span * per_quantum + fixed) +
                         (ns > 1 ? 3.0 + ns * (double)out_rows * c.head_dim * 8.0 / 6.0e6 : 0.0);
     if (cost < best_cost * 0.99) best_cost = cost, best = ns;
@@ -214,7 +214,7 @@ ls_status ls_cache_write(const ls_kv_cache* cache, int32_t src_dtype, const void
   if (!k || !v || !slots) return fail(LS_ERR_INVALID_ARGUMENT, "k, v and slots must be non-NULL");
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8))
     return fail(LS_ERR_INVALID_ARGUMENT, "k and v must be 16-byte aligned, slots 8-byte");
-  if (n_tok > INT64_MAX / 65536 / cache->hkv) return fail(LS_ERR_UNSUPPORTED, "n_tok too large");
+  if (n_tok > INT32_MAX / cache->hkv) return fail(LS_ERR_UNSUPPORTED, "n_tok * hkv too large");
   uint32_t* status;
   LS_CHECK(status_word(ws, ws_bytes, &status));
   LS_CUDA(launch_cache_write(*cache, src_dtype, k, v, k_stride, v_stride, slots, n_tok, status,
@@ -234,7 +234,7 @@ ls_status ls_cache_read(const ls_kv_cache* cache, const int64_t* slots, int64_t 
   if (!k || !v || !slots) return fail(LS_ERR_INVALID_ARGUMENT, "k, v and slots must be non-NULL");
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8))
     return fail(LS_ERR_INVALID_ARGUMENT, "k and v must be 16-byte aligned, slots 8-byte");
-  if (n_tok > INT64_MAX / 65536 / cache->hkv) return fail(LS_ERR_UNSUPPORTED, "n_tok too large");
+  if (n_tok > INT32_MAX / cache->hkv) return fail(LS_ERR_UNSUPPORTED, "n_tok * hkv too large");
   uint32_t* status;
   LS_CHECK(status_word(ws, ws_bytes, &status));
   LS_CUDA(launch_cache_read(*cache, slots, n_tok, dst_dtype, k, v, status,

@@ -11,9 +11,9 @@
 // into D in the product's epilogue, and uses D in two products.
 //
 // One tiled product serves all three: TILE x TILE outputs for 256 threads,
-// 16 of the inner dimension at a time through shared memory, 8 x 8 (or, where
-// 128 x 128 tiles would leave SMs idle, 4 x 4) outputs a thread.  It is bound
-// by FMA issue; its rate is near that of a library float32 product.
+// 16 of the inner dimension at a time through two shared buffers, 8 x 8 (or,
+// where 128 x 128 tiles would leave SMs idle, 4 x 4) outputs a thread; few
+// rows' dh is cut along the vocabulary into float32 sums.  Bound by FMA issue.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -39,22 +39,62 @@ struct Operand {
   const T* p;
   int64_t si, sk;  // strides of i and k; one of them is 1
   int64_t n;       // extent of i
+  bool quads;      // four neighbours of the contiguous index can be read at once
 };
+template <typename T>
+Operand<T> operand(const T* p, int64_t si, int64_t sk, int64_t n) {
+  const int64_t other = sk == 1 ? si : sk;
+  return {p, si, sk, n, reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0 && other % 4 == 0};
+}
 
-// C tile = sum_k A(m, k) B(n, k); epi(m, n, value) for each output of the tile.
+__device__ __forceinline__ float4 ld4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+}
+
+// C tile = sum_k A(m, k) B(n, k) over k in [kb, ke).  The next 16 of k are
+// loaded into registers while this 16 is multiplied from shared memory.
 template <int TM, typename TA, typename TB>
 struct Product {
   static constexpr int TILE = 16 * TM;
-  float a[kBK][TILE + 4], b[kBK][TILE + 4];
+  static constexpr int Q = TILE * kBK / 4 / 256;  // quads of an operand's tile per thread
+  float a[2][kBK][TILE + 4], b[2][kBK][TILE + 4];
 
   template <typename T>
-  __device__ __forceinline__ static void load(float (&dst)[kBK][TILE + 4], const Operand<T>& o,
-                                              int64_t i0, int64_t k0, int64_t K) {
+  __device__ __forceinline__ static void load(float4 (&r)[Q], const Operand<T>& o, int64_t i0, int64_t k0, int64_t ke) {
+    // a quad lies along the contiguous index, and so do neighbouring threads
 #pragma unroll
-    for (int x = threadIdx.x; x < TILE * kBK; x += 256) {
-      // neighbouring threads follow the contiguous index
-      const int i = o.sk == 1 ? x / kBK : x % TILE, k = o.sk == 1 ? x % kBK : x / TILE;
-      dst[k][i] = i0 + i < o.n && k0 + k < K ? ldf(o.p + (i0 + i) * o.si + (k0 + k) * o.sk) : 0.f;
+    for (int q = 0; q < Q; ++q) {
+      const int x = threadIdx.x + q * 256;
+      const bool kc = o.sk == 1;
+      const int64_t i = i0 + (kc ? x / 4 : x % (TILE / 4) * 4), k = k0 + (kc ? x % 4 * 4 : x / (TILE / 4));
+      const T* src = o.p + i * o.si + k * o.sk;
+      const int64_t left = kc ? ke - k : o.n - i;  // of the contiguous index
+      const bool there = kc ? i < o.n : k < ke;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (there && left >= 4 && o.quads) {
+        v = ld4(src);
+      } else if (there) {
+        if (left > 0) v.x = ldf(src);
+        if (left > 1) v.y = ldf(src + 1);
+        if (left > 2) v.z = ldf(src + 2);
+        if (left > 3) v.w = ldf(src + 3);
+      }
+      r[q] = v;
+    }
+  }
+  __device__ __forceinline__ static void store(float (&dst)[kBK][TILE + 4], const float4 (&r)[Q], bool kc) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int x = threadIdx.x + q * 256;
+      if (kc) {
+        const int i = x / 4, k = x % 4 * 4;
+        dst[k][i] = r[q].x, dst[k + 1][i] = r[q].y, dst[k + 2][i] = r[q].z, dst[k + 3][i] = r[q].w;
+      } else {
+        *reinterpret_cast<float4*>(&dst[x / (TILE / 4)][x % (TILE / 4) * 4]) = r[q];
+      }
     }
   }
 
@@ -62,30 +102,43 @@ struct Product {
   __device__ __forceinline__ static int at(int t, int i) { return TM == 8 ? (i / 4) * 64 + t * 4 + (i & 3) : t * 4 + i; }
 
   __device__ __forceinline__ void run(const Operand<TA>& A, const Operand<TB>& B, int64_t m0, int64_t n0,
-                                      int64_t K, float (&acc)[TM][TM]) {
+                                      int64_t kb, int64_t ke, float (&acc)[TM][TM]) {
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TM; ++j) acc[i][j] = 0.f;
-    for (int64_t k0 = 0; k0 < K; k0 += kBK) {
-      __syncthreads();
-      load(a, A, m0, k0, K);
-      load(b, B, n0, k0, K);
-      __syncthreads();
+    float4 ra[Q], rb[Q];
+    load(ra, A, m0, kb, ke);
+    load(rb, B, n0, kb, ke);
+    store(a[0], ra, A.sk == 1);
+    store(b[0], rb, B.sk == 1);
+    __syncthreads();
+    int buf = 0;
+    for (int64_t k0 = kb; k0 < ke; k0 += kBK, buf ^= 1) {
+      const bool more = k0 + kBK < ke;
+      if (more) {
+        load(ra, A, m0, k0 + kBK, ke);
+        load(rb, B, n0, k0 + kBK, ke);
+      }
 #pragma unroll
       for (int k = 0; k < kBK; ++k) {
         float x[TM], y[TM];
 #pragma unroll
         for (int i = 0; i < TM; i += 4) {
-          *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(&a[k][at(ty, i)]);
-          *reinterpret_cast<float4*>(y + i) = *reinterpret_cast<const float4*>(&b[k][at(tx, i)]);
+          *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(&a[buf][k][at(ty, i)]);
+          *reinterpret_cast<float4*>(y + i) = *reinterpret_cast<const float4*>(&b[buf][k][at(tx, i)]);
         }
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
           for (int j = 0; j < TM; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
       }
+      if (more) {
+        store(a[buf ^ 1], ra, A.sk == 1);
+        store(b[buf ^ 1], rb, B.sk == 1);
+      }
+      __syncthreads();
     }
   }
 };
@@ -93,13 +146,13 @@ struct Product {
 // Forward: per row of a 16*TM-column tile of the vocabulary, (maximum, sum of
 // 2^(x - maximum)) of the logits in base 2, and the target's logit.
 template <int TM, typename T>
-__global__ void __launch_bounds__(256) vocab_fwd_kernel(const ls_vocab_desc d, const T* h, const T* w,
-                                                        const int64_t* targets, float2* parts, float* hit) {
+__global__ void __launch_bounds__(256) vocab_fwd_kernel(const ls_vocab_desc d, const Operand<T> A,
+                                                        const Operand<T> B, const int64_t* targets, float2* parts, float* hit) {
   using P = Product<TM, T, T>;
   __shared__ __align__(16) P sm;
   const int64_t m0 = (int64_t)blockIdx.x * P::TILE, n0 = (int64_t)blockIdx.y * P::TILE;
   float acc[TM][TM];
-  sm.run({h, d.h_stride, 1, d.n_rows}, {w, d.w_stride, 1, d.vocab}, m0, n0, d.hidden, acc);
+  sm.run(A, B, m0, n0, 0, d.hidden, acc);
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
@@ -168,14 +221,14 @@ __global__ void __launch_bounds__(256) vocab_join_kernel(int n_tiles, int64_t n_
 
 // D of a piece of the vocabulary: columns v0 .. v0 + np of the logits.
 template <int TM, typename T>
-__global__ void __launch_bounds__(256) vocab_slope_kernel(const ls_vocab_desc d, const T* h, const T* w,
-                                                          const int64_t* targets, const float* lse,
+__global__ void __launch_bounds__(256) vocab_slope_kernel(const ls_vocab_desc d, const Operand<T> A,
+                                                          const Operand<T> B, const int64_t* targets, const float* lse,
                                                           const float* d_logp, int64_t v0, int64_t np, float* out) {
   using P = Product<TM, T, T>;
   __shared__ __align__(16) P sm;
   const int64_t m0 = (int64_t)blockIdx.x * P::TILE, n0 = (int64_t)blockIdx.y * P::TILE;
   float acc[TM][TM];
-  sm.run({h, d.h_stride, 1, d.n_rows}, {w + v0 * d.w_stride, d.w_stride, 1, np}, m0, n0, d.hidden, acc);
+  sm.run(A, B, m0, n0, 0, d.hidden, acc);
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
@@ -195,15 +248,17 @@ __global__ void __launch_bounds__(256) vocab_slope_kernel(const ls_vocab_desc d,
   }
 }
 
-// out[m][n] (row stride n) = A B^T (+ add), rounded to TO once.
+// out[z][m][n] = A B^T over split z's share of the inner dimension (+ what is there), rounded to TO once.
 template <int TM, typename TA, typename TB, typename TO>
-__global__ void __launch_bounds__(256) vocab_product_kernel(Operand<TA> A, Operand<TB> B, int64_t K,
-                                                            const float* add, TO* out) {
+__global__ void __launch_bounds__(256) vocab_product_kernel(Operand<TA> A, Operand<TB> B, int64_t K, int64_t per,
+                                                            bool add, TO* out) {
   using P = Product<TM, TA, TB>;
   __shared__ __align__(16) P sm;
   const int64_t m0 = (int64_t)blockIdx.x * P::TILE, n0 = (int64_t)blockIdx.y * P::TILE;
   float acc[TM][TM];
-  sm.run(A, B, m0, n0, K, acc);
+  const int64_t kb = blockIdx.z * per, ke = kb + per < K ? kb + per : K;
+  out += (int64_t)blockIdx.z * A.n * B.n;
+  sm.run(A, B, m0, n0, kb, ke, acc);
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
@@ -214,10 +269,21 @@ __global__ void __launch_bounds__(256) vocab_product_kernel(Operand<TA> A, Opera
       const int64_t n = n0 + P::at(tx, j);
       if (n >= B.n) continue;
       float v = acc[i][j];
-      if (add) v += add[m * B.n + n];
+      if constexpr (sizeof(TO) == 4)
+        if (add) v += out[m * B.n + n];
       stf(out + m * B.n + n, v);
     }
   }
+}
+
+// dh from its float32 sums [split][n].
+template <typename T>
+__global__ void __launch_bounds__(256) vocab_sum_kernel(int splits, int64_t n, const float* __restrict__ sums, T* __restrict__ out) {
+  const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (x >= n) return;
+  float a = 0.f;
+  for (int s = 0; s < splits; ++s) a += __ldcs(sums + s * n + x);
+  stf(out + x, a);
 }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -233,6 +299,21 @@ int64_t simt_piece(const ls_vocab_desc& d) {
 bool small_tiles(int64_t m, int64_t n) {
   return ((m + 127) / 128) * ((n + 127) / 128) < device_sms();
 }
+// Ways to cut dh's inner dimension, a piece of the vocabulary: where its tiles
+// leave SMs idle, two CTAs an SM, 256 columns each at least.
+int simt_splits(const ls_vocab_desc& d) {
+  const int64_t tile = small_tiles(d.n_rows, d.hidden) ? 64 : 128;
+  const int64_t tiles = ((d.n_rows + tile - 1) / tile) * ((d.hidden + tile - 1) / tile);
+  int64_t s = tiles > 0 ? 2 * device_sms() / tiles : 1;
+  const int64_t most = simt_piece(d) / 256;
+  s = s < most ? s : most;
+  return s < 1 ? 1 : (int)s;
+}
+int64_t simt_per_split(const ls_vocab_desc& d) {
+  const int64_t s = simt_splits(d);
+  return round_up((size_t)((simt_piece(d) + s - 1) / s), kBK);
+}
+
 template <typename F>
 cudaError_t with_tile(int64_t m, int64_t n, F f) {
   const bool small = small_tiles(m, n);
@@ -249,6 +330,8 @@ cudaError_t with_tile(int64_t m, int64_t n, F f) {
 template <typename T>
 cudaError_t simt_fwd(const VocabParams& p, cudaStream_t s) {
   const ls_vocab_desc& d = p.d;
+  const auto A = operand(static_cast<const T*>(p.h), d.h_stride, 1, d.n_rows);
+  const auto B = operand(static_cast<const T*>(p.w), d.w_stride, 1, d.vocab);
   float2* parts = static_cast<float2*>(p.scratch);
   const int64_t tiles64 = (d.vocab + 63) / 64;
   float* hit = reinterpret_cast<float*>(parts + tiles64 * d.n_rows);
@@ -257,7 +340,7 @@ cudaError_t simt_fwd(const VocabParams& p, cudaStream_t s) {
     LaunchScope ls(kKVocabSimt, s);
     const cudaError_t e = with_tile(d.n_rows, d.vocab, [&](auto tm, dim3 grid) {
       n_tiles = (int)grid.y;
-      vocab_fwd_kernel<tm.value, T><<<grid, 256, 0, s>>>(d, static_cast<const T*>(p.h), static_cast<const T*>(p.w), p.targets, parts, hit);
+      vocab_fwd_kernel<tm.value, T><<<grid, 256, 0, s>>>(d, A, B, p.targets, parts, hit);
     });
     if (e != cudaSuccess) return e;
   }
@@ -269,38 +352,48 @@ cudaError_t simt_bwd(const VocabParams& p, cudaStream_t s) {
   const ls_vocab_desc& d = p.d;
   const T* h = static_cast<const T*>(p.h);
   const T* w = static_cast<const T*>(p.w);
-  const int64_t piece = simt_piece(d);
+  const int64_t piece = simt_piece(d), per = simt_per_split(d);
+  const int splits = (int)((piece + per - 1) / per);
+  const bool direct = splits == 1 && piece == d.vocab;
   float* slope = static_cast<float*>(p.scratch);
-  float* dh32 = slope + round_up((size_t)d.n_rows * piece, 64);
+  float* sums = slope + round_up((size_t)d.n_rows * piece, 64);
   for (int64_t v0 = 0; v0 < d.vocab; v0 += piece) {
     const int64_t np = d.vocab - v0 < piece ? d.vocab - v0 : piece;
     LaunchScope ls(kKVocabSimt, s);
     cudaError_t e = with_tile(d.n_rows, np, [&](auto tm, dim3 grid) {
-      vocab_slope_kernel<tm.value, T><<<grid, 256, 0, s>>>(d, h, w, p.targets, p.lse_in, p.d_logp, v0, np, slope);
+      vocab_slope_kernel<tm.value, T><<<grid, 256, 0, s>>>(d, operand(h, d.h_stride, 1, d.n_rows),
+                                                           operand(w + v0 * d.w_stride, d.w_stride, 1, np), p.targets,
+                                                           p.lse_in, p.d_logp, v0, np, slope);
     });
     if (e != cudaSuccess) return e;
     if (p.dh) {
-      const Operand<float> A{slope, np, 1, d.n_rows};
-      const Operand<T> B{w + v0 * d.w_stride, 1, d.w_stride, d.hidden};
-      const float* add = v0 > 0 ? dh32 : nullptr;
+      const auto A = operand(static_cast<const float*>(slope), np, 1, d.n_rows);
+      const auto B = operand(w + v0 * d.w_stride, 1, d.w_stride, d.hidden);
       e = with_tile(d.n_rows, d.hidden, [&](auto tm, dim3 grid) {
         ls.more_kernels(1);
-        if (v0 + np == d.vocab)
-          vocab_product_kernel<tm.value, float, T, T><<<grid, 256, 0, s>>>(A, B, np, add, static_cast<T*>(p.dh));
+        grid.z = (unsigned)((np + per - 1) / per);  // a shorter last piece has fewer
+        if (direct)
+          vocab_product_kernel<tm.value, float, T, T><<<grid, 256, 0, s>>>(A, B, np, per, false, static_cast<T*>(p.dh));
         else
-          vocab_product_kernel<tm.value, float, T, float><<<grid, 256, 0, s>>>(A, B, np, add, dh32);
+          vocab_product_kernel<tm.value, float, T, float><<<grid, 256, 0, s>>>(A, B, np, per, v0 > 0, sums);
       });
       if (e != cudaSuccess) return e;
     }
     if (p.dw) {
-      const Operand<float> A{slope, 1, np, np};
-      const Operand<T> B{h, 1, d.h_stride, d.hidden};
+      const auto A = operand(static_cast<const float*>(slope), 1, np, np);
+      const auto B = operand(h, 1, d.h_stride, d.hidden);
       e = with_tile(np, d.hidden, [&](auto tm, dim3 grid) {
         ls.more_kernels(1);
-        vocab_product_kernel<tm.value, float, T, T><<<grid, 256, 0, s>>>(A, B, d.n_rows, nullptr, static_cast<T*>(p.dw) + v0 * d.hidden);
+        vocab_product_kernel<tm.value, float, T, T><<<grid, 256, 0, s>>>(A, B, d.n_rows, d.n_rows, false, static_cast<T*>(p.dw) + v0 * d.hidden);
       });
       if (e != cudaSuccess) return e;
     }
+  }
+  if (p.dh && !direct) {
+    const int64_t n = d.n_rows * d.hidden;
+    LaunchScope ls(kKVocabReduce, s);
+    vocab_sum_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(splits, n, sums, static_cast<T*>(p.dh));
+    return cudaGetLastError();
   }
   return cudaSuccess;
 }
@@ -319,8 +412,9 @@ size_t vocab_simt_scratch(const ls_vocab_desc& d, bool with_grad) {
   const size_t n = (size_t)d.n_rows;
   size_t need = (size_t)((d.vocab + 63) / 64) * n * sizeof(float2) + n * sizeof(float);
   if (with_grad) {
+    const size_t splits = (size_t)((simt_piece(d) + simt_per_split(d) - 1) / simt_per_split(d));
     const size_t g = (round_up(n * (size_t)simt_piece(d), 64) +
-                      (simt_piece(d) < d.vocab ? n * (size_t)d.hidden : 0)) * sizeof(float);
+                      (splits > 1 || simt_piece(d) < d.vocab ? splits * n * (size_t)d.hidden : 0)) * sizeof(float);
     need = g > need ? g : need;
   }
   return round_up(need, 256);
