@@ -212,13 +212,17 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+_CODES = {}  # torch dtype -> LS_DTYPE_*
+
+
 def _dtype_code(dt) -> int:
-    import torch
-    if dt == torch.float32:
-        return LS_DTYPE_F32
-    if dt == torch.bfloat16:
-        return LS_DTYPE_BF16
-    raise ValueError(f"unsupported dtype {dt}")
+    if not _CODES:
+        import torch
+        _CODES.update({torch.float32: LS_DTYPE_F32, torch.bfloat16: LS_DTYPE_BF16})
+    code = _CODES.get(dt)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dt}")
+    return code
 
 
 def desc_for(hq, hkv, head_dim, page_size, dtype, softmax_scale=None) -> AttnDesc:
@@ -433,7 +437,7 @@ def _want(t, dtype, shape, name):
     """Shape, dtype and contiguity of a tensor the library takes by its address alone."""
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -442,9 +446,10 @@ def _want(t, dtype, shape, name):
 def _token_stride(t, name):
     """Elements from one token to the next of a [n, heads, d] tensor whose heads are contiguous."""
     n, heads, d = t.shape
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+    s = t.stride()
+    if (s[2] != 1 or (heads > 1 and s[1] != d)) and t.numel():
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(0) if n > 1 else heads * d
+    return s[0] if n > 1 else heads * d
 
 
 def kv_cache_from(k, v, k_exp=None, v_exp=None) -> KvCache:
@@ -468,28 +473,29 @@ def kv_cache_from(k, v, k_exp=None, v_exp=None) -> KvCache:
 
 def _cache_rows(cache, slots, k, v):
     import torch
-    _want(slots, torch.int64, (k.shape[0],), "slots")
-    want = (k.shape[0], cache.hkv, cache.head_dim)
-    if tuple(k.shape) != want or tuple(v.shape) != want or v.dtype != k.dtype:
+    n = k.shape[0]
+    _want(slots, torch.int64, (n,), "slots")
+    want = (n, cache.hkv, cache.head_dim)
+    if k.shape != want or v.shape != want or v.dtype != k.dtype:
         raise ValueError(f"k and v must be {want} of one dtype")
+    return n
 
 
 def ls_cache_write(cache, k, v, slots, ws=None, stream=None):
     """Token t's rows of k, v [n, Hkv, d] (any token stride) into slot slots[t] (see ls.h)."""
-    _cache_rows(cache, slots, k, v)
-    _check(lib().ls_cache_write(ctypes.byref(cache), _dtype_code(k.dtype), _ptr(k), _ptr(v),
-                                _token_stride(k, "k"), _token_stride(v, "v"), _ptr(slots),
-                                k.shape[0], _ptr(ws), 0 if ws is None else _nbytes(ws),
-                                _stream(stream)))
+    n = _cache_rows(cache, slots, k, v)
+    _check(lib().ls_cache_write(cache, _dtype_code(k.dtype), k.data_ptr(), v.data_ptr(),
+                                _token_stride(k, "k"), _token_stride(v, "v"), slots.data_ptr(),
+                                n, _ptr(ws), 0 if ws is None else _nbytes(ws), _stream(stream)))
 
 
 def ls_cache_read(cache, slots, k, v, ws=None, stream=None):
     """Slot slots[t] into token t of k, v [n, Hkv, d] (see ls.h)."""
-    _cache_rows(cache, slots, k, v)
-    _want(k, k.dtype, k.shape, "k")
-    _want(v, k.dtype, k.shape, "v")
-    _check(lib().ls_cache_read(ctypes.byref(cache), _ptr(slots), k.shape[0], _dtype_code(k.dtype),
-                               _ptr(k), _ptr(v), _ptr(ws), 0 if ws is None else _nbytes(ws),
+    n = _cache_rows(cache, slots, k, v)
+    if not (k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("k and v must be contiguous")
+    _check(lib().ls_cache_read(cache, slots.data_ptr(), n, _dtype_code(k.dtype), k.data_ptr(),
+                               v.data_ptr(), _ptr(ws), 0 if ws is None else _nbytes(ws),
                                _stream(stream)))
 
 
@@ -512,17 +518,18 @@ def ls_cached_attn(desc, cache, q, q_start, kv_len, page_table, o, lse, ws, stre
     """Attention of each sequence's new tokens over its pages (see ls.h)."""
     import torch
     shape = (desc.total_q, desc.hq, cache.head_dim)
-    if tuple(q.shape) != shape or _dtype_code(q.dtype) != desc.q_dtype or \
+    if q.shape != shape or _dtype_code(q.dtype) != desc.q_dtype or \
             _token_stride(q, "q") != desc.q_stride:
         raise ValueError(f"q is not the {shape} tensor of the desc")
     _want(o, torch.float32 if desc.o_dtype == LS_DTYPE_F32 else torch.bfloat16, shape, "o")
     _want(lse, torch.float32, shape[:2], "lse")
     _want(q_start, torch.int32, (desc.batch + 1,), "q_start")
     _want(kv_len, torch.int64, (desc.batch,), "kv_len")
-    _want(page_table, torch.int32, (desc.batch, page_table.shape[-1]), "page_table")
-    _check(lib().ls_cached_attn(ctypes.byref(desc), ctypes.byref(cache), _ptr(q), _ptr(q_start),
-                                _ptr(kv_len), _ptr(page_table), page_table.shape[1], _ptr(o),
-                                _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
+    pages = page_table.shape[-1]
+    _want(page_table, torch.int32, (desc.batch, pages), "page_table")
+    _check(lib().ls_cached_attn(desc, cache, q.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
+                                page_table.data_ptr(), pages, o.data_ptr(), lse.data_ptr(),
+                                ws.data_ptr(), _nbytes(ws), _stream(stream)))
 
 
 def _rows(t, name):
@@ -549,7 +556,7 @@ def ls_vocab_logprob_workspace_size(desc, with_grad=True) -> int:
 def _vocab_check(desc, h, w, targets, *rows):
     import torch
     for t, n, stride, name in ((h, desc.n_rows, desc.h_stride, "h"), (w, desc.vocab, desc.w_stride, "w")):
-        if tuple(t.shape) != (n, desc.hidden) or _dtype_code(t.dtype) != desc.dtype or \
+        if t.shape != (n, desc.hidden) or _dtype_code(t.dtype) != desc.dtype or \
                 _rows(t, name) != stride:
             raise ValueError(f"{name} is not the tensor of the desc")
     _want(targets, torch.int64, (desc.n_rows,), "targets")

@@ -82,6 +82,8 @@ __global__ void __launch_bounds__(128) cached_simt_kernel(const CachedParams p) 
   float* sk = sq + kSimtRows * d;        // [32][d + 4]
   float* sv = sk + kSimtKeys * ks;       // [32][d]
   const int b = blockIdx.z, kvh = blockIdx.y;
+  // the kernel that joins the parts may be launched; it waits for this one's end
+  asm volatile("griddepcontrol.launch_dependents;");
   const int part = blockIdx.x % p.ns, tile = blockIdx.x / p.ns;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Seq s = load_seq(p, b, tid == 0 && kvh == 0 && blockIdx.x == 0);
@@ -331,6 +333,8 @@ __global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 2) cached_mma_kernel
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int b = blockIdx.z, kvh = blockIdx.y;
+  // the kernel that joins the parts may be launched; it waits for this one's end
+  asm volatile("griddepcontrol.launch_dependents;");
   const int part = blockIdx.x % p.ns, tile = blockIdx.x / p.ns;
   const Seq s = load_seq(p, b, tid == 0 && kvh == 0 && blockIdx.x == 0);
   const int nrows = s.n * p.gq, r0 = tile * 8 * NT;

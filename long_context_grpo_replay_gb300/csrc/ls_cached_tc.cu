@@ -46,15 +46,19 @@ constexpr int kBM = 128, kBN = 128, kThreads = 640;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kBar = 8;  // barriers per ring (more than chunks), and tiles of key tables
 
-template <int D>
+// PAIR: two CTAs (cta_group::2) share a tile of 256 rows; each has half of
+// every K tile's keys and half of every V tile's columns.
+template <int D, bool PAIR>
 struct TcShape {
-  static constexpr int CW = D < 128 ? D : 128;         // columns of a chunk
-  static constexpr int NCH = D / CW;                   // chunks of a K or V tile
-  static constexpr int NC = D == 256 ? 4 : 5;          // chunks of the ring
-  static constexpr uint32_t kBox = kBN * 128;          // [128 keys x 64 columns] of 16-bit values
-  static constexpr uint32_t kChunk = kBN * CW * 2;
+  static constexpr int CW = PAIR || D < 128 ? D : 128;  // columns of a chunk (of both CTAs' for V)
+  static constexpr int NCH = D / CW;                    // chunks of a K or V tile
+  static constexpr int NC = PAIR ? (D == 256 ? 4 : 6) : D == 256 ? 4 : 5;  // chunks of the ring
+  static constexpr uint32_t kBoxV = kBN * 128;          // [128 keys x 64 columns] of 16-bit values
+  static constexpr uint32_t kBoxK = PAIR ? kBoxV / 2 : kBoxV;
+  static constexpr uint32_t kChunk = kBN * CW * (PAIR ? 1 : 2);
   static constexpr uint32_t kQ = kBM * D * 2;
   static constexpr uint32_t kSmem = kQ + NC * kChunk + 1024;
+  static_assert(!PAIR || D >= 128, "half of V's columns is at least a box");
   static_assert(kSmem + 20480 <= 227 * 1024, "shared memory, with 20 KB of tables");
   static_assert(NC < kBar, "a chunk's barriers are free before its slot is");
 };
@@ -98,6 +102,69 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Arrives on the barrier at this address in the pair's first CTA.
+__device__ __forceinline__ void arrive_first(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar)
+      : "memory");
+}
+// mbar_wait_short for a barrier that the other CTA arrives on too.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 131072;\n"
+      "W_%=:\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+      "sub.u32 n, n, 1;\n\tsetp.ne.and.u32 q, n, 0, !p;\n\t@q bra W_%=;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+template <bool PAIR>
+__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    mma_ss(d, a, b, idesc, acc);
+}
+template <bool PAIR>
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    mma_ts(d, a, b, idesc, acc);
+}
+// Arrives once the products so far are done: in a pair, in both CTAs.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    mma_commit(bar);
+}
+
+constexpr int log2_of(int x) { return x <= 1 ? 0 : 1 + log2_of(x / 2); }
+
 // Position of K_j / V_j in the order of use, and what stands at position u.
 __device__ __forceinline__ int unit_of_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int unit_of_v(int j, int n) { return j < n - 1 ? 2 * j + 2 : 2 * n - 1; }
@@ -113,9 +180,10 @@ __device__ __forceinline__ void unit_at(int u, int n, int& j, bool& is_v) {
   }
 }
 
-template <int D, bool E4>
+template <int D, bool E4, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedParams p) {
-  using L = TcShape<D>;
+  using L = TcShape<D, PAIR>;
+  constexpr int kCtas = PAIR ? 2 : 1;
   constexpr float kOff = E4 ? 11.f : 0.f;
   constexpr float kSlack = E4 ? 4.f : 8.f;
   // registers: 96 a thread at launch, 61,440 in all; 56 + 2 x 64 + 2 x 144 per
@@ -123,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
   constexpr int kRegsControl = 56, kRegsFill = 64, kRegsSoftmax = 144;
   static_assert(128 * (kRegsControl + 2 * kRegsFill + 2 * kRegsSoftmax) <= kThreads * 96, "register split");
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t bar_q, bar_full[kBar], bar_done[kBar], bar_rows[kBar], bar_tile[kBar], bar_s[2], bar_p[2], bar_o,
+  __shared__ uint64_t bar_q, bar_back, bar_full[kBar], bar_done[kBar], bar_rows[kBar], bar_tile[kBar], bar_s[2], bar_p[2], bar_o,
       bar_last, bar_pair[4], bar_drain;
   __shared__ uint32_t tmem_base_s;
   __shared__ int row_s[kBar][kBN];
@@ -134,27 +202,33 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u, sRing = sQ + L::kQ;
   const int b = blockIdx.z, kvh = blockIdx.y;
-  const int part = blockIdx.x % p.ns, tile = blockIdx.x / p.ns;
+  // the kernel that joins the parts may be launched; it waits for this one's end
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int rank = PAIR ? (int)cluster_rank() : 0;
+  const int part = (int)(blockIdx.x / kCtas) % p.ns, tile = (int)(blockIdx.x / kCtas) / p.ns;
   const Seq s = load_seq(p, b, tid == 0 && kvh == 0 && blockIdx.x == 0);
-  const int nrows = s.n * p.gq, r0 = tile * kBM;
-  if (r0 >= nrows) return;
-  const int r1 = r0 + kBM < nrows ? r0 + kBM : nrows;
+  const int nrows = s.n * p.gq, t0 = tile * kBM * kCtas, t1 = t0 + kBM * kCtas < nrows ? t0 + kBM * kCtas : nrows;
+  if (t0 >= nrows) return;  // both CTAs of a pair
+  // this CTA's rows (a pair's second may have none, and then only fills its share)
+  const int r0 = t0 + rank * kBM, r1 = r0 + kBM < nrows ? r0 + kBM : nrows;
   int kb, ke;
-  part_range(p, s, part, (r1 - 1) / p.gq, kb, ke);
+  part_range(p, s, part, (t1 - 1) / p.gq, kb, ke);
   const int ntiles = ke > kb ? (ke - kb + kBN - 1) / kBN : 0;
   const int nchunks = 2 * ntiles * L::NCH;
 
   if (tid == 0) {
-    mbar_init(smem_u32(&bar_q), 8);
+    // what the products wait for is counted in the pair's first CTA
+    mbar_init(smem_u32(&bar_q), 8 * kCtas);
+    mbar_init(smem_u32(&bar_back), 8);
     for (int i = 0; i < kBar; ++i) {
-      mbar_init(smem_u32(&bar_full[i]), 4);
+      mbar_init(smem_u32(&bar_full[i]), 4 * kCtas);
       mbar_init(smem_u32(&bar_done[i]), 1);
       mbar_init(smem_u32(&bar_rows[i]), 1);
       mbar_init(smem_u32(&bar_tile[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bar_s[i]), 1);
-      mbar_init(smem_u32(&bar_p[i]), 8);
+      mbar_init(smem_u32(&bar_p[i]), 8 * kCtas);
     }
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bar_pair[i]), 64);
     mbar_init(smem_u32(&bar_o), 1);
@@ -163,16 +237,28 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     fence_mbar_init();
   }
   if (warp == 2) {
-    tmem_alloc(smem_u32(&tmem_base_s), 512);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_base_s)) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      tmem_alloc(smem_u32(&tmem_base_s), 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();
   tc_fence_after();
   const uint32_t tbase = tmem_base_s;
   const uint32_t tS = tbase + 256;
   // where a role's wait gave up; it then leaves, and the others' waits end likewise
   int gave_up = 0;
+  auto arrive = [&](uint64_t& bar) {
+    if constexpr (PAIR)
+      arrive_first(smem_u32(&bar));
+    else
+      mbar_arrive(smem_u32(&bar));
+  };
   auto wait = [&](uint64_t& bar, int parity, int line) -> bool {  // whole warps
     if (mbar_wait_short_warp(smem_u32(&bar), parity)) return true;
     gave_up = line;
@@ -218,93 +304,101 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bar_rows[sl]));
       }
-    } else if (warp == 1 && lane == 0 && ntiles > 0) {
+    } else if (warp == 1 && lane == 0 && rank == 0 && ntiles > 0) {
       // ---------------------------------------------------------- products
       constexpr uint32_t kF16 = (1u << 7) | (1u << 10);  // the operands' type bits: bf16, cleared for f16
-      constexpr uint32_t idesc_s = idesc_bf16(kBM, kBN, false) & ~(E4 ? kF16 : 0u);
-      constexpr uint32_t idesc_o = idesc_bf16(kBM, L::CW, true) & ~(E4 ? kF16 : 0u);
+      constexpr uint32_t idesc_s = idesc_bf16(kBM * kCtas, kBN, false) & ~(E4 ? kF16 : 0u);
+      constexpr uint32_t idesc_o = idesc_bf16(kBM * kCtas, L::CW, true) & ~(E4 ? kF16 : 0u);
+      auto ready = [&](uint32_t bar, uint32_t parity) { return PAIR ? wait_cluster(bar, parity) : mbar_wait_short(bar, parity); };
       // descriptors count in 16 bytes: a tile's differ by constants
       const uint64_t qd = sdesc_sw128(sQ, 16, 1024);
-      bool ok = mbar_wait_short(smem_u32(&bar_q), 0);
+      bool ok = ready(smem_u32(&bar_q), 0);
       for (int j = -1; ok && j < ntiles; ++j) {
         // S_{j+1} goes to the buffer that held P_{j-1}, read by products issued before
         if (j + 1 < ntiles) {
 #pragma unroll 1
           for (int h = 0; h < L::NCH; ++h) {
             const int c = unit_of_k(j + 1) * L::NCH + h;
-            ok = mbar_wait_short(smem_u32(&bar_full[c % kBar]), (c / kBar) & 1);
+            ok = ready(smem_u32(&bar_full[c % kBar]), (c / kBar) & 1);
             if (!ok) break;
             tc_fence_after();
             const uint64_t kd = sdesc_sw128(sRing + (c % L::NC) * L::kChunk, 16, 1024);
             const uint64_t qh = qd + (h * 2 * (kBM * 128) >> 4);
 #pragma unroll
             for (int kk = 0; kk < L::CW / 16; ++kk)
-              mma_ss(tS + ((j + 1) & 1) * kBN, qh + (((kk >> 2) * (kBM * 128) + (kk & 3) * 32) >> 4),
-                     kd + (((kk >> 2) * L::kBox + (kk & 3) * 32) >> 4), idesc_s, (h > 0 || kk > 0) ? 1u : 0u);
-            if (h == L::NCH - 1) mma_commit(smem_u32(&bar_s[(j + 1) & 1]));
-            mma_commit(smem_u32(&bar_done[c % kBar]));
+              product_ss<PAIR>(tS + ((j + 1) & 1) * kBN, qh + (((kk >> 2) * (kBM * 128) + (kk & 3) * 32) >> 4),
+                     kd + (((kk >> 2) * L::kBoxK + (kk & 3) * 32) >> 4), idesc_s, (h > 0 || kk > 0) ? 1u : 0u);
+            if (h == L::NCH - 1) commit<PAIR>(smem_u32(&bar_s[(j + 1) & 1]));
+            commit<PAIR>(smem_u32(&bar_done[c % kBar]));
           }
         }
         if (!ok) gave_up = __LINE__;
         if (j < 0 || !ok) continue;
-        ok = mbar_wait_short(smem_u32(&bar_p[j & 1]), (j >> 1) & 1);
+        ok = ready(smem_u32(&bar_p[j & 1]), (j >> 1) & 1);
 #pragma unroll 1
         for (int h = 0; ok && h < L::NCH; ++h) {
           const int c = unit_of_v(j, ntiles) * L::NCH + h;
-          ok = mbar_wait_short(smem_u32(&bar_full[c % kBar]), (c / kBar) & 1);
+          ok = ready(smem_u32(&bar_full[c % kBar]), (c / kBar) & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t vd = sdesc_sw128(sRing + (c % L::NC) * L::kChunk, L::kBox, 1024);
+          const uint64_t vd = sdesc_sw128(sRing + (c % L::NC) * L::kChunk, L::kBoxV, 1024);
 #pragma unroll
           for (int kk = 0; kk < kBN / 16; ++kk)
-            mma_ts(tbase + h * L::CW, tS + (j & 1) * kBN + kk * 8, vd + (kk * 2048 >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(smem_u32(&bar_done[c % kBar]));
+            product_ts<PAIR>(tbase + h * L::CW, tS + (j & 1) * kBN + kk * 8, vd + (kk * 2048 >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+          commit<PAIR>(smem_u32(&bar_done[c % kBar]));
         }
         if (!ok) {
           gave_up = __LINE__;
           break;
         }
-        mma_commit(smem_u32(&bar_tile[j % kBar]));
-        mma_commit(smem_u32(&bar_o));
-        if (j == ntiles - 1) mma_commit(smem_u32(&bar_last));
+        commit<PAIR>(smem_u32(&bar_tile[j % kBar]));
+        commit<PAIR>(smem_u32(&bar_o));
+        if (j == ntiles - 1) commit<PAIR>(smem_u32(&bar_last));
       }
-      mma_commit(smem_u32(&bar_drain));
-      mbar_wait_short(smem_u32(&bar_drain), 0);
+      commit<PAIR>(smem_u32(&bar_drain));
+      ready(smem_u32(&bar_drain), 0);
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ chunks
     // four warps take the even chunks, four the odd ones
     fewer_registers<kRegsFill>();
     const int w = tid & 127, group = (warp - 4) >> 2;
-    const int sh = E4 ? 4 : 3;                                     // a thread's piece: 16 codes or 8 bf16 columns
-    constexpr int PR = L::CW / (E4 ? 16 : 8), RS = 128 / PR, NP = kBN / RS;
-    const int pc = w % PR, rr = w / PR;
+    // a thread's NP pieces of a chunk (16 codes or 8 bf16 columns each): piece
+    // pc of rows rr, rr + rs, ...  A pair's CTA has 64 keys of K and all its
+    // columns, 128 keys of V and half its columns.
+    constexpr int PC = E4 ? 16 : 8, ES = E4 ? 1 : 2;
+    constexpr int NP = (PAIR ? 64 * D : kBN * L::CW) / PC / 128;
+    constexpr int kLogK = log2_of(L::CW / PC), kLogV = PAIR ? kLogK - 1 : kLogK;
     int copied = -1;  // bf16: the chunk whose copies are under way
     auto filled = [&](int c) {
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bar_full[c % kBar]));
+      if (lane == 0) arrive(bar_full[c % kBar]);
     };
-    auto source = [&](int c, int& j) -> const char* {
-      bool is_v;
-      unit_at(c / L::NCH, ntiles, j, is_v);
-      return static_cast<const char*>(is_v ? p.c.v : p.c.k) + ((c % L::NCH) * L::CW + (pc << sh)) * (E4 ? 1 : 2);
-    };
-    // e4m3: a thread's pieces of its next chunk; each is loaded as soon as its
-    // place is converted, so that a group always has about a chunk in flight
-    uint4 v[E4 ? NP : 1];
+    int pc, rr, rs;      // of the chunk to load next
     const char* src = nullptr;
     const int* rows = nullptr;
+    auto source = [&](int c) -> bool {  // and waits for its rows
+      int j;
+      bool is_v;
+      unit_at(c / L::NCH, ntiles, j, is_v);
+      const int lg = is_v ? kLogV : kLogK;
+      pc = w & ((1 << lg) - 1), rr = w >> lg, rs = 128 >> lg;
+      src = static_cast<const char*>(is_v ? p.c.v : p.c.k) +
+            ((c % L::NCH) * L::CW + pc * PC + (PAIR && is_v ? rank * (D / 2) : 0)) * ES;
+      rows = &row_s[j % kBar][rr + (PAIR && !is_v ? rank * 64 : 0)];
+      return wait(bar_rows[j % kBar], (j / kBar) & 1, __LINE__);
+    };
+    // e4m3: the pieces of the next chunk; each is loaded as soon as its place is
+    // converted, so that a group always has about a chunk in flight
+    uint4 v[E4 ? NP : 1];
     auto fetch = [&](int i) {
-      const int row = rows[i * RS];
+      const int row = rows[i * rs];
       v[i] = row >= 0 ? load_once(reinterpret_cast<const uint4*>(src + (int64_t)row * D)) : make_uint4(0u, 0u, 0u, 0u);
     };
     bool ok = true;
     if (E4 && group < nchunks) {
-      int j;
-      src = source(group, j);
-      rows = &row_s[j % kBar][rr];
-      ok = wait(bar_rows[j % kBar], (j / kBar) & 1, __LINE__);
+      ok = source(group);
       if (ok)
 #pragma unroll
         for (int i = 0; i < NP; ++i) fetch(i);
@@ -312,20 +406,17 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
 #pragma unroll 1
     for (int c = group; ok && c < nchunks; c += 2) {
       const int next = E4 ? c + 2 : c;
-      int j = 0;
-      if (next < nchunks) {
-        src = source(next, j);
-        rows = &row_s[j % kBar][rr];
-        ok = wait(bar_rows[j % kBar], (j / kBar) & 1, __LINE__);
-        if (!ok) break;
-      }
-      if (c >= L::NC) ok = wait(bar_done[(c - L::NC) % kBar], ((c - L::NC) / kBar) & 1, __LINE__);
+      const int my_pc = pc, my_rr = rr, my_rs = rs;
+      if (next < nchunks) ok = source(next);
+      if (ok && c >= L::NC) ok = wait(bar_done[(c - L::NC) % kBar], ((c - L::NC) / kBar) & 1, __LINE__);
       if (!ok) break;
-      const uint32_t dst = sRing + (c % L::NC) * L::kChunk + (pc >> (E4 ? 2 : 3)) * L::kBox;
+      const uint32_t slot = sRing + (c % L::NC) * L::kChunk;
+      const uint32_t box = PAIR && (E4 ? my_rs : rs) == (128 >> kLogK) && kLogK != kLogV ? L::kBoxK : L::kBoxV;
       if constexpr (E4) {
-        // pieces 4-7 write their halves in the other order: the eight threads
-        // of a row then cover all banks with each store
-        const int flip = pc >> 2, at = (pc & 3) * 2;
+        // pieces 4-7 of eight write their halves in the other order: the eight
+        // threads of a row then cover all banks with each store
+        const uint32_t dst = slot + (my_pc >> 2) * box;
+        const int flip = (my_pc >> 2) & 1, at = (my_pc & 3) * 2;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           uint4 x, y;
@@ -333,17 +424,18 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
           codes_f16(v[i].y, x.z, x.w);
           codes_f16(v[i].z, y.x, y.y);
           codes_f16(v[i].w, y.z, y.w);
-          const int r = rr + i * RS;
+          const int r = my_rr + i * my_rs;
           st_shared_v4(dst + sw128_offset(r, at + flip), flip ? y : x);
           st_shared_v4(dst + sw128_offset(r, at + 1 - flip), flip ? x : y);
           if (next < nchunks) fetch(i);
         }
         filled(c);
       } else {
+        const uint32_t dst = slot + (pc >> 3) * box;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          const int r = rr + i * RS, row = rows[i * RS];
-          copy16(dst + sw128_offset(r, pc & 7), src + (int64_t)(row < 0 ? 0 : row) * D * 2, row >= 0);
+          const int row = rows[i * rs];
+          copy16(dst + sw128_offset(rr + i * rs, pc & 7), src + (int64_t)(row < 0 ? 0 : row) * D * 2, row >= 0);
         }
         copy_commit();
         if (copied >= 0) {
@@ -393,9 +485,12 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&bar_q));
+    if (lane == 0) {
+      mbar_arrive(smem_u32(&bar_back));
+      arrive(bar_q);
+    }
 
-    bool ok = wait(bar_q, 0, __LINE__);  // back_s of rows that other warps wrote
+    bool ok = wait(bar_back, 0, __LINE__);  // back_s of rows that other warps wrote
     const bool row_ok = r0 + i < r1;
     const int tok = row_ok ? (r0 + i) / p.gq : 0, hh = row_ok ? r0 + i - tok * p.gq : 0;
     // a row past the end has zero queries; seeing every key keeps its warp on the short path
@@ -532,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bar_p[bf]));
+      if (lane == 0) arrive(bar_p[bf]);
     }
     // ---- the row sums of both halves, then this half of O's columns
     float l = 0.f;
@@ -590,33 +685,53 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tbase, 512);
+    if constexpr (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tbase) : "memory");
+    else
+      tmem_dealloc(tbase, 512);
   }
 }
 
-template <int D, bool E4>
+template <int D, bool E4, bool PAIR>
 cudaError_t run_tc(const CachedParams& p, cudaStream_t s) {
-  using L = TcShape<D>;
-  auto* kernel = cached_tc_kernel<D, E4>;
+  using L = TcShape<D, PAIR>;
+  auto* kernel = cached_tc_kernel<D, E4, PAIR>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = ((int64_t)p.max_q * p.gq + kBM - 1) / kBM;
-  if (tiles * p.ns > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int64_t rows = (int64_t)p.max_q * p.gq, per = kBM * (PAIR ? 2 : 1);
+  const int64_t ctas = (rows + per - 1) / per * p.ns * (PAIR ? 2 : 1);
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
   LaunchScope ls(kKCachedTc, s);
-  kernel<<<dim3((unsigned)(tiles * p.ns), p.c.hkv, p.batch), kThreads, L::kSmem, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas, p.c.hkv, p.batch);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = PAIR ? 2 : 1, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace
 
+bool cached_tc_pairs(int64_t rows, int d) { return rows > kBM && d >= 128; }
+
 cudaError_t launch_cached_tc(const CachedParams& p, cudaStream_t s) {
-  const bool e4 = p.c.format == LS_CACHE_E4M3;
+  const bool e4 = p.c.format == LS_CACHE_E4M3, pair = cached_tc_pairs((int64_t)p.max_q * p.gq, p.c.head_dim);
   switch (p.c.head_dim) {
-    case 64: return e4 ? run_tc<64, true>(p, s) : run_tc<64, false>(p, s);
-    case 128: return e4 ? run_tc<128, true>(p, s) : run_tc<128, false>(p, s);
-    default: return e4 ? run_tc<256, true>(p, s) : run_tc<256, false>(p, s);
+    case 64: return e4 ? run_tc<64, true, false>(p, s) : run_tc<64, false, false>(p, s);
+    case 128:
+      if (pair) return e4 ? run_tc<128, true, true>(p, s) : run_tc<128, false, true>(p, s);
+      return e4 ? run_tc<128, true, false>(p, s) : run_tc<128, false, false>(p, s);
+    default:
+      if (pair) return e4 ? run_tc<256, true, true>(p, s) : run_tc<256, false, true>(p, s);
+      return e4 ? run_tc<256, true, false>(p, s) : run_tc<256, false, false>(p, s);
   }
 }
 

@@ -235,7 +235,9 @@ struct CachedParams {
 };
 cudaError_t launch_cached_simt(const CachedParams& p, cudaStream_t s);
 cudaError_t launch_cached_mma(const CachedParams& p, cudaStream_t s);
-cudaError_t launch_cached_tc(const CachedParams& p, cudaStream_t s);  // tiles of 128 rows
+// Tiles of 128 rows, or of 256 for a pair of CTAs where there are that many.
+cudaError_t launch_cached_tc(const CachedParams& p, cudaStream_t s);
+bool cached_tc_pairs(int64_t rows, int d);
 // Joins the ns parts (at most kCachedMaxParts) of every row.
 constexpr int kCachedMaxParts = 128;
 cudaError_t launch_cached_join(const CachedParams& p, cudaStream_t s);

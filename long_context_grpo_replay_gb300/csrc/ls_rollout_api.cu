@@ -126,7 +126,8 @@ CachedPlan plan_cached(const ls_cached_attn_desc& d, const ls_kv_cache& c) {
     per_quantum = quantum * key_bytes / 22e3, fixed = 6.0;
   } else {
     pl.route = kRouteTc;
-    tile = 128, quantum = 128;
+    const bool pair = cached_tc_pairs(rows, c.head_dim);
+    tile = pair ? 256 : 128, quantum = 128, ctas = pair ? sms / 2 : sms;
     per_quantum = 1.3 * c.head_dim / 256.0 + 0.2, fixed = 5.0;
   }
   const int64_t units = (int64_t)d.batch * c.hkv * ((rows + tile - 1) / tile);
