@@ -68,6 +68,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -110,11 +115,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrives on the barrier at this address in the pair's first CTA.
+// Arrives on the barrier at this address in the pair's first CTA.  What it
+// announces is in tensor memory (behind tcgen05.fence::before_thread_sync) or
+// in this CTA's shared memory behind each writer's fence.proxy.async; no data
+// of other kinds pass, so the arrival needs no fence of the cluster's scope,
+// which cost 1,200 cycles a tile.
 __device__ __forceinline__ void arrive_first(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar)
+      "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar)
       : "memory");
 }
 // mbar_wait_short for a barrier that the other CTA arrives on too.
@@ -186,9 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
   constexpr int kCtas = PAIR ? 2 : 1;
   constexpr float kOff = E4 ? 11.f : 0.f;
   constexpr float kSlack = E4 ? 4.f : 8.f;
-  // registers: 96 a thread at launch, 61,440 in all; 56 + 2 x 64 + 2 x 144 per
-  // group of 128 threads make 60,416, and no role spills
-  constexpr int kRegsControl = 56, kRegsFill = 64, kRegsSoftmax = 144;
+  // registers: 96 a thread at launch, 61,440 in all; 64 + 2 x 72 + 2 x 136 per
+  // group of 128 threads make all of them
+  constexpr int kRegsControl = 64, kRegsFill = 72, kRegsSoftmax = 136;
   static_assert(128 * (kRegsControl + 2 * kRegsFill + 2 * kRegsSoftmax) <= kThreads * 96, "register split");
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bar_q, bar_back, bar_full[kBar], bar_done[kBar], bar_rows[kBar], bar_tile[kBar], bar_s[2], bar_p[2], bar_o,
@@ -287,7 +296,10 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
           }
         }
         // the tables of tile j - kBar are used up once its O is done
-        if (j >= kBar && !wait(bar_tile[sl], (j / kBar - 1) & 1, __LINE__)) break;
+        if (j >= kBar && !mbar_wait_lazy_warp<200>(smem_u32(&bar_tile[sl]), (j / kBar - 1) & 1)) {
+          gave_up = __LINE__;
+          break;
+        }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           row_s[sl][x * 32 + lane] = row[x];
@@ -408,25 +420,31 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       const int next = E4 ? c + 2 : c;
       const int my_pc = pc, my_rr = rr, my_rs = rs;
       if (next < nchunks) ok = source(next);
-      if (ok && c >= L::NC) ok = wait(bar_done[(c - L::NC) % kBar], ((c - L::NC) / kBar) & 1, __LINE__);
+      if (ok && c >= L::NC && !mbar_wait_lazy_warp<20>(smem_u32(&bar_done[(c - L::NC) % kBar]), ((c - L::NC) / kBar) & 1)) {
+        gave_up = __LINE__;
+        ok = false;
+      }
       if (!ok) break;
       const uint32_t slot = sRing + (c % L::NC) * L::kChunk;
       const uint32_t box = PAIR && (E4 ? my_rs : rs) == (128 >> kLogK) && kLogK != kLogV ? L::kBoxK : L::kBoxV;
       if constexpr (E4) {
         // pieces 4-7 of eight write their halves in the other order: the eight
         // threads of a row then cover all banks with each store
-        const uint32_t dst = slot + (my_pc >> 2) * box;
-        const int flip = (my_pc >> 2) & 1, at = (my_pc & 3) * 2;
+        const bool flip = my_pc & 4;
+        const int at = (my_pc & 3) * 2;
+        // rs is a multiple of 8: a thread's rows have one place in the swizzle
+        uint32_t d0 = slot + (my_pc >> 2) * box + sw128_offset(my_rr, at + flip);
+        uint32_t d1 = slot + (my_pc >> 2) * box + sw128_offset(my_rr, at + 1 - flip);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           uint4 x, y;
-          codes_f16(v[i].x, x.x, x.y);
-          codes_f16(v[i].y, x.z, x.w);
-          codes_f16(v[i].z, y.x, y.y);
-          codes_f16(v[i].w, y.z, y.w);
-          const int r = my_rr + i * my_rs;
-          st_shared_v4(dst + sw128_offset(r, at + flip), flip ? y : x);
-          st_shared_v4(dst + sw128_offset(r, at + 1 - flip), flip ? x : y);
+          codes_f16(flip ? v[i].z : v[i].x, x.x, x.y);
+          codes_f16(flip ? v[i].w : v[i].y, x.z, x.w);
+          codes_f16(flip ? v[i].x : v[i].z, y.x, y.y);
+          codes_f16(flip ? v[i].y : v[i].w, y.z, y.w);
+          st_shared_v4(d0, x);
+          st_shared_v4(d1, y);
+          d0 += my_rs * 128, d1 += my_rs * 128;
           if (next < nchunks) fetch(i);
         }
         filled(c);
@@ -544,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       for (int c = 0; c < 32; ++c) {
         float a, bb;
         f2_split(y[c], a, bb);
-        mq[c & 3] = fmaxf(mq[c & 3], fmaxf(a, bb));
+        mq[c & 3] = max3f(mq[c & 3], a, bb);
       }
       float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
       // both halves of a row meet: they exchange their maxima, and each has

@@ -105,6 +105,17 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool mbar_wait_short_warp(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait_short(bar, parity));
 }
+// The same for a warp that runs well ahead of what it waits for: it sleeps
+// about `ns` between polls, which leaves the issue slots to the others.
+template <int NS>
+__device__ __forceinline__ bool mbar_wait_lazy_warp(uint32_t bar, uint32_t parity) {
+  bool ok = mbar_try_wait(bar, parity);
+  for (int n = 0; !__all_sync(0xffffffffu, ok) && n < 2000000000 / NS; ++n) {
+    __nanosleep(NS);
+    ok = mbar_try_wait(bar, parity);
+  }
+  return __all_sync(0xffffffffu, ok);
+}
 
 // ---------------------------------------------------------------- proxies
 __device__ __forceinline__ void fence_proxy_async_smem() {
