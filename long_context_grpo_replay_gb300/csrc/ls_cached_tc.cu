@@ -404,16 +404,23 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     // e4m3: the pieces of the next chunk; each is loaded as soon as its place is
     // converted, so that a group always has about a chunk in flight
     uint4 v[E4 ? NP : 1];
+    int at_row[E4 ? NP : 1];
     auto fetch = [&](int i) {
-      const int row = rows[i * rs];
+      const int row = at_row[i];
       v[i] = row >= 0 ? load_once(reinterpret_cast<const uint4*>(src + (int64_t)row * D)) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto find = [&] {  // the rows of all pieces at once, ahead of the loads that need them
+#pragma unroll
+      for (int i = 0; i < NP; ++i) at_row[i] = rows[i * rs];
     };
     bool ok = true;
     if (E4 && group < nchunks) {
       ok = source(group);
-      if (ok)
+      if (ok) {
+        find();
 #pragma unroll
         for (int i = 0; i < NP; ++i) fetch(i);
+      }
     }
 #pragma unroll 1
     for (int c = group; ok && c < nchunks; c += 2) {
@@ -430,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       if constexpr (E4) {
         // pieces 4-7 of eight write their halves in the other order: the eight
         // threads of a row then cover all banks with each store
+        if (next < nchunks) find();
         const bool flip = my_pc & 4;
         const int at = (my_pc & 3) * 2;
         // rs is a multiple of 8: a thread's rows have one place in the swizzle
@@ -515,7 +523,16 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     const int lim = row_ok ? row_limit(p, s, tok) : INT32_MAX;
     const float crow = E4 ? back_s[i] : p.scale_log2;
     float m_run = -CUDART_INF_F, l_run = 0.f;
-    for (int j = 0; ok && j < ntiles; ++j) {
+    if (r0 + q4 * 32 >= r1) {
+      // a warp without rows only keeps step: its rows of P may hold anything,
+      // since each row of O depends on its own row of P alone
+      for (int j = 0; ok && j < ntiles; ++j) {
+        ok = wait(bar_s[j & 1], (j >> 1) & 1, __LINE__);
+        if (ok && lane == 0) arrive(bar_p[j & 1]);
+      }
+    }
+    const bool busy = r0 + q4 * 32 < r1;
+    for (int j = 0; ok && busy && j < ntiles; ++j) {
       const int bf = j & 1, sl = j % kBar, key0 = kb + j * kBN + hf * 64;
       ok = wait(bar_rows[sl], (j / kBar) & 1, __LINE__) && wait(bar_s[bf], (j >> 1) & 1, __LINE__);
       if (!ok) break;
@@ -649,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     }
     // ---- the row sums of both halves, then this half of O's columns
     float l = 0.f;
-    if (ok && ntiles > 0) {
+    if (ok && ntiles > 0 && busy) {
       ok = wait(bar_last, 0, __LINE__);
       tc_fence_after();
       if (ok) {
@@ -665,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     for (int c0 = hf * (D / 2); c0 < (hf + 1) * (D / 2); c0 += 32) {
       uint32_t rr[32];
       __syncwarp();
-      if (ok && ntiles > 0) {
+      if (ok && ntiles > 0 && busy) {
         tmem_ld32(tbase + lanes + c0, rr);
         tmem_wait_ld_r(rr);
       } else {

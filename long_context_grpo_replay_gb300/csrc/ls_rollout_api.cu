@@ -128,7 +128,7 @@ CachedPlan plan_cached(const ls_cached_attn_desc& d, const ls_kv_cache& c) {
     pl.route = kRouteTc;
     const bool pair = cached_tc_pairs(rows, c.head_dim);
     tile = pair ? 256 : 128, quantum = 128, ctas = pair ? sms / 2 : sms;
-    per_quantum = 1.3 * c.head_dim / 256.0 + 0.2, fixed = 5.0;
+    per_quantum = (pair ? 1.6 : 2.6) + 0.4 * c.head_dim / 256.0, fixed = 8.0;
   }
   const int64_t units = (int64_t)d.batch * c.hkv * ((rows + tile - 1) / tile);
   const int64_t quanta = d.max_kv > 0 ? (d.max_kv + quantum - 1) / quantum : 1;
