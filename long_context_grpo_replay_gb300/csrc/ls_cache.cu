@@ -9,9 +9,10 @@
 // rounding of the code: x * 2^-e never rounds in float32 where the code is
 // not zero, and code * 2^e is a bf16 number.  The scale is one byte a row.
 //
-// Both kernels only move bytes: one group of d/8 lanes takes a token's K and
-// V row of one head, eight elements a lane, so that a row is read in 16-byte
-// (bf16) pieces, its maximum needs log2(d/8) shuffles, and no shared memory.
+// Both kernels only move bytes: a group of lanes takes a token's K and V row of
+// one head (writing: sixteen elements a lane, so that codes leave in 16-byte
+// pieces; reading: eight), all loads before the first use.  A row's maximum is
+// log2 of the group's lanes in shuffles; no shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -69,43 +70,88 @@ __device__ __forceinline__ int row_exp(uint32_t amax) {
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126..127
 
-template <int LANES>
-__device__ __forceinline__ void quant_row(const Row8& r, unsigned mask, bool first, uint8_t* dst,
-                                          int8_t* exp_dst) {
-  uint32_t m = 0;
+// Sixteen elements of a row as they lie in memory.
+template <typename T>
+struct Raw16 {
+  static constexpr int N = (int)sizeof(T);  // 16-byte pieces
+  uint4 w[N];
+};
+template <typename T>
+__device__ __forceinline__ Raw16<T> load16(const T* p) {
+  Raw16<T> r;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(r.x[i]) & 0x7fffffffu);
-#pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
-  const int e = row_exp(m);
-  uint2 code = make_uint2(0u, 0u);
-  if (e != kNanRow) {
-    const float s = pow2(-e);
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c[i] = __nv_cvt_float2_to_fp8x2(make_float2(r.x[2 * i] * s, r.x[2 * i + 1] * s), __NV_SATFINITE,
-                                      __NV_E4M3);
-    code = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-  }
-  *reinterpret_cast<uint2*>(dst) = code;
-  if (first) *exp_dst = (int8_t)e;
+  for (int i = 0; i < Raw16<T>::N; ++i) r.w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+  return r;
+}
+__device__ __forceinline__ float2 pair_of(const Raw16<float>& r, int i) {
+  const uint4 w = r.w[i >> 1];
+  return i & 1 ? make_float2(__uint_as_float(w.z), __uint_as_float(w.w)) : make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+}
+__device__ __forceinline__ float2 pair_of(const Raw16<__nv_bfloat16>& r, int i) {
+  const uint4 w = r.w[i >> 2];
+  const uint32_t u = (i & 3) == 0 ? w.x : (i & 3) == 1 ? w.y : (i & 3) == 2 ? w.z : w.w;
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
-// One group of D/8 lanes per (token, head): its K row and its V row.
+// Writes a group's row (LANES lanes of sixteen elements) into the cache.
+template <int FMT, int LANES, typename T>
+__device__ __forceinline__ void put_row(const Raw16<T>& r, unsigned mask, bool first, void* pool, int8_t* exps, int64_t dst,
+                                        int part) {
+  const int64_t at = dst * (LANES * 16) + part * 16;
+  if constexpr (FMT == LS_CACHE_E4M3) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 x = pair_of(r, i);
+      m = max(m, max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu));
+    }
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
+    const int e = row_exp(m);
+    uint32_t c[4] = {0u, 0u, 0u, 0u};
+    if (e != kNanRow) {
+      const float s = pow2(-e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 x = pair_of(r, i);
+        c[i >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x.x * s, x.y * s), __NV_SATFINITE, __NV_E4M3) << (16 * (i & 1));
+      }
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(pool) + at) = make_uint4(c[0], c[1], c[2], c[3]);
+    if (first) exps[dst] = (int8_t)e;
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      Row8 x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 y = pair_of(r, h * 4 + i);
+        x.x[2 * i] = y.x, x.x[2 * i + 1] = y.y;
+      }
+      if constexpr (FMT == LS_CACHE_BF16)
+        store8(static_cast<__nv_bfloat16*>(pool) + at + h * 8, x);
+      else
+        store8(static_cast<float*>(pool) + at + h * 8, x);
+    }
+  }
+}
+
+// One group of D/16 lanes per (token, head): its K row and its V row.
 template <typename T, int FMT, int D>
 __global__ void __launch_bounds__(256) cache_write_kernel(
     const ls_kv_cache c, const T* __restrict__ k, const T* __restrict__ v, int64_t k_stride,
     int64_t v_stride, const int64_t* __restrict__ slots, uint32_t n_rows, int64_t pool_slots, uint32_t* status) {
-  constexpr int LANES = D / 8;
+  constexpr int LANES = D / 16;
   const int lane = threadIdx.x & 31;
   const uint32_t row = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
   const int part = threadIdx.x % LANES;
-  const unsigned mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << (lane / LANES * LANES);
+  const unsigned mask = ((1u << LANES) - 1u) << (lane / LANES * LANES);
   if (row >= n_rows) return;  // a whole group leaves
   const uint32_t t = row / (uint32_t)c.hkv;
   const int head = (int)(row - t * c.hkv);
   const int64_t slot = __ldg(slots + t);
+  const Raw16<T> rk = load16(k + (int64_t)t * k_stride + head * D + part * 16);
+  const Raw16<T> rv = load16(v + (int64_t)t * v_stride + head * D + part * 16);
   if (slot < 0) return;
   if (slot >= pool_slots) {
     if (part == 0 && status) atomicOr(status, kStatusBadIndex);
@@ -113,18 +159,8 @@ __global__ void __launch_bounds__(256) cache_write_kernel(
   }
   const uint32_t page = (uint32_t)slot / (uint32_t)c.page_size;  // rows of the pool number below 2^31
   const int64_t dst = (int64_t)((page * c.hkv + head) * c.page_size + ((uint32_t)slot - page * c.page_size));
-  const Row8 rk = load8(k + (int64_t)t * k_stride + head * D + part * 8);
-  const Row8 rv = load8(v + (int64_t)t * v_stride + head * D + part * 8);
-  if constexpr (FMT == LS_CACHE_E4M3) {
-    quant_row<LANES>(rk, mask, part == 0, static_cast<uint8_t*>(c.k) + dst * D + part * 8, c.k_exp + dst);
-    quant_row<LANES>(rv, mask, part == 0, static_cast<uint8_t*>(c.v) + dst * D + part * 8, c.v_exp + dst);
-  } else if constexpr (FMT == LS_CACHE_BF16) {
-    store8(static_cast<__nv_bfloat16*>(c.k) + dst * D + part * 8, rk);
-    store8(static_cast<__nv_bfloat16*>(c.v) + dst * D + part * 8, rv);
-  } else {
-    store8(static_cast<float*>(c.k) + dst * D + part * 8, rk);
-    store8(static_cast<float*>(c.v) + dst * D + part * 8, rv);
-  }
+  put_row<FMT, LANES>(rk, mask, part == 0, c.k, c.k_exp, dst, part);
+  put_row<FMT, LANES>(rv, mask, part == 0, c.v, c.v_exp, dst, part);
 }
 
 __device__ __forceinline__ Row8 load_codes(const uint8_t* p, int e) {
@@ -198,7 +234,7 @@ cudaError_t launch_cache_write(const ls_kv_cache& c, int src_dtype, const void* 
                                int64_t k_stride, int64_t v_stride, const int64_t* slots,
                                int64_t n_tok, uint32_t* status, cudaStream_t s) {
   const int64_t rows = n_tok * c.hkv;
-  const int64_t blocks = (rows * (c.head_dim / 8) + 255) / 256;
+  const int64_t blocks = (rows * (c.head_dim / 16) + 255) / 256;
   if (rows > INT32_MAX) return cudaErrorInvalidConfiguration;
   const int64_t pool_slots = c.pool_pages * c.page_size;
   return with_shape(c, [&](auto fmt, auto d) {

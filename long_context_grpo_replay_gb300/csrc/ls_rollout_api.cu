@@ -117,33 +117,33 @@ CachedPlan plan_cached(const ls_cached_attn_desc& d, const ls_kv_cache& c) {
   double per_quantum, fixed;
   if (d.q_dtype != LS_DTYPE_BF16 || c.format == LS_CACHE_F32 || force_simt()) {
     pl.route = kRouteSimt;
-    tile = 16, quantum = 32;
-    per_quantum = 1.5, fixed = 2.0;
+    tile = 16, quantum = 32, ctas = 4 * sms;
+    per_quantum = 6.0, fixed = 6.0;
   } else if (rows <= cached_mma_rows(c.head_dim) || !device_is_sm100_family()) {
     pl.route = kRouteMma;
     tile = rows < 8 ? 8 : rows < cached_mma_rows(c.head_dim) ? rows : cached_mma_rows(c.head_dim);
     quantum = 128, ctas = 2 * sms;
-    per_quantum = quantum * key_bytes / 22e3, fixed = 6.0;
+    per_quantum = quantum * key_bytes / 22e3, fixed = 10.0;
   } else {
     pl.route = kRouteTc;
     const bool pair = cached_tc_pairs(rows, c.head_dim);
     tile = pair ? 256 : 128, quantum = 128, ctas = pair ? sms / 2 : sms;
-    per_quantum = (pair ? 1.6 : 2.6) + 0.4 * c.head_dim / 256.0, fixed = 8.0;
+    per_quantum = (pair ? 1.6 : 2.6) + 0.4 * c.head_dim / 256.0, fixed = pair ? 24.0 : 8.0;
   }
   const int64_t units = (int64_t)d.batch * c.hkv * ((rows + tile - 1) / tile);
   const int64_t quanta = d.max_kv > 0 ? (d.max_kv + quantum - 1) / quantum : 1;
   const size_t out_rows = (size_t)d.total_q * d.hq;
-  // Rounds of CTAs against the parts' float32 results, written
-  // and read once.  Several sequences end at different lengths: the model
-  // takes them for half as long as the longest on average, and asks for a few
-  // rounds, which even them out.
+  // Rounds of CTAs against the parts' float32 results, written and read once.
+  // Where everything runs at once the longest part counts.  Beyond that,
+  // sequences that end at different lengths, taken for half the longest on
+  // average, fill rounds unevenly.
   int64_t best = 1;
   double best_cost = 1e300;
   for (int64_t ns = 1; ns <= kCachedMaxParts && ns <= quanta && units > 0; ++ns) {
     const int64_t span = (quanta + ns - 1) / ns;
     if ((quanta + span - 1) / span != ns) continue;
-    double rounds = (double)((units * ns + ctas - 1) / ctas);
-    if (d.batch > 1) rounds = 0.5 * (double)(units * ns) / ctas + 1.0;
+    const double x = (double)(units * ns) / ctas;
+    const double rounds = x <= 1.0 ? 1.0 : d.batch > 1 ? 0.5 * x + 0.7 : std::ceil(x);
     const double cost = rounds * (span * per_quantum + fixed) +
                         (ns > 1 ? 3.0 + ns * (double)out_rows * c.head_dim * 8.0 / 6.0e6 : 0.0);
     if (cost < best_cost * 0.99) best_cost = cost, best = ns;
