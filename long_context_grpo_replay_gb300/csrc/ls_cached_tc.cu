@@ -15,9 +15,12 @@
 // registers, as f16 (exact: e4m3 is a subset).  Rows are found per key, so any
 // page size works; a missing key's row is zeros.
 //
-// e4m3 scales stay out of the products: y = x 2^ek + ev (base 2) is the score
-// and the exponent of the value row, w = 2^(y - m) the weight that multiplies
-// codes, l = sum w 2^-ev, o = sum w code / l.  Weights are f16, held 2^11 times
+// A key's scale goes into its f16 values, relative to the tile's largest: what
+// that rounds (rows 2^10 times smaller and more) is 2^-33 of the largest key's
+// part of a score, and the tile's scale multiplies the scores.  Value scales
+// stay out of the product, whose small rows may be the ones that count: y = x +
+// ev (base 2) is the score and the exponent of the value row, w = 2^(y - m) the
+// weight that multiplies codes, l = sum w 2^-ev, o = sum w code / l.  Weights are f16, held 2^11 times
 // their value and at most 2^15: 11 bits down to 2^-25 of the largest, so a sum
 // of many small weights beside a large one is not lost.  bf16: P in bf16, as in
 // the replay kernels.  Each row's maximum only moves when exceeded by 2^4
@@ -77,12 +80,21 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// Two pairs of e4m3 codes as two f16 pairs.
-__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+// Two pairs of e4m3 codes as two f16 pairs, times an f16 pair where SCALE.
+template <bool SCALE>
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi) {
+  if constexpr (!SCALE) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+    return;
+  }
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t"
+      "mul.rn.f16x2 %0, %0, %3;\n\tmul.rn.f16x2 %1, %1, %3;\n\t}"
+      : "=&r"(lo), "=&r"(hi)
+      : "r"(w), "r"(scale));
 }
 // 16 bytes that are read once: past L1.
 __device__ __forceinline__ uint4 load_once(const uint4* p) {
@@ -193,6 +205,7 @@ template <int D, bool E4, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedParams p) {
   using L = TcShape<D, PAIR>;
   constexpr int kCtas = PAIR ? 2 : 1;
+  constexpr bool FOLD = PAIR;
   constexpr float kOff = E4 ? 11.f : 0.f;
   constexpr float kSlack = E4 ? 4.f : 8.f;
   // registers: 96 a thread at launch, 61,440 in all; 64 + 2 x 72 + 2 x 136 per
@@ -204,7 +217,10 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       bar_last, bar_pair[4], bar_drain;
   __shared__ uint32_t tmem_base_s;
   __shared__ int row_s[kBar][kBN];
-  __shared__ __align__(16) float kf_s[E4 ? kBar : 1][kBN], ev_s[E4 ? kBar : 1][kBN], vi_s[E4 ? kBar : 1][kBN];
+  // a key's scale: FOLD: 2^ek over the tile's largest, twice in f16; else the float32
+  __shared__ __align__(16) uint32_t kh_s[E4 ? kBar : 1][kBN];
+  __shared__ float kmax_s[kBar];                 // 2^(the tile's largest ek)
+  __shared__ __align__(16) float ev_s[E4 ? kBar : 1][kBN], vi_s[E4 ? kBar : 1][kBN];
   __shared__ uint32_t there_s[kBar][4];
   __shared__ float top_s[2][2][kBM], back_s[kBM];
 
@@ -295,6 +311,13 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
             ev[x] = row[x] >= 0 ? __ldg(p.c.v_exp + row[x]) : 0;
           }
         }
+        int top = -127;  // the largest scale of the tile's keys
+        if constexpr (E4) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) top = row[x] >= 0 && ek[x] > top ? ek[x] : top;
+          top = __reduce_max_sync(0xffffffffu, top);
+          top = top == -127 ? 0 : top;
+        }
         // the tables of tile j - kBar are used up once its O is done
         if (j >= kBar && !mbar_wait_lazy_warp<200>(smem_u32(&bar_tile[sl]), (j / kBar - 1) & 1)) {
           gave_up = __LINE__;
@@ -306,13 +329,18 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
           const uint32_t m = __ballot_sync(0xffffffffu, row[x] >= 0);
           if (lane == 0) there_s[sl][x] = m;
           if constexpr (E4) {
-            kf_s[sl][x * 32 + lane] = exp_scale(ek[x]);
+            if constexpr (!FOLD) kh_s[sl][x * 32 + lane] = __float_as_uint(exp_scale(ek[x]));
+            // 2^(ek - top) in f16 bits: normal to 2^-14, subnormal to 2^-24, then 0
+            const int dk = top - ek[x];
+            const uint32_t h = ek[x] == -128 ? 0x7fffu : dk <= 14 ? (uint32_t)(15 - dk) << 10 : dk <= 24 ? 1u << (24 - dk) : 0u;
+            if constexpr (FOLD) kh_s[sl][x * 32 + lane] = h | h << 16;
             // a NaN row reaches only the rows that see it: through the exponent
             const bool nan = ev[x] == -128;
             ev_s[sl][x * 32 + lane] = nan ? exp_scale(-128) : (float)ev[x];
             vi_s[sl][x * 32 + lane] = nan ? 1.f : exp_scale(-ev[x]);
           }
         }
+        if (E4 && lane == 0) kmax_s[sl] = exp_scale(top);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bar_rows[sl]));
       }
@@ -390,12 +418,22 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     int pc, rr, rs;      // of the chunk to load next
     const char* src = nullptr;
     const int* rows = nullptr;
+    const uint32_t* scales = nullptr;  // e4m3: of the rows of a K chunk
     auto source = [&](int c) -> bool {  // and waits for its rows
       int j;
       bool is_v;
       unit_at(c / L::NCH, ntiles, j, is_v);
       const int lg = is_v ? kLogV : kLogK;
-      pc = w & ((1 << lg) - 1), rr = w >> lg, rs = 128 >> lg;
+      if constexpr (E4) {
+        // four threads on four pieces of a row, the next four on the next row's:
+        // their two 16-byte halves then fall on all banks (rows r and r + 1 differ
+        // in the swizzle's lowest bit)
+        pc = (w & 3) | ((w >> 3) & ((1 << (lg - 2)) - 1)) << 2, rr = (w >> 2 & 1) | (w >> (lg + 1)) << 1;
+        scales = is_v ? nullptr : &kh_s[j % kBar][rr + (PAIR ? rank * 64 : 0)];
+      } else {
+        pc = w & ((1 << lg) - 1), rr = w >> lg;
+      }
+      rs = 128 >> lg;
       src = static_cast<const char*>(is_v ? p.c.v : p.c.k) +
             ((c % L::NCH) * L::CW + pc * PC + (PAIR && is_v ? rank * (D / 2) : 0)) * ES;
       rows = &row_s[j % kBar][rr + (PAIR && !is_v ? rank * 64 : 0)];
@@ -405,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     // converted, so that a group always has about a chunk in flight
     uint4 v[E4 ? NP : 1];
     int at_row[E4 ? NP : 1];
+    uint32_t at_scale[E4 ? NP : 1] = {};
     auto fetch = [&](int i) {
       const int row = at_row[i];
       v[i] = row >= 0 ? load_once(reinterpret_cast<const uint4*>(src + (int64_t)row * D)) : make_uint4(0u, 0u, 0u, 0u);
@@ -412,6 +451,11 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     auto find = [&] {  // the rows of all pieces at once, ahead of the loads that need them
 #pragma unroll
       for (int i = 0; i < NP; ++i) at_row[i] = rows[i * rs];
+    };
+    // The scale of piece i, read for the chunk at hand before the next one's source.
+    auto find_scales = [&] {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) at_scale[i] = scales ? scales[i * rs] : 0x3c003c00u;  // 1
     };
     bool ok = true;
     if (E4 && group < nchunks) {
@@ -426,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     for (int c = group; ok && c < nchunks; c += 2) {
       const int next = E4 ? c + 2 : c;
       const int my_pc = pc, my_rr = rr, my_rs = rs;
+      if constexpr (E4 && FOLD) find_scales();
       if (next < nchunks) ok = source(next);
       if (ok && c >= L::NC && !mbar_wait_lazy_warp<20>(smem_u32(&bar_done[(c - L::NC) % kBar]), ((c - L::NC) / kBar) & 1)) {
         gave_up = __LINE__;
@@ -435,24 +480,20 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       const uint32_t slot = sRing + (c % L::NC) * L::kChunk;
       const uint32_t box = PAIR && (E4 ? my_rs : rs) == (128 >> kLogK) && kLogK != kLogV ? L::kBoxK : L::kBoxV;
       if constexpr (E4) {
-        // pieces 4-7 of eight write their halves in the other order: the eight
-        // threads of a row then cover all banks with each store
         if (next < nchunks) find();
-        const bool flip = my_pc & 4;
-        const int at = (my_pc & 3) * 2;
-        // rs is a multiple of 8: a thread's rows have one place in the swizzle
-        uint32_t d0 = slot + (my_pc >> 2) * box + sw128_offset(my_rr, at + flip);
-        uint32_t d1 = slot + (my_pc >> 2) * box + sw128_offset(my_rr, at + 1 - flip);
+        // rs is a multiple of 8: a thread's rows have one place in the swizzle,
+        // and a piece's halves stand in neighbouring places
+        uint32_t d0 = slot + (my_pc >> 2) * box + sw128_offset(my_rr, (my_pc & 3) * 2);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           uint4 x, y;
-          codes_f16(flip ? v[i].z : v[i].x, x.x, x.y);
-          codes_f16(flip ? v[i].w : v[i].y, x.z, x.w);
-          codes_f16(flip ? v[i].x : v[i].z, y.x, y.y);
-          codes_f16(flip ? v[i].y : v[i].w, y.z, y.w);
+          codes_f16<FOLD>(v[i].x, at_scale[i], x.x, x.y);
+          codes_f16<FOLD>(v[i].y, at_scale[i], x.z, x.w);
+          codes_f16<FOLD>(v[i].z, at_scale[i], y.x, y.y);
+          codes_f16<FOLD>(v[i].w, at_scale[i], y.z, y.w);
           st_shared_v4(d0, x);
-          st_shared_v4(d1, y);
-          d0 += my_rs * 128, d1 += my_rs * 128;
+          st_shared_v4(d0 ^ 16u, y);
+          d0 += my_rs * 128;
           if (next < nchunks) fetch(i);
         }
         filled(c);
@@ -552,14 +593,20 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
         }
       }
       if constexpr (E4) {
-        const uint64_t c2 = f2(crow, crow);
-        const ulonglong2* kf = reinterpret_cast<const ulonglong2*>(&kf_s[sl][hf * 64]);
+        const float ct = FOLD ? crow * kmax_s[sl] : crow;
+        const uint64_t c2 = f2(ct, ct);
+        const ulonglong2* kf = reinterpret_cast<const ulonglong2*>(&kh_s[sl][hf * 64]);
         const ulonglong2* ev = reinterpret_cast<const ulonglong2*>(&ev_s[sl][hf * 64]);
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const ulonglong2 f = kf[c], e = ev[c];
-          y[2 * c] = f2_fma(f2_mul(y[2 * c], f.x), c2, e.x);
-          y[2 * c + 1] = f2_fma(f2_mul(y[2 * c + 1], f.y), c2, e.y);
+          const ulonglong2 e = ev[c];
+          if constexpr (!FOLD) {
+            const ulonglong2 f = kf[c];
+            y[2 * c] = f2_mul(y[2 * c], f.x);
+            y[2 * c + 1] = f2_mul(y[2 * c + 1], f.y);
+          }
+          y[2 * c] = f2_fma(y[2 * c], c2, e.x);
+          y[2 * c + 1] = f2_fma(y[2 * c + 1], c2, e.y);
         }
       }
       // keys that exist and that this row sees
