@@ -11,7 +11,7 @@
 // into D in the product's epilogue, and uses D in two products.
 //
 // One tiled product serves all three: TILE x TILE outputs for 256 threads,
-// 16 of the inner dimension at a time through two shared buffers, 8 x 8 (or,
+// 16 or 32 of the inner dimension at a time through two shared buffers, 8 x 8 (or,
 // where 128 x 128 tiles would leave SMs idle, 4 x 4) outputs a thread; few
 // rows' dh is cut along the vocabulary into float32 sums.  Bound by FMA issue.
 #include <cuda_bf16.h>
@@ -24,7 +24,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kBK = 16;
+constexpr int kQuantum = 32;  // splits of the inner dimension are multiples of it
 
 __device__ __forceinline__ float ldf(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float ldf(const __nv_bfloat16* p) {
@@ -54,12 +54,14 @@ __device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
                      __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
 }
 
-// C tile = sum_k A(m, k) B(n, k) over k in [kb, ke).  The next 16 of k are
-// loaded into registers while this 16 is multiplied from shared memory.
+// C tile = sum_k A(m, k) B(n, k) over k in [kb, ke).  The next 16 (or 32) of k
+// are loaded into registers while these are multiplied from shared memory.
 template <int TM, typename TA, typename TB>
 struct Product {
   static constexpr int TILE = 16 * TM;
-  static constexpr int Q = TILE * kBK / 4 / 256;  // quads of an operand's tile per thread
+  // the small tile has 32 of the inner dimension at a time, for fewer barriers
+  static constexpr int kBK = TM == 4 ? 32 : 16, KQ = kBK / 4;
+  static constexpr int Q = TILE * KQ / 256;  // quads of an operand's tile per thread
   float a[2][kBK][TILE + 4], b[2][kBK][TILE + 4];
 
   template <typename T>
@@ -69,7 +71,7 @@ struct Product {
     for (int q = 0; q < Q; ++q) {
       const int x = threadIdx.x + q * 256;
       const bool kc = o.sk == 1;
-      const int64_t i = i0 + (kc ? x / 4 : x % (TILE / 4) * 4), k = k0 + (kc ? x % 4 * 4 : x / (TILE / 4));
+      const int64_t i = i0 + (kc ? x / KQ : x % (TILE / 4) * 4), k = k0 + (kc ? x % KQ * 4 : x / (TILE / 4));
       const T* src = o.p + i * o.si + k * o.sk;
       const int64_t left = kc ? ke - k : o.n - i;  // of the contiguous index
       const bool there = kc ? i < o.n : k < ke;
@@ -90,7 +92,7 @@ struct Product {
     for (int q = 0; q < Q; ++q) {
       const int x = threadIdx.x + q * 256;
       if (kc) {
-        const int i = x / 4, k = x % 4 * 4;
+        const int i = x / KQ, k = x % KQ * 4;
         dst[k][i] = r[q].x, dst[k + 1][i] = r[q].y, dst[k + 2][i] = r[q].z, dst[k + 3][i] = r[q].w;
       } else {
         *reinterpret_cast<float4*>(&dst[x / (TILE / 4)][x % (TILE / 4) * 4]) = r[q];
@@ -311,7 +313,7 @@ int simt_splits(const ls_vocab_desc& d) {
 }
 int64_t simt_per_split(const ls_vocab_desc& d) {
   const int64_t s = simt_splits(d);
-  return round_up((size_t)((simt_piece(d) + s - 1) / s), kBK);
+  return round_up((size_t)((simt_piece(d) + s - 1) / s), kQuantum);
 }
 
 template <typename F>
