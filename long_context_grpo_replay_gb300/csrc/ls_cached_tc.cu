@@ -296,14 +296,28 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       // ---------------------------------------------------------- key tables
       // two warps, every other tile each: a tile takes two loads that depend
       // on one another (page id, scales), about as long as its products
+      const int32_t* pages = p.page_table + (int64_t)b * p.pages_per_seq;
+      const uint32_t pool_pages = (uint32_t)p.c.pool_pages;  // a pool's rows number below 2^31
+      const uint32_t head_row = (uint32_t)kvh * p.c.page_size, page_rows = (uint32_t)p.c.hkv * p.c.page_size;
+#pragma unroll 1
       for (int j = warp >> 1; j < ntiles; j += 2) {
-        const int sl = j % kBar;
+        const int sl = j % kBar, key0 = kb + j * kBN + lane;
         int row[4], ek[4], ev[4];
+        bool bad = false;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int key = kb + j * kBN + x * 32 + lane;
-          row[x] = key < ke ? pool_row(p, b, kvh, key) : -1;
+          const uint32_t key = key0 + x * 32;
+          const uint32_t page = p.page_mul ? __umulhi(key, p.page_mul) >> p.page_shift : key;
+          row[x] = (int)key < ke ? __ldg(pages + page) : -1;  // the page's slot for now
+          ek[x] = (int)(key - page * p.c.page_size);
         }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const bool in = (uint32_t)row[x] < pool_pages;
+          bad |= !in && key0 + x * 32 < ke;
+          row[x] = in ? (int)(row[x] * page_rows + head_row + ek[x]) : -1;
+        }
+        if (bad) atomicOr(p.status, kStatusBadPage);
         if constexpr (E4) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) {

@@ -258,6 +258,9 @@ struct VocabParams {
   void* scratch;  // after the status header
   uint32_t* status;
 };
+// Rows that the forward takes at a time, so that its tiles' statistics stay
+// within 8 bytes x 65,536 rows per 256 (or 64) columns.
+constexpr int64_t kVocabRows = 65536;
 size_t vocab_simt_scratch(const ls_vocab_desc& d, bool with_grad);
 // lse and logp from n_tiles (maximum, sum) pairs per row, [tile][row], in base 2.
 cudaError_t launch_vocab_join(int n_tiles, const VocabParams& p, const float2* parts, const float* hit,

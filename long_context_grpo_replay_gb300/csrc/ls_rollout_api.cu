@@ -328,19 +328,23 @@ ls_status ls_vocab_logprob_fwd(const ls_vocab_desc* desc, const void* h, const v
     return fail(LS_ERR_INVALID_ARGUMENT, "buffers must be aligned to their elements");
   LS_CHECK(check_ws(ws, ws_bytes, vocab_need(*desc, false)));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  VocabParams p{};
-  p.d = *desc;
-  p.h = h;
-  p.w = w;
-  p.targets = targets;
-  p.logp = logp;
-  p.lse = lse;
-  p.scratch = static_cast<char*>(ws) + kWsHeader;
-  p.status = static_cast<uint32_t*>(ws);
-  if (vocab_tc_shape(*desc) && aligned(h, 16) && aligned(w, 16))
-    LS_CUDA(launch_vocab_tc_fwd(p, s), "vocabulary forward launch");
-  else
-    LS_CUDA(launch_vocab_simt_fwd(p, s), "vocabulary forward launch");
+  const bool tc = vocab_tc_shape(*desc) && aligned(h, 16) && aligned(w, 16);
+  for (int64_t r0 = 0; r0 < desc->n_rows; r0 += kVocabRows) {
+    VocabParams p{};
+    p.d = *desc;
+    p.d.n_rows = desc->n_rows - r0 < kVocabRows ? desc->n_rows - r0 : kVocabRows;
+    p.h = static_cast<const char*>(h) + r0 * desc->h_stride * (int64_t)esz;
+    p.w = w;
+    p.targets = targets + r0;
+    p.logp = logp + r0;
+    p.lse = lse + r0;
+    p.scratch = static_cast<char*>(ws) + kWsHeader;
+    p.status = static_cast<uint32_t*>(ws);
+    if (tc)
+      LS_CUDA(launch_vocab_tc_fwd(p, s), "vocabulary forward launch");
+    else
+      LS_CUDA(launch_vocab_simt_fwd(p, s), "vocabulary forward launch");
+  }
   return LS_OK;
 }
 

@@ -411,8 +411,8 @@ cudaError_t launch_vocab_join(int n_tiles, const VocabParams& p, const float2* p
 }
 
 size_t vocab_simt_scratch(const ls_vocab_desc& d, bool with_grad) {
-  const size_t n = (size_t)d.n_rows;
-  size_t need = (size_t)((d.vocab + 63) / 64) * n * sizeof(float2) + n * sizeof(float);
+  const size_t n = (size_t)d.n_rows, nf = (size_t)(d.n_rows < kVocabRows ? d.n_rows : kVocabRows);
+  size_t need = (size_t)((d.vocab + 63) / 64) * nf * sizeof(float2) + nf * sizeof(float);
   if (with_grad) {
     const size_t splits = (size_t)((simt_piece(d) + simt_per_split(d) - 1) / simt_per_split(d));
     const size_t g = (round_up(n * (size_t)simt_piece(d), 64) +

@@ -447,8 +447,8 @@ int dh_splits(const ls_vocab_desc& d) {
 }  // namespace
 
 size_t vocab_tc_scratch(const ls_vocab_desc& d, bool with_grad) {
-  const size_t n = (size_t)d.n_rows;
-  size_t need = (size_t)div_up(d.vocab, kTile) * n * sizeof(float2) + n * sizeof(float);
+  const size_t n = (size_t)d.n_rows, nf = (size_t)(d.n_rows < kVocabRows ? d.n_rows : kVocabRows);
+  size_t need = (size_t)div_up(d.vocab, kTile) * nf * sizeof(float2) + nf * sizeof(float);
   if (with_grad) {
     const int64_t piece = tc_piece(d);
     const int splits = dh_splits(d);

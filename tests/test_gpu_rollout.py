@@ -687,3 +687,12 @@ def test_vocab_stream_and_graph(dtype, dev):
     torch.cuda.synchronize()
     for a, b in zip(want[:4], (logp, lse, dh, dw)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_vocab_many_rows(dtype, dev):
+    """More rows than the forward takes at a time."""
+    h, w, t, dl = vocab_case(65536 + 300, 8, 40, dtype)
+    got = run_vocab(h, w, t, dl, dev)
+    ls.ls_read_device_status(got[4])
+    check_vocab(h, w, t, dl, 1.0, *got[:4])
