@@ -18,6 +18,7 @@
 #include <math_constants.h>
 
 #include "ls_internal.h"
+#include "ls_tc.cuh"
 
 namespace ls {
 namespace {
@@ -106,10 +107,13 @@ struct Product {
   __device__ __forceinline__ void run(const Operand<TA>& A, const Operand<TB>& B, int64_t m0, int64_t n0,
                                       int64_t kb, int64_t ke, float (&acc)[TM][TM]) {
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+    // outputs two by two along n: one packed instruction for two products, each
+    // rounded as fmaf rounds it
+    uint64_t sum[TM][TM / 2];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int j = 0; j < TM; ++j) acc[i][j] = 0.f;
+      for (int j = 0; j < TM / 2; ++j) sum[i][j] = 0ull;
     float4 ra[Q], rb[Q];
     load(ra, A, m0, kb, ke);
     load(rb, B, n0, kb, ke);
@@ -125,16 +129,19 @@ struct Product {
       }
 #pragma unroll
       for (int k = 0; k < kBK; ++k) {
-        float x[TM], y[TM];
+        float x[TM];
+        uint64_t y[TM / 2];
 #pragma unroll
         for (int i = 0; i < TM; i += 4) {
           *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(&a[buf][k][at(ty, i)]);
-          *reinterpret_cast<float4*>(y + i) = *reinterpret_cast<const float4*>(&b[buf][k][at(tx, i)]);
+          *reinterpret_cast<ulonglong2*>(y + i / 2) = *reinterpret_cast<const ulonglong2*>(&b[buf][k][at(tx, i)]);
         }
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < TM; ++i) {
+          const uint64_t xx = tc::f2(x[i], x[i]);
 #pragma unroll
-          for (int j = 0; j < TM; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+          for (int j = 0; j < TM / 2; ++j) sum[i][j] = tc::f2_fma(xx, y[j], sum[i][j]);
+        }
       }
       if (more) {
         store(a[buf ^ 1], ra, A.sk == 1);
@@ -142,13 +149,17 @@ struct Product {
       }
       __syncthreads();
     }
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TM / 2; ++j) tc::f2_split(sum[i][j], acc[i][2 * j], acc[i][2 * j + 1]);
   }
 };
 
 // Forward: per row of a 16*TM-column tile of the vocabulary, (maximum, sum of
 // 2^(x - maximum)) of the logits in base 2, and the target's logit.
 template <int TM, typename T>
-__global__ void __launch_bounds__(256) vocab_fwd_kernel(const ls_vocab_desc d, const Operand<T> A,
+__global__ void __launch_bounds__(256, 2) vocab_fwd_kernel(const ls_vocab_desc d, const Operand<T> A,
                                                         const Operand<T> B, const int64_t* targets, float2* parts, float* hit) {
   using P = Product<TM, T, T>;
   __shared__ __align__(16) P sm;
@@ -223,7 +234,7 @@ __global__ void __launch_bounds__(256) vocab_join_kernel(int n_tiles, int64_t n_
 
 // D of a piece of the vocabulary: columns v0 .. v0 + np of the logits.
 template <int TM, typename T>
-__global__ void __launch_bounds__(256) vocab_slope_kernel(const ls_vocab_desc d, const Operand<T> A,
+__global__ void __launch_bounds__(256, 2) vocab_slope_kernel(const ls_vocab_desc d, const Operand<T> A,
                                                           const Operand<T> B, const int64_t* targets, const float* lse,
                                                           const float* d_logp, int64_t v0, int64_t np, float* out) {
   using P = Product<TM, T, T>;
@@ -252,7 +263,7 @@ __global__ void __launch_bounds__(256) vocab_slope_kernel(const ls_vocab_desc d,
 
 // out[z][m][n] = A B^T over split z's share of the inner dimension (+ what is there), rounded to TO once.
 template <int TM, typename TA, typename TB, typename TO>
-__global__ void __launch_bounds__(256) vocab_product_kernel(Operand<TA> A, Operand<TB> B, int64_t K, int64_t per,
+__global__ void __launch_bounds__(256, 2) vocab_product_kernel(Operand<TA> A, Operand<TB> B, int64_t K, int64_t per,
                                                             bool add, TO* out) {
   using P = Product<TM, TA, TB>;
   __shared__ __align__(16) P sm;
@@ -297,18 +308,24 @@ int64_t simt_piece(const ls_vocab_desc& d) {
   return np < d.vocab ? np : d.vocab;
 }
 
-// Smaller tiles where 128 x 128 ones would not give every SM a CTA.
-bool small_tiles(int64_t m, int64_t n) {
-  return ((m + 127) / 128) * ((n + 127) / 128) < device_sms();
+// Smaller tiles where half of a 128-row tile would be empty, or 128 x 128 ones
+// would leave half the SMs idle (128 x 1024 x 16384: 128 large tiles 120 us,
+// 512 small ones 160).
+bool small_tiles(int64_t m, int64_t n, int64_t splits = 1) {
+  return m <= 64 || n <= 64 || ((m + 127) / 128) * ((n + 127) / 128) * splits < device_sms() / 2;
 }
 // Ways to cut dh's inner dimension, a piece of the vocabulary: where its tiles
 // leave SMs idle, two CTAs an SM, 256 columns each at least.
+int64_t most_splits(const ls_vocab_desc& d) {
+  const int64_t s = simt_piece(d) / 256;
+  return s < 1 ? 1 : s;
+}
+bool dh_small(const ls_vocab_desc& d) { return small_tiles(d.n_rows, d.hidden, most_splits(d)); }
 int simt_splits(const ls_vocab_desc& d) {
-  const int64_t tile = small_tiles(d.n_rows, d.hidden) ? 64 : 128;
+  const int64_t tile = dh_small(d) ? 64 : 128;
   const int64_t tiles = ((d.n_rows + tile - 1) / tile) * ((d.hidden + tile - 1) / tile);
   int64_t s = tiles > 0 ? 2 * device_sms() / tiles : 1;
-  const int64_t most = simt_piece(d) / 256;
-  s = s < most ? s : most;
+  s = s < most_splits(d) ? s : most_splits(d);
   return s < 1 ? 1 : (int)s;
 }
 int64_t simt_per_split(const ls_vocab_desc& d) {
@@ -317,8 +334,7 @@ int64_t simt_per_split(const ls_vocab_desc& d) {
 }
 
 template <typename F>
-cudaError_t with_tile(int64_t m, int64_t n, F f) {
-  const bool small = small_tiles(m, n);
+cudaError_t with_tile(int64_t m, int64_t n, bool small, F f) {
   const int64_t tile = small ? 64 : 128;
   const dim3 grid((unsigned)((m + tile - 1) / tile), (unsigned)((n + tile - 1) / tile));
   if ((n + tile - 1) / tile > 65535) return cudaErrorInvalidConfiguration;
@@ -340,7 +356,7 @@ cudaError_t simt_fwd(const VocabParams& p, cudaStream_t s) {
   int n_tiles = 0;
   {
     LaunchScope ls(kKVocabSimt, s);
-    const cudaError_t e = with_tile(d.n_rows, d.vocab, [&](auto tm, dim3 grid) {
+    const cudaError_t e = with_tile(d.n_rows, d.vocab, small_tiles(d.n_rows, d.vocab), [&](auto tm, dim3 grid) {
       n_tiles = (int)grid.y;
       vocab_fwd_kernel<tm.value, T><<<grid, 256, 0, s>>>(d, A, B, p.targets, parts, hit);
     });
@@ -362,7 +378,7 @@ cudaError_t simt_bwd(const VocabParams& p, cudaStream_t s) {
   for (int64_t v0 = 0; v0 < d.vocab; v0 += piece) {
     const int64_t np = d.vocab - v0 < piece ? d.vocab - v0 : piece;
     LaunchScope ls(kKVocabSimt, s);
-    cudaError_t e = with_tile(d.n_rows, np, [&](auto tm, dim3 grid) {
+    cudaError_t e = with_tile(d.n_rows, np, small_tiles(d.n_rows, np), [&](auto tm, dim3 grid) {
       vocab_slope_kernel<tm.value, T><<<grid, 256, 0, s>>>(d, operand(h, d.h_stride, 1, d.n_rows),
                                                            operand(w + v0 * d.w_stride, d.w_stride, 1, np), p.targets,
                                                            p.lse_in, p.d_logp, v0, np, slope);
@@ -371,7 +387,7 @@ cudaError_t simt_bwd(const VocabParams& p, cudaStream_t s) {
     if (p.dh) {
       const auto A = operand(static_cast<const float*>(slope), np, 1, d.n_rows);
       const auto B = operand(w + v0 * d.w_stride, 1, d.w_stride, d.hidden);
-      e = with_tile(d.n_rows, d.hidden, [&](auto tm, dim3 grid) {
+      e = with_tile(d.n_rows, d.hidden, dh_small(d), [&](auto tm, dim3 grid) {
         ls.more_kernels(1);
         grid.z = (unsigned)((np + per - 1) / per);  // a shorter last piece has fewer
         if (direct)
@@ -384,7 +400,7 @@ cudaError_t simt_bwd(const VocabParams& p, cudaStream_t s) {
     if (p.dw) {
       const auto A = operand(static_cast<const float*>(slope), 1, np, np);
       const auto B = operand(h, 1, d.h_stride, d.hidden);
-      e = with_tile(np, d.hidden, [&](auto tm, dim3 grid) {
+      e = with_tile(np, d.hidden, small_tiles(np, d.hidden), [&](auto tm, dim3 grid) {
         ls.more_kernels(1);
         vocab_product_kernel<tm.value, float, T, T><<<grid, 256, 0, s>>>(A, B, d.n_rows, d.n_rows, false, static_cast<T*>(p.dw) + v0 * d.hidden);
       });
