@@ -10,10 +10,11 @@
 // backward forms them again, a piece of the vocabulary at a time, turns them
 // into D in the product's epilogue, and uses D in two products.
 //
-// One tiled product serves all three: TILE x TILE outputs for 256 threads,
-// 16 or 32 of the inner dimension at a time through two shared buffers, 8 x 8 (or,
-// where 128 x 128 tiles would leave SMs idle, 4 x 4) outputs a thread; few
-// rows' dh is cut along the vocabulary into float32 sums.  Bound by FMA issue.
+// One tiled product serves all three: 128 x 128, 64 x 64 or 16 x 256 outputs for
+// 256 threads, 16 or 32 of the inner dimension at a time through two shared
+// buffers, 8 x 8 or 4 x 4 outputs a thread; few rows' dh is cut along the
+// vocabulary into float32 sums.  Bound by FMA issue (1024 x 2048 x 16384: 53.7
+// TFLOP/s, a library float32 product 58), for few rows by the weight's bytes.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -57,25 +58,28 @@ __device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
 
 // C tile = sum_k A(m, k) B(n, k) over k in [kb, ke).  The next 16 (or 32) of k
 // are loaded into registers while these are multiplied from shared memory.
-template <int TM, typename TA, typename TB>
+template <int TM, int TX, typename TA, typename TB>
 struct Product {
-  static constexpr int TILE = 16 * TM;
-  // the small tile has 32 of the inner dimension at a time, for fewer barriers
-  static constexpr int kBK = TM == 4 ? 32 : 16, KQ = kBK / 4;
-  static constexpr int Q = TILE * KQ / 256;  // quads of an operand's tile per thread
-  float a[2][kBK][TILE + 4], b[2][kBK][TILE + 4];
+  static constexpr int TILE_M = 256 / TX * TM, TILE_N = TX * TM;
+  // the 64 x 64 tile has 32 of the inner dimension at a time, for fewer barriers
+  static constexpr int kBK = TM == 4 && TX == 16 ? 32 : 16, KQ = kBK / 4;
+  float a[2][kBK][TILE_M + 4], b[2][kBK][TILE_N + 4];
 
-  template <typename T>
-  __device__ __forceinline__ static void load(float4 (&r)[Q], const Operand<T>& o, int64_t i0, int64_t k0, int64_t ke) {
+  template <int TILE>
+  static constexpr int quads() {  // of an operand's tile per thread
+    return TILE * KQ >= 256 ? TILE * KQ / 256 : 1;
+  }
+  template <int TILE, typename T>
+  __device__ __forceinline__ static void load(float4 (&r)[quads<TILE>()], const Operand<T>& o, int64_t i0, int64_t k0, int64_t ke) {
     // a quad lies along the contiguous index, and so do neighbouring threads
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
+    for (int q = 0; q < quads<TILE>(); ++q) {
       const int x = threadIdx.x + q * 256;
       const bool kc = o.sk == 1;
       const int64_t i = i0 + (kc ? x / KQ : x % (TILE / 4) * 4), k = k0 + (kc ? x % KQ * 4 : x / (TILE / 4));
       const T* src = o.p + i * o.si + k * o.sk;
       const int64_t left = kc ? ke - k : o.n - i;  // of the contiguous index
-      const bool there = kc ? i < o.n : k < ke;
+      const bool there = (kc ? i < o.n : k < ke) && x < TILE * KQ;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (there && left >= 4 && o.quads) {
         v = ld4(src);
@@ -88,10 +92,12 @@ struct Product {
       r[q] = v;
     }
   }
-  __device__ __forceinline__ static void store(float (&dst)[kBK][TILE + 4], const float4 (&r)[Q], bool kc) {
+  template <int TILE>
+  __device__ __forceinline__ static void store(float (&dst)[kBK][TILE + 4], const float4 (&r)[quads<TILE>()], bool kc) {
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
+    for (int q = 0; q < quads<TILE>(); ++q) {
       const int x = threadIdx.x + q * 256;
+      if (x >= TILE * KQ) break;
       if (kc) {
         const int i = x / KQ, k = x % KQ * 4;
         dst[k][i] = r[q].x, dst[k + 1][i] = r[q].y, dst[k + 2][i] = r[q].z, dst[k + 3][i] = r[q].w;
@@ -101,12 +107,12 @@ struct Product {
     }
   }
 
-  // acc[i][j]: rows (i / 4) * TILE/2 + ty * 4 + i % 4 (TM 8) or ty * 4 + i (TM 4)
-  __device__ __forceinline__ static int at(int t, int i) { return TM == 8 ? (i / 4) * 64 + t * 4 + (i & 3) : t * 4 + i; }
+  // Row (column) of output i (j) of the thread's: four together, TM 8 in two groups half a tile apart.
+  __device__ __forceinline__ static int at_m(int i) { return i / 4 * (TILE_M / 2) + threadIdx.x / TX * 4 + (i & 3); }
+  __device__ __forceinline__ static int at_n(int j) { return j / 4 * (TILE_N / 2) + threadIdx.x % TX * 4 + (j & 3); }
 
   __device__ __forceinline__ void run(const Operand<TA>& A, const Operand<TB>& B, int64_t m0, int64_t n0,
                                       int64_t kb, int64_t ke, float (&acc)[TM][TM]) {
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
     // outputs two by two along n: one packed instruction for two products, each
     // rounded as fmaf rounds it
     uint64_t sum[TM][TM / 2];
@@ -114,18 +120,18 @@ struct Product {
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TM / 2; ++j) sum[i][j] = 0ull;
-    float4 ra[Q], rb[Q];
-    load(ra, A, m0, kb, ke);
-    load(rb, B, n0, kb, ke);
-    store(a[0], ra, A.sk == 1);
-    store(b[0], rb, B.sk == 1);
+    float4 ra[quads<TILE_M>()], rb[quads<TILE_N>()];
+    load<TILE_M>(ra, A, m0, kb, ke);
+    load<TILE_N>(rb, B, n0, kb, ke);
+    store<TILE_M>(a[0], ra, A.sk == 1);
+    store<TILE_N>(b[0], rb, B.sk == 1);
     __syncthreads();
     int buf = 0;
     for (int64_t k0 = kb; k0 < ke; k0 += kBK, buf ^= 1) {
       const bool more = k0 + kBK < ke;
       if (more) {
-        load(ra, A, m0, k0 + kBK, ke);
-        load(rb, B, n0, k0 + kBK, ke);
+        load<TILE_M>(ra, A, m0, k0 + kBK, ke);
+        load<TILE_N>(rb, B, n0, k0 + kBK, ke);
       }
 #pragma unroll
       for (int k = 0; k < kBK; ++k) {
@@ -133,8 +139,8 @@ struct Product {
         uint64_t y[TM / 2];
 #pragma unroll
         for (int i = 0; i < TM; i += 4) {
-          *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(&a[buf][k][at(ty, i)]);
-          *reinterpret_cast<ulonglong2*>(y + i / 2) = *reinterpret_cast<const ulonglong2*>(&b[buf][k][at(tx, i)]);
+          *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(&a[buf][k][at_m(i)]);
+          *reinterpret_cast<ulonglong2*>(y + i / 2) = *reinterpret_cast<const ulonglong2*>(&b[buf][k][at_n(i)]);
         }
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
@@ -144,8 +150,8 @@ struct Product {
         }
       }
       if (more) {
-        store(a[buf ^ 1], ra, A.sk == 1);
-        store(b[buf ^ 1], rb, B.sk == 1);
+        store<TILE_M>(a[buf ^ 1], ra, A.sk == 1);
+        store<TILE_N>(b[buf ^ 1], rb, B.sk == 1);
       }
       __syncthreads();
     }
@@ -156,40 +162,41 @@ struct Product {
   }
 };
 
-// Forward: per row of a 16*TM-column tile of the vocabulary, (maximum, sum of
+// Forward: per row and the columns of one warp, (maximum, sum of
 // 2^(x - maximum)) of the logits in base 2, and the target's logit.
-template <int TM, typename T>
+template <int TM, int TX, typename T>
 __global__ void __launch_bounds__(256, 2) vocab_fwd_kernel(const ls_vocab_desc d, const Operand<T> A,
                                                         const Operand<T> B, const int64_t* targets, float2* parts, float* hit) {
-  using P = Product<TM, T, T>;
+  using P = Product<TM, TX, T, T>;
+  constexpr int kLanes = TX < 32 ? TX : 32;  // of a warp that share a row; a row's warps leave statistics of their own
   __shared__ __align__(16) P sm;
-  const int64_t m0 = (int64_t)blockIdx.x * P::TILE, n0 = (int64_t)blockIdx.y * P::TILE;
+  const int64_t m0 = (int64_t)blockIdx.x * P::TILE_M, n0 = (int64_t)blockIdx.y * P::TILE_N;
   float acc[TM][TM];
   sm.run(A, B, m0, n0, 0, d.hidden, acc);
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int64_t row = m0 + P::at(ty, i);
+    const int64_t row = m0 + P::at_m(i);
     const int64_t target = row < d.n_rows ? __ldg(targets + row) : -1;
     float top = -CUDART_INF_F;
     float y[TM];
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-      const int64_t v = n0 + P::at(tx, j);
+      const int64_t v = n0 + P::at_n(j);
       const float x = acc[i][j] * d.logit_scale;
       if (v == target && v < d.vocab) hit[row] = x;
       y[j] = v < d.vocab ? x * kLog2e : -CUDART_INF_F;
       top = fmaxf(top, y[j]);
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float ref = top == -CUDART_INF_F ? 0.f : top;
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < TM; ++j) sum += exp2f(y[j] - ref);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (tx == 0 && row < d.n_rows) parts[(int64_t)blockIdx.y * d.n_rows + row] = make_float2(top, sum);
+    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (threadIdx.x % kLanes == 0 && row < d.n_rows)
+      parts[((int64_t)blockIdx.y * (TX / kLanes) + threadIdx.x % TX / kLanes) * d.n_rows + row] = make_float2(top, sum);
   }
 }
 
@@ -233,26 +240,25 @@ __global__ void __launch_bounds__(256) vocab_join_kernel(int n_tiles, int64_t n_
 }
 
 // D of a piece of the vocabulary: columns v0 .. v0 + np of the logits.
-template <int TM, typename T>
+template <int TM, int TX, typename T>
 __global__ void __launch_bounds__(256, 2) vocab_slope_kernel(const ls_vocab_desc d, const Operand<T> A,
                                                           const Operand<T> B, const int64_t* targets, const float* lse,
                                                           const float* d_logp, int64_t v0, int64_t np, float* out) {
-  using P = Product<TM, T, T>;
+  using P = Product<TM, TX, T, T>;
   __shared__ __align__(16) P sm;
-  const int64_t m0 = (int64_t)blockIdx.x * P::TILE, n0 = (int64_t)blockIdx.y * P::TILE;
+  const int64_t m0 = (int64_t)blockIdx.x * P::TILE_M, n0 = (int64_t)blockIdx.y * P::TILE_N;
   float acc[TM][TM];
   sm.run(A, B, m0, n0, 0, d.hidden, acc);
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int64_t row = m0 + P::at(ty, i);
+    const int64_t row = m0 + P::at_m(i);
     if (row >= d.n_rows) continue;
     const int64_t target = __ldg(targets + row);
     const float c = target >= 0 && target < d.vocab ? __ldg(d_logp + row) * d.logit_scale : 0.f;
     const float z = __ldg(lse + row);
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-      const int64_t n = n0 + P::at(tx, j);
+      const int64_t n = n0 + P::at_n(j);
       if (n >= np) continue;
       const float p = exp2f((acc[i][j] * d.logit_scale - z) * kLog2e);
       // a row that takes no part has no gradient even where its logits are not finite
@@ -262,24 +268,23 @@ __global__ void __launch_bounds__(256, 2) vocab_slope_kernel(const ls_vocab_desc
 }
 
 // out[z][m][n] = A B^T over split z's share of the inner dimension (+ what is there), rounded to TO once.
-template <int TM, typename TA, typename TB, typename TO>
+template <int TM, int TX, typename TA, typename TB, typename TO>
 __global__ void __launch_bounds__(256, 2) vocab_product_kernel(Operand<TA> A, Operand<TB> B, int64_t K, int64_t per,
                                                             bool add, TO* out) {
-  using P = Product<TM, TA, TB>;
+  using P = Product<TM, TX, TA, TB>;
   __shared__ __align__(16) P sm;
-  const int64_t m0 = (int64_t)blockIdx.x * P::TILE, n0 = (int64_t)blockIdx.y * P::TILE;
+  const int64_t m0 = (int64_t)blockIdx.x * P::TILE_M, n0 = (int64_t)blockIdx.y * P::TILE_N;
   float acc[TM][TM];
   const int64_t kb = blockIdx.z * per, ke = kb + per < K ? kb + per : K;
   out += (int64_t)blockIdx.z * A.n * B.n;
   sm.run(A, B, m0, n0, kb, ke, acc);
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int64_t m = m0 + P::at(ty, i);
+    const int64_t m = m0 + P::at_m(i);
     if (m >= A.n) continue;
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-      const int64_t n = n0 + P::at(tx, j);
+      const int64_t n = n0 + P::at_n(j);
       if (n >= B.n) continue;
       float v = acc[i][j];
       if constexpr (sizeof(TO) == 4)
@@ -308,11 +313,20 @@ int64_t simt_piece(const ls_vocab_desc& d) {
   return np < d.vocab ? np : d.vocab;
 }
 
-// Smaller tiles where half of a 128-row tile would be empty, or 128 x 128 ones
-// would leave half the SMs idle (128 x 1024 x 16384: 128 large tiles 120 us,
-// 512 small ones 160).
-bool small_tiles(int64_t m, int64_t n, int64_t splits = 1) {
-  return m <= 64 || n <= 64 || ((m + 127) / 128) * ((n + 127) / 128) * splits < device_sms() / 2;
+// The product's tile: 16 x 256 for up to 16 rows (bound by the weight's bytes if
+// the empty rows of a larger tile are left out), 64 x 64 where half of a 128-row
+// tile would be empty or 128 x 128 ones would leave half the SMs idle (128 x 1024
+// x 16384: 128 large tiles 120 us, 512 small ones 160), else 128 x 128.
+enum Tile { kWide, kSmall, kLarge };
+int tile_m(Tile t) { return t == kWide ? 16 : t == kSmall ? 64 : 128; }
+int tile_n(Tile t) { return t == kWide ? 256 : t == kSmall ? 64 : 128; }
+int64_t tiles_of(Tile t, int64_t m, int64_t n) {
+  return ((m + tile_m(t) - 1) / tile_m(t)) * ((n + tile_n(t) - 1) / tile_n(t));
+}
+Tile pick_tile(int64_t m, int64_t n, int64_t splits = 1) {
+  if (m <= 16) return kWide;
+  if (m <= 64 || n <= 64 || tiles_of(kLarge, m, n) * splits < device_sms() / 2) return kSmall;
+  return kLarge;
 }
 // Ways to cut dh's inner dimension, a piece of the vocabulary: where its tiles
 // leave SMs idle, two CTAs an SM, 256 columns each at least.
@@ -320,10 +334,9 @@ int64_t most_splits(const ls_vocab_desc& d) {
   const int64_t s = simt_piece(d) / 256;
   return s < 1 ? 1 : s;
 }
-bool dh_small(const ls_vocab_desc& d) { return small_tiles(d.n_rows, d.hidden, most_splits(d)); }
+Tile dh_tile(const ls_vocab_desc& d) { return pick_tile(d.n_rows, d.hidden, most_splits(d)); }
 int simt_splits(const ls_vocab_desc& d) {
-  const int64_t tile = dh_small(d) ? 64 : 128;
-  const int64_t tiles = ((d.n_rows + tile - 1) / tile) * ((d.hidden + tile - 1) / tile);
+  const int64_t tiles = tiles_of(dh_tile(d), d.n_rows, d.hidden);
   int64_t s = tiles > 0 ? 2 * device_sms() / tiles : 1;
   s = s < most_splits(d) ? s : most_splits(d);
   return s < 1 ? 1 : (int)s;
@@ -334,16 +347,21 @@ int64_t simt_per_split(const ls_vocab_desc& d) {
 }
 
 template <typename F>
-cudaError_t with_tile(int64_t m, int64_t n, bool small, F f) {
-  const int64_t tile = small ? 64 : 128;
-  const dim3 grid((unsigned)((m + tile - 1) / tile), (unsigned)((n + tile - 1) / tile));
-  if ((n + tile - 1) / tile > 65535) return cudaErrorInvalidConfiguration;
-  if (small)
-    f(std::integral_constant<int, 4>{}, grid);
+cudaError_t with_tile(int64_t m, int64_t n, Tile t, F f) {
+  const dim3 grid((unsigned)((m + tile_m(t) - 1) / tile_m(t)), (unsigned)((n + tile_n(t) - 1) / tile_n(t)));
+  if ((n + tile_n(t) - 1) / tile_n(t) > 65535) return cudaErrorInvalidConfiguration;
+  using std::integral_constant;
+  if (t == kWide)
+    f(integral_constant<int, 4>{}, integral_constant<int, 64>{}, grid);
+  else if (t == kSmall)
+    f(integral_constant<int, 4>{}, integral_constant<int, 16>{}, grid);
   else
-    f(std::integral_constant<int, 8>{}, grid);
+    f(integral_constant<int, 8>{}, integral_constant<int, 16>{}, grid);
   return cudaGetLastError();
 }
+
+// Statistics per row: one for 64 columns, or two for 256.
+int64_t most_parts(const ls_vocab_desc& d) { return (d.vocab + 63) / 64 + 1; }
 
 template <typename T>
 cudaError_t simt_fwd(const VocabParams& p, cudaStream_t s) {
@@ -351,14 +369,14 @@ cudaError_t simt_fwd(const VocabParams& p, cudaStream_t s) {
   const auto A = operand(static_cast<const T*>(p.h), d.h_stride, 1, d.n_rows);
   const auto B = operand(static_cast<const T*>(p.w), d.w_stride, 1, d.vocab);
   float2* parts = static_cast<float2*>(p.scratch);
-  const int64_t tiles64 = (d.vocab + 63) / 64;
-  float* hit = reinterpret_cast<float*>(parts + tiles64 * d.n_rows);
+  const int64_t n_parts = most_parts(d);
+  float* hit = reinterpret_cast<float*>(parts + n_parts * d.n_rows);
   int n_tiles = 0;
   {
     LaunchScope ls(kKVocabSimt, s);
-    const cudaError_t e = with_tile(d.n_rows, d.vocab, small_tiles(d.n_rows, d.vocab), [&](auto tm, dim3 grid) {
-      n_tiles = (int)grid.y;
-      vocab_fwd_kernel<tm.value, T><<<grid, 256, 0, s>>>(d, A, B, p.targets, parts, hit);
+    const cudaError_t e = with_tile(d.n_rows, d.vocab, pick_tile(d.n_rows, d.vocab), [&](auto tm, auto tx, dim3 grid) {
+      n_tiles = (int)grid.y * (tx.value < 32 ? 1 : tx.value / 32);
+      vocab_fwd_kernel<tm.value, tx.value, T><<<grid, 256, 0, s>>>(d, A, B, p.targets, parts, hit);
     });
     if (e != cudaSuccess) return e;
   }
@@ -378,8 +396,8 @@ cudaError_t simt_bwd(const VocabParams& p, cudaStream_t s) {
   for (int64_t v0 = 0; v0 < d.vocab; v0 += piece) {
     const int64_t np = d.vocab - v0 < piece ? d.vocab - v0 : piece;
     LaunchScope ls(kKVocabSimt, s);
-    cudaError_t e = with_tile(d.n_rows, np, small_tiles(d.n_rows, np), [&](auto tm, dim3 grid) {
-      vocab_slope_kernel<tm.value, T><<<grid, 256, 0, s>>>(d, operand(h, d.h_stride, 1, d.n_rows),
+    cudaError_t e = with_tile(d.n_rows, np, pick_tile(d.n_rows, np), [&](auto tm, auto tx, dim3 grid) {
+      vocab_slope_kernel<tm.value, tx.value, T><<<grid, 256, 0, s>>>(d, operand(h, d.h_stride, 1, d.n_rows),
                                                            operand(w + v0 * d.w_stride, d.w_stride, 1, np), p.targets,
                                                            p.lse_in, p.d_logp, v0, np, slope);
     });
@@ -387,22 +405,22 @@ cudaError_t simt_bwd(const VocabParams& p, cudaStream_t s) {
     if (p.dh) {
       const auto A = operand(static_cast<const float*>(slope), np, 1, d.n_rows);
       const auto B = operand(w + v0 * d.w_stride, 1, d.w_stride, d.hidden);
-      e = with_tile(d.n_rows, d.hidden, dh_small(d), [&](auto tm, dim3 grid) {
+      e = with_tile(d.n_rows, d.hidden, dh_tile(d), [&](auto tm, auto tx, dim3 grid) {
         ls.more_kernels(1);
         grid.z = (unsigned)((np + per - 1) / per);  // a shorter last piece has fewer
         if (direct)
-          vocab_product_kernel<tm.value, float, T, T><<<grid, 256, 0, s>>>(A, B, np, per, false, static_cast<T*>(p.dh));
+          vocab_product_kernel<tm.value, tx.value, float, T, T><<<grid, 256, 0, s>>>(A, B, np, per, false, static_cast<T*>(p.dh));
         else
-          vocab_product_kernel<tm.value, float, T, float><<<grid, 256, 0, s>>>(A, B, np, per, v0 > 0, sums);
+          vocab_product_kernel<tm.value, tx.value, float, T, float><<<grid, 256, 0, s>>>(A, B, np, per, v0 > 0, sums);
       });
       if (e != cudaSuccess) return e;
     }
     if (p.dw) {
       const auto A = operand(static_cast<const float*>(slope), 1, np, np);
       const auto B = operand(h, 1, d.h_stride, d.hidden);
-      e = with_tile(np, d.hidden, small_tiles(np, d.hidden), [&](auto tm, dim3 grid) {
+      e = with_tile(np, d.hidden, pick_tile(np, d.hidden), [&](auto tm, auto tx, dim3 grid) {
         ls.more_kernels(1);
-        vocab_product_kernel<tm.value, float, T, T><<<grid, 256, 0, s>>>(A, B, d.n_rows, d.n_rows, false, static_cast<T*>(p.dw) + v0 * d.hidden);
+        vocab_product_kernel<tm.value, tx.value, float, T, T><<<grid, 256, 0, s>>>(A, B, d.n_rows, d.n_rows, false, static_cast<T*>(p.dw) + v0 * d.hidden);
       });
       if (e != cudaSuccess) return e;
     }
@@ -428,7 +446,7 @@ cudaError_t launch_vocab_join(int n_tiles, const VocabParams& p, const float2* p
 
 size_t vocab_simt_scratch(const ls_vocab_desc& d, bool with_grad) {
   const size_t n = (size_t)d.n_rows, nf = (size_t)(d.n_rows < kVocabRows ? d.n_rows : kVocabRows);
-  size_t need = (size_t)((d.vocab + 63) / 64) * nf * sizeof(float2) + nf * sizeof(float);
+  size_t need = (size_t)most_parts(d) * nf * sizeof(float2) + nf * sizeof(float);
   if (with_grad) {
     const size_t splits = (size_t)((simt_piece(d) + simt_per_split(d) - 1) / simt_per_split(d));
     const size_t g = (round_up(n * (size_t)simt_piece(d), 64) +

@@ -38,7 +38,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTile = 256, kHalf = 128, kBK = 64, kStages = 6, kThreads = 256;
 constexpr uint32_t kOperand = kHalf * kBK * 2;  // 16 KB: one CTA's share of A or B of a stage
 constexpr uint32_t kStage = 2 * kOperand;
-constexpr uint32_t kSmem = kStages * kStage + 1024;
+constexpr uint32_t kOutBox = 32 * 128;          // an epilogue warp's 32 rows x 64 columns of bf16
+constexpr uint32_t kSmem = kStages * kStage + 4 * 2 * kOutBox + 1024;
 constexpr uint32_t kMnBox = kBK * 128;          // [64 inner x 64 columns] of an MN-major operand
 
 enum Epilogue { kStats, kSlope, kOut };
@@ -58,10 +59,8 @@ struct ProductParams {
   float* hit;
   const float* lse;
   const float* d_logp;
-  __nv_bfloat16* slope;
-  int64_t slope_ld;
-  // gradients: to `out`, rounded, or (out NULL) to / added to float32 `sums` [split][m][n]
-  __nv_bfloat16* out;
+  // gradients: rounded, through the output's map, or (sums not NULL) to / added
+  // to float32 sums [split][m][n]
   float* sums;
   int32_t add;
   uint32_t* status;
@@ -117,9 +116,23 @@ __device__ __forceinline__ void commit2(uint32_t bar) {
       : "memory");
 }
 
+// Stores a swizzled [32 x 64] box of bf16 from shared memory; the map clips it.
+__device__ __forceinline__ void store_box(const CUtensorMap* m, uint32_t src, int32_t c0, int32_t c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(m)), "r"(src), "r"(c0), "r"(c1)
+      : "memory");
+}
+// All but the last N of this thread's stores have read their shared memory.
+template <int N>
+__device__ __forceinline__ void store_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
 template <int EPI, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    vocab_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const ProductParams p) {
+    vocab_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmC, const ProductParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bar_full[kStages], bar_empty[kStages], bar_done[2], bar_free[2];
   __shared__ uint32_t tmem_base_s, abort_s, never_s;
@@ -177,6 +190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       prefetch_tmap(&tmA);
       prefetch_tmap(&tmB);
+      prefetch_tmap(&tmC);
       int it = 0;
       bool ok = true;
       for (int u = pair; ok && u < units; u += pairs) {
@@ -254,7 +268,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
     const int q = warp - 4;
-    int n = 0;
+    const uint32_t out_box = ring + kStages * kStage + q * 2 * kOutBox;
+    int n = 0, boxes = 0;
     for (int u = pair; u < units; u += pairs, ++n) {
       const Unit t = unit(u);
       const int b = n & 1;
@@ -277,14 +292,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t acc = tbase + ((uint32_t)(q * 32) << 16) + b * kTile;
       const int cols = p.n - n0 < kTile ? p.n - n0 : kTile;
       const int hit = target >= p.v0 + n0 && target < p.v0 + n0 + cols ? (int)(target - p.v0 - n0) : -1;
-      float top = -CUDART_INF_F, sum = 0.f;
+      if constexpr (EPI == kStats) {
+        float top = -CUDART_INF_F, sum = 0.f;
 #pragma unroll 1
-      for (int c0 = 0; c0 < cols; c0 += 32) {
-        uint32_t r[32];
-        __syncwarp();
-        tmem_ld32(acc + c0, r);
-        tmem_wait_ld_r(r);
-        if constexpr (EPI == kStats) {
+        for (int c0 = 0; c0 < cols; c0 += 32) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld32(acc + c0, r);
+          tmem_wait_ld_r(r);
           float y[32], mx = -CUDART_INF_F;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
@@ -298,52 +313,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 32; ++j) s4[j & 3] += ex2(y[j] - ref);
           sum = sum * ex2(top - ref) + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
           top = mn;
-        } else if constexpr (EPI == kSlope) {
-          float d[32];
+        }
+        if (row_ok) p.parts[(int64_t)t.n * p.m + row] = make_float2(top, sum);
+      } else if (EPI == kOut && p.sums) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < cols; c0 += 32) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld32(acc + c0, r);
+          tmem_wait_ld_r(r);
+          if (!row_ok) continue;
+          // n is a multiple of 8: four columns are there or not
+          float* dst = p.sums + ((int64_t)t.split * p.m + row) * p.n + n0 + c0;
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            d[j] = c == 0.f ? 0.f : c * ((c0 + j == hit ? 1.f : 0.f) - ex2(fmaf(__uint_as_float(r[j]), p.scale_log2, -z2)));
-          if (row_ok) {
-            // the row's pitch is a multiple of 64 columns, so the pieces past the end are its own
-            __nv_bfloat16* dst = p.slope + (int64_t)row * p.slope_ld + n0 + c0;
-#pragma unroll
-            for (int j = 0; j < 32; j += 8)
-              if (n0 + c0 + j < p.slope_ld)
-                *reinterpret_cast<uint4*>(dst + j) = make_uint4(pack_bf16x2(d[j], d[j + 1]), pack_bf16x2(d[j + 2], d[j + 3]),
-                                                                pack_bf16x2(d[j + 4], d[j + 5]), pack_bf16x2(d[j + 6], d[j + 7]));
-          }
-        } else if (row_ok) {
-          // n is a multiple of 8: a piece of eight columns is there or not
-          if (p.out) {
-            __nv_bfloat16* dst = p.out + (int64_t)row * p.n + n0 + c0;
-#pragma unroll
-            for (int j = 0; j < 32; j += 8)
-              if (c0 + j < cols)
-                *reinterpret_cast<uint4*>(dst + j) =
-                    make_uint4(pack_bf16x2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
-                               pack_bf16x2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])),
-                               pack_bf16x2(__uint_as_float(r[j + 4]), __uint_as_float(r[j + 5])),
-                               pack_bf16x2(__uint_as_float(r[j + 6]), __uint_as_float(r[j + 7])));
-          } else {
-            float* dst = p.sums + ((int64_t)t.split * p.m + row) * p.n + n0 + c0;
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              if (c0 + j >= cols) break;
-              float4 v = make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]), __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
-              if (p.add) {
-                const float4 w = *reinterpret_cast<const float4*>(dst + j);
-                v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
-              }
-              *reinterpret_cast<float4*>(dst + j) = v;
+          for (int j = 0; j < 32; j += 4) {
+            if (c0 + j >= cols) break;
+            float4 v = make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]), __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
+            if (p.add) {
+              const float4 w = *reinterpret_cast<const float4*>(dst + j);
+              v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
             }
+            *reinterpret_cast<float4*>(dst + j) = v;
           }
+        }
+      } else {
+        // 64 columns at a time through the warp's own two boxes in shared memory
+        // and out by TMA: rows' lines leave whole.  (Each thread storing its
+        // row's 16-byte pieces, dw of 4 rows, 75,189 x 4584, took 300 us.)
+        const int row0 = t.m * kTile + (int)rank * kHalf + q * 32;
+#pragma unroll 1
+        for (int c0 = 0; c0 < cols && row0 < p.m; c0 += 64, ++boxes) {
+          const uint32_t box = out_box + (boxes & 1) * kOutBox;
+          if (lane == 0) store_read<1>();  // the box's last store has read it
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            tmem_ld32(acc + c0 + 32 * h, r);
+            tmem_wait_ld_r(r);
+            if constexpr (EPI == kSlope) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float e = ex2(fmaf(__uint_as_float(r[j]), p.scale_log2, -z2));
+                r[j] = __float_as_uint(c == 0.f ? 0.f : c * ((c0 + 32 * h + j == hit ? 1.f : 0.f) - e));
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+              st_shared_v4(box + sw128_offset(lane, 4 * h + j / 8),
+                           make_uint4(pack_bf16x2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                                      pack_bf16x2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])),
+                                      pack_bf16x2(__uint_as_float(r[j + 4]), __uint_as_float(r[j + 5])),
+                                      pack_bf16x2(__uint_as_float(r[j + 6]), __uint_as_float(r[j + 7]))));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) store_box(&tmC, box, n0 + c0, row0);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_at(map_to(smem_u32(&bar_free[b]), 0));
-      if (EPI == kStats && row_ok) p.parts[(int64_t)t.n * p.m + row] = make_float2(top, sum);
     }
+    // the stores have left before the CTA does
+    if (EPI != kStats && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -380,6 +413,11 @@ bool mn_major(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t
   return encode_matrix_map(m, p, rows, cols, stride, kBK, *boxes == 1 ? 2 : 1);
 }
 
+// An output: boxes of 32 rows x 64 columns.
+bool output(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t stride) {
+  return encode_matrix_map(m, p, rows, cols, stride, 32, 1);
+}
+
 // Pairs of CTAs that the device holds at once.
 template <typename K>
 int resident_pairs(K kernel) {
@@ -401,7 +439,7 @@ int resident_pairs(K kernel) {
 }
 
 template <int EPI, bool A_MN, bool B_MN>
-cudaError_t run_product(const CUtensorMap& a, const CUtensorMap& b, ProductParams p, cudaStream_t s) {
+cudaError_t run_product(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, ProductParams p, cudaStream_t s) {
   auto* kernel = vocab_tc_kernel<EPI, A_MN, B_MN>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
@@ -410,7 +448,7 @@ cudaError_t run_product(const CUtensorMap& a, const CUtensorMap& b, ProductParam
   if (units > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
   const int pairs = units < most ? (int)units : most;
   LaunchScope ls(kKVocabTc, s);
-  kernel<<<2 * pairs, kThreads, kSmem, s>>>(a, b, p);
+  kernel<<<2 * pairs, kThreads, kSmem, s>>>(a, b, c, p);
   return cudaGetLastError();
 }
 
@@ -475,7 +513,7 @@ cudaError_t launch_vocab_tc_fwd(const VocabParams& v, cudaStream_t s) {
   p.parts = static_cast<float2*>(v.scratch);
   p.hit = reinterpret_cast<float*>(p.parts + (int64_t)p.n_tiles * p.m);
   p.status = v.status;
-  const cudaError_t e = run_product<kStats, false, false>(a, b, p, s);
+  const cudaError_t e = run_product<kStats, false, false>(a, b, a, p, s);
   if (e != cudaSuccess) return e;
   return launch_vocab_join(p.n_tiles, v, p.parts, p.hit, s);
 }
@@ -494,11 +532,15 @@ cudaError_t launch_vocab_tc_bwd(const VocabParams& v, cudaStream_t s) {
     return cudaErrorInvalidValue;
   for (int64_t v0 = 0; v0 < d.vocab; v0 += piece) {
     const int64_t np = d.vocab - v0 < piece ? d.vocab - v0 : piece;
-    CUtensorMap wk, wm, sk, sm;
+    CUtensorMap wk, wm, sk, sm, so, dho, dwo;
+    memset(&dho, 0, sizeof(dho));
+    memset(&dwo, 0, sizeof(dwo));
     int32_t w_boxes = 1, s_boxes = 1;
     if (!k_major(&wk, w + v0 * d.w_stride, np, d.hidden, d.w_stride) ||
         !mn_major(&wm, w + v0 * d.w_stride, np, d.hidden, d.w_stride, &w_boxes) ||
-        !k_major(&sk, slope, d.n_rows, np, ld) || !mn_major(&sm, slope, d.n_rows, ld, ld, &s_boxes))
+        !k_major(&sk, slope, d.n_rows, np, ld) || !mn_major(&sm, slope, d.n_rows, ld, ld, &s_boxes) ||
+        !output(&so, slope, d.n_rows, np, ld) || (v.dh && !output(&dho, v.dh, d.n_rows, d.hidden, d.hidden)) ||
+        (v.dw && !output(&dwo, static_cast<__nv_bfloat16*>(v.dw) + v0 * d.hidden, np, d.hidden, d.hidden)))
       return cudaErrorInvalidValue;
     ProductParams p{};
     p.m = (int32_t)d.n_rows, p.n = (int32_t)np, p.k = d.hidden;
@@ -510,10 +552,8 @@ cudaError_t launch_vocab_tc_bwd(const VocabParams& v, cudaStream_t s) {
     p.targets = v.targets;
     p.lse = v.lse_in;
     p.d_logp = v.d_logp;
-    p.slope = slope;
-    p.slope_ld = ld;
     p.status = v.status;
-    cudaError_t e = run_product<kSlope, false, false>(hk, wk, p, s);
+    cudaError_t e = run_product<kSlope, false, false>(hk, wk, so, p, s);
     if (e != cudaSuccess) return e;
     if (v.dh) {
       ProductParams g{};
@@ -524,11 +564,10 @@ cudaError_t launch_vocab_tc_bwd(const VocabParams& v, cudaStream_t s) {
       g.splits = (int32_t)div_up(div_up(np, kBK), g.k_blocks);
       g.m_fast = 1;
       g.b_boxes = w_boxes;
-      g.out = direct ? static_cast<__nv_bfloat16*>(v.dh) : nullptr;
-      g.sums = sums;
+      g.sums = direct ? nullptr : sums;
       g.add = v0 > 0;
       g.status = v.status;
-      e = run_product<kOut, false, true>(sk, wm, g, s);
+      e = run_product<kOut, false, true>(sk, wm, dho, g, s);
       if (e != cudaSuccess) return e;
     }
     if (v.dw) {
@@ -538,9 +577,8 @@ cudaError_t launch_vocab_tc_bwd(const VocabParams& v, cudaStream_t s) {
       g.splits = 1, g.k_blocks = (int32_t)div_up(g.k, kBK);
       g.m_fast = 0;  // a strip of D serves all columns, h stays in L2
       g.a_boxes = s_boxes, g.b_boxes = h_boxes;
-      g.out = static_cast<__nv_bfloat16*>(v.dw) + v0 * d.hidden;
       g.status = v.status;
-      e = run_product<kOut, true, true>(sm, hm, g, s);
+      e = run_product<kOut, true, true>(sm, hm, dwo, g, s);
       if (e != cudaSuccess) return e;
     }
   }
