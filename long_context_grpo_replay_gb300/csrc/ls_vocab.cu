@@ -108,11 +108,12 @@ struct Product {
   }
 
   // Row (column) of output i (j) of the thread's: four together, TM 8 in two groups half a tile apart.
-  __device__ __forceinline__ static int at_m(int i) { return i / 4 * (TILE_M / 2) + threadIdx.x / TX * 4 + (i & 3); }
-  __device__ __forceinline__ static int at_n(int j) { return j / 4 * (TILE_N / 2) + threadIdx.x % TX * 4 + (j & 3); }
+  __device__ __forceinline__ static int at_m(int ty, int i) { return i / 4 * (TILE_M / 2) + ty * 4 + (i & 3); }
+  __device__ __forceinline__ static int at_n(int tx, int j) { return j / 4 * (TILE_N / 2) + tx * 4 + (j & 3); }
 
   __device__ __forceinline__ void run(const Operand<TA>& A, const Operand<TB>& B, int64_t m0, int64_t n0,
                                       int64_t kb, int64_t ke, float (&acc)[TM][TM]) {
+    const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
     // outputs two by two along n: one packed instruction for two products, each
     // rounded as fmaf rounds it
     uint64_t sum[TM][TM / 2];
@@ -139,8 +140,8 @@ struct Product {
         uint64_t y[TM / 2];
 #pragma unroll
         for (int i = 0; i < TM; i += 4) {
-          *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(&a[buf][k][at_m(i)]);
-          *reinterpret_cast<ulonglong2*>(y + i / 2) = *reinterpret_cast<const ulonglong2*>(&b[buf][k][at_n(i)]);
+          *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(&a[buf][k][at_m(ty, i)]);
+          *reinterpret_cast<ulonglong2*>(y + i / 2) = *reinterpret_cast<const ulonglong2*>(&b[buf][k][at_n(tx, i)]);
         }
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
@@ -173,15 +174,16 @@ __global__ void __launch_bounds__(256, 2) vocab_fwd_kernel(const ls_vocab_desc d
   const int64_t m0 = (int64_t)blockIdx.x * P::TILE_M, n0 = (int64_t)blockIdx.y * P::TILE_N;
   float acc[TM][TM];
   sm.run(A, B, m0, n0, 0, d.hidden, acc);
+  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int64_t row = m0 + P::at_m(i);
+    const int64_t row = m0 + P::at_m(ty, i);
     const int64_t target = row < d.n_rows ? __ldg(targets + row) : -1;
     float top = -CUDART_INF_F;
     float y[TM];
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-      const int64_t v = n0 + P::at_n(j);
+      const int64_t v = n0 + P::at_n(tx, j);
       const float x = acc[i][j] * d.logit_scale;
       if (v == target && v < d.vocab) hit[row] = x;
       y[j] = v < d.vocab ? x * kLog2e : -CUDART_INF_F;
@@ -249,16 +251,17 @@ __global__ void __launch_bounds__(256, 2) vocab_slope_kernel(const ls_vocab_desc
   const int64_t m0 = (int64_t)blockIdx.x * P::TILE_M, n0 = (int64_t)blockIdx.y * P::TILE_N;
   float acc[TM][TM];
   sm.run(A, B, m0, n0, 0, d.hidden, acc);
+  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int64_t row = m0 + P::at_m(i);
+    const int64_t row = m0 + P::at_m(ty, i);
     if (row >= d.n_rows) continue;
     const int64_t target = __ldg(targets + row);
     const float c = target >= 0 && target < d.vocab ? __ldg(d_logp + row) * d.logit_scale : 0.f;
     const float z = __ldg(lse + row);
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-      const int64_t n = n0 + P::at_n(j);
+      const int64_t n = n0 + P::at_n(tx, j);
       if (n >= np) continue;
       const float p = exp2f((acc[i][j] * d.logit_scale - z) * kLog2e);
       // a row that takes no part has no gradient even where its logits are not finite
@@ -278,13 +281,14 @@ __global__ void __launch_bounds__(256, 2) vocab_product_kernel(Operand<TA> A, Op
   const int64_t kb = blockIdx.z * per, ke = kb + per < K ? kb + per : K;
   out += (int64_t)blockIdx.z * A.n * B.n;
   sm.run(A, B, m0, n0, kb, ke, acc);
+  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int64_t m = m0 + P::at_m(i);
+    const int64_t m = m0 + P::at_m(ty, i);
     if (m >= A.n) continue;
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-      const int64_t n = n0 + P::at_n(j);
+      const int64_t n = n0 + P::at_n(tx, j);
       if (n >= B.n) continue;
       float v = acc[i][j];
       if constexpr (sizeof(TO) == 4)
