@@ -443,8 +443,8 @@ LS_API ls_status ls_cache_read(const ls_kv_cache* cache, const int64_t* slots, i
  *   q_dtype / o_dtype: o_dtype is q_dtype or LS_DTYPE_F32.
  *   max_q, max_kv: upper bounds of the lengths, for planning and the
  *     workspace; a longer sequence of queries is refused on the device (its
- *     o and lse are not written, the status word says so), a longer kv_len is
- *     computed, more slowly.  kv_len is at most pages_per_seq * S_p (more is
+ *     keys are not read, its o and lse hold nothing of use, the status word
+ *     says so), a longer kv_len is computed, more slowly.  kv_len is at most pages_per_seq * S_p (more is
  *     cut there and reported).
  *   q_stride: elements from one token of q to the next (a multiple of 8, at
  *     least Hq * d); o is contiguous. */
