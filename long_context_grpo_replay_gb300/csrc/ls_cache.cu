@@ -12,7 +12,9 @@
 // Both kernels only move bytes: a group of lanes takes a token's K and V row of
 // one head (writing: sixteen elements a lane, so that codes leave in 16-byte
 // pieces; reading: eight), all loads before the first use.  A row's maximum is
-// log2 of the group's lanes in shuffles; no shared memory.
+// log2 of the group's lanes in shuffles; no shared memory.  Measured: 131,075
+// tokens of 4 x 256 written from bf16 in 129 us (6.25 TB/s), 60,001 read to bf16
+// in 61.5 us (6.0 TB/s); a copy runs at 6.75.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 

@@ -249,6 +249,10 @@ __global__ void __launch_bounds__(128) cached_simt_kernel(const CachedParams p) 
 // exceeded by 2^4), so weights keep 11 bits down to 2^-25 of the largest.
 // Queries go to f16 with a power of two per row taken out.
 // bf16: the values as they are, P rounded to bf16 once.
+//
+// Measured (24/4 heads, d 256, e4m3): 1,000,003 keys in 300 us (6.85 TB/s, a copy's
+// rate); 32 sequences up to 16,384 keys in 116 us (5.2 TB/s); 8 sequences of 1 to 5
+// tokens over bf16 pages of 16, 8 x 128, in 39 us.
 // ===========================================================================
 template <bool E4>
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
