@@ -377,6 +377,23 @@ __global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 2) cached_mma_kernel
     return __ldg((lane < 16 ? p.c.k_exp : p.c.v_exp) + row);
   };
 
+  // the first ST-1 blocks on their way before anything else is waited for
+  int8_t first_exp[ST - 1];
+  int row_next;
+  {
+    int rows[ST];
+#pragma unroll
+    for (int x = 0; x < ST; ++x) rows[x] = lookup(warp + x * NW);
+#pragma unroll
+    for (int x = 0; x < ST - 1; ++x) {
+      issue(rows[x], x);
+      copy_commit();
+    }
+#pragma unroll
+    for (int x = 0; x < ST - 1; ++x) first_exp[x] = load_exp(rows[x]);
+    row_next = rows[ST - 1];
+  }
+
   // queries: B fragments of every product, and each row's factor and limit
   uint32_t qf[KS][NT][2];
   float crow[NT][2];
@@ -440,13 +457,7 @@ __global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 2) cached_mma_kernel
   // into shared memory one block later, its pool rows one block earlier, so
   // no load is waited for where it is issued
 #pragma unroll
-  for (int st = 0; st < ST - 1; ++st) {
-    const int row = lookup(warp + st * NW);
-    issue(row, st);
-    copy_commit();
-    exps[warp][st][lane] = load_exp(row);
-  }
-  int row_next = lookup(warp + (ST - 1) * NW);
+  for (int x = 0; x < ST - 1; ++x) exps[warp][x][lane] = first_exp[x];
   int8_t exp_next = 0;
   int st = 0, pend = -1;
   for (int blk = warp; blk < nblk; blk += NW) {

@@ -550,33 +550,39 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     const int sw = warp - 12, q4 = sw & 3, hf = sw >> 2;
     const int i = q4 * 32 + lane;
     const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
-    // queries: a warp takes 16 rows, eight columns a lane
-#pragma unroll 2
+    // queries: a warp takes 16 rows, eight columns a lane, all copied to their
+    // places at once; e4m3 turns them into f16 there
+    const uint32_t my_q = sQ + (lane >> 3) * (kBM * 128);
+#pragma unroll 4
     for (int x = 0; x < 16; ++x) {
       const int r = sw * 16 + x, t = r0 + r;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (t < r1 && lane < D / 8) {
-        const int tok = t / p.gq, hh = t - tok * p.gq;
-        v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(s.q0 + tok) * p.q_stride +
-                                                 (int64_t)(kvh * p.gq + hh) * D) + lane);
-      }
-      if constexpr (E4) {
+      const int tok = t < r1 ? t / p.gq : 0, hh = t < r1 ? t - tok * p.gq : 0;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(s.q0 + tok) * p.q_stride + (int64_t)(kvh * p.gq + hh) * D + lane * 8;
+      if (lane < D / 8) copy16(my_q + sw128_offset(r, lane & 7), src, t < r1);
+    }
+    copy_commit();
+    copy_wait<0>();
+    if constexpr (E4) {
+#pragma unroll 2
+      for (int x = 0; x < 16; ++x) {
+        const int r = sw * 16 + x;
+        const uint32_t at = my_q + sw128_offset(r, lane & 7);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (lane < D / 8) v = ld_shared_v4(at);
         // f16 with the row's power of two taken out: its largest element in [1, 4)
         uint32_t e[4] = {v.x, v.y, v.z, v.w}, top = 0;
 #pragma unroll
         for (int y = 0; y < 4; ++y) top = max(top, max((e[y] << 16) & 0x7fffffffu, e[y] & 0x7fff0000u));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = __reduce_max_sync(0xffffffffu, top);
         int f = 254 - (int)(top >> 23);
         f = f < 1 ? 1 : f > 253 ? 253 : f;
         const float to = __int_as_float(f << 23);
 #pragma unroll
         for (int y = 0; y < 4; ++y)
           e[y] = pack_f16x2(__uint_as_float(e[y] << 16) * to, __uint_as_float(e[y] & 0xffff0000u) * to);
-        v = make_uint4(e[0], e[1], e[2], e[3]);
+        if (lane < D / 8) st_shared_v4(at, make_uint4(e[0], e[1], e[2], e[3]));
         if (lane == 0) back_s[r] = __int_as_float((254 - f) << 23) * p.scale_log2;
       }
-      if (lane < D / 8) st_shared_v4(sQ + (lane >> 3) * (kBM * 128) + sw128_offset(r, lane & 7), v);
     }
     fence_proxy_async_smem();
     __syncwarp();
