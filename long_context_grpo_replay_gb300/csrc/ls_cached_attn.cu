@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(128) cached_simt_kernel(const CachedParams p) 
 // bf16: the values as they are, P rounded to bf16 once.
 //
 // Measured (24/4 heads, d 256, e4m3): 1,000,003 keys in 300 us (6.85 TB/s, a copy's
-// rate); 32 sequences up to 16,384 keys in 116 us (5.2 TB/s); 8 sequences of 1 to 5
+// rate); 32 sequences up to 16,384 keys in 114 us (5.3 TB/s); 8 sequences of 1 to 5
 // tokens over bf16 pages of 16, 8 x 128, in 39 us.
 // ===========================================================================
 template <bool E4>
@@ -750,27 +750,46 @@ cudaError_t run_mma(const CachedParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Rows of a tile: eight where that is all there is, else what the registers
-// hold (the output of one warp is NT * D/2 registers).
-template <int D>
+// Most rows that this kernel takes; more go to cached_tc_kernel.  By time on 100,000
+// keys (24/4 heads for d 256, 32/8 else), this kernel against that one: e4m3, d 256:
+// 12 rows 63 against 70 us, 18 rows 86 against 72; d 128: 24 rows 74 against 84, 28
+// rows 117 against 84; d 64: 32 rows 63 against 74, 48 rows 104 against 74.  bf16, d
+// 256: 12 rows 100 against 90 (6 rows of 8 sequences 70 and 70); d 128: 8 sequences of
+// up to 20 rows 43 against 49, 28 rows of one 121 against 88; d 64: 8 of up to 20 rows
+// 51 against 43.
+template <int D, bool E4>
+constexpr int kMmaRows = E4 ? (D == 256 ? 16 : D == 128 ? 24 : 32) : (D == 256 ? 8 : D == 128 ? 24 : 16);
+
+// Tiles of as many rows as there are, in eights.
+template <int D, bool E4>
 cudaError_t run_mma_d(const CachedParams& p, cudaStream_t s) {
-  const bool e4 = p.c.format == LS_CACHE_E4M3;
+  constexpr int kMost = kMmaRows<D, E4>;
   const int64_t rows = (int64_t)p.max_q * p.gq;
-  if (rows <= 8) return e4 ? run_mma<D, true, 1>(p, s) : run_mma<D, false, 1>(p, s);
-  if (rows <= 16 || D == 256) return e4 ? run_mma<D, true, 2>(p, s) : run_mma<D, false, 2>(p, s);
-  if constexpr (D < 256) return e4 ? run_mma<D, true, D == 128 ? 3 : 4>(p, s) : run_mma<D, false, D == 128 ? 3 : 4>(p, s);
+  if (rows <= 8) return run_mma<D, E4, 1>(p, s);
+  if constexpr (kMost > 8)
+    if (rows <= 16) return run_mma<D, E4, 2>(p, s);
+  if constexpr (kMost > 16)
+    if (rows <= kMost) return run_mma<D, E4, kMost / 8>(p, s);
   return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-int cached_mma_rows(int d) { return d == 256 ? 16 : d == 128 ? 24 : 32; }
+int cached_mma_rows(int d, int format) {
+  const bool e4 = format == LS_CACHE_E4M3;
+  switch (d) {
+    case 64: return e4 ? kMmaRows<64, true> : kMmaRows<64, false>;
+    case 128: return e4 ? kMmaRows<128, true> : kMmaRows<128, false>;
+    default: return e4 ? kMmaRows<256, true> : kMmaRows<256, false>;
+  }
+}
 
 cudaError_t launch_cached_mma(const CachedParams& p, cudaStream_t s) {
+  const bool e4 = p.c.format == LS_CACHE_E4M3;
   switch (p.c.head_dim) {
-    case 64: return run_mma_d<64>(p, s);
-    case 128: return run_mma_d<128>(p, s);
-    default: return run_mma_d<256>(p, s);
+    case 64: return e4 ? run_mma_d<64, true>(p, s) : run_mma_d<64, false>(p, s);
+    case 128: return e4 ? run_mma_d<128, true>(p, s) : run_mma_d<128, false>(p, s);
+    default: return e4 ? run_mma_d<256, true>(p, s) : run_mma_d<256, false>(p, s);
   }
 }
 

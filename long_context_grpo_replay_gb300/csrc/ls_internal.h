@@ -241,7 +241,7 @@ bool cached_tc_pairs(int64_t rows, int d);
 // Joins the ns parts (at most kCachedMaxParts) of every row.
 constexpr int kCachedMaxParts = 128;
 cudaError_t launch_cached_join(const CachedParams& p, cudaStream_t s);
-int cached_mma_rows(int d);  // rows of one tile of launch_cached_mma, at most
+int cached_mma_rows(int d, int format);  // rows that launch_cached_mma takes, at most
 
 // Vocabulary log-probabilities (ls_vocab.cu, ls_vocab_tc.cu).
 struct VocabParams {

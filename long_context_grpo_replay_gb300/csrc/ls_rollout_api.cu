@@ -119,9 +119,9 @@ CachedPlan plan_cached(const ls_cached_attn_desc& d, const ls_kv_cache& c) {
     pl.route = kRouteSimt;
     tile = 16, quantum = 32, ctas = 4 * sms;
     per_quantum = 6.0, fixed = 6.0;
-  } else if (rows <= cached_mma_rows(c.head_dim) || !device_is_sm100_family()) {
+  } else if (rows <= cached_mma_rows(c.head_dim, c.format)) {
     pl.route = kRouteMma;
-    tile = rows < 8 ? 8 : rows < cached_mma_rows(c.head_dim) ? rows : cached_mma_rows(c.head_dim);
+    tile = rows < 8 ? 8 : rows;
     quantum = 128, ctas = 2 * sms;
     per_quantum = quantum * key_bytes / 22e3, fixed = 10.0;
   } else {
