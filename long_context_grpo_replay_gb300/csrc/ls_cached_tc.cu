@@ -418,8 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
         commit<PAIR>(smem_u32(&bar_o));
         if (j == ntiles - 1) commit<PAIR>(smem_u32(&bar_last));
       }
-      // to this CTA alone: nothing may be on its way to the other when it ends
-      // (it waits for bar_last itself, which follows what else it was sent)
+      // no product is under way when the pair ends, not even after a wait gave up; to
+      // this CTA alone (what the other was sent, its warp 2 waits for)
       if constexpr (PAIR)
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&bar_drain)) : "memory");
       else
@@ -793,6 +793,19 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
         p.lse_parts[(int64_t)part * p.total_q * p.hq + out] = z;
       else
         p.lse[out] = z;
+    }
+  }
+  // What the products announce has arrived before a CTA ends, whether or not it has rows:
+  // an arrival must not find its shared memory given back.  bar_last comes with the last
+  // product; by then each other barrier stands at its last phase or the one before.
+  if (warp == 2 && ntiles > 0) {
+    bool in = wait(bar_last, 0, __LINE__) && wait(bar_o, (ntiles - 1) & 1, __LINE__);
+#pragma unroll 1
+    for (int x = 1; in && x <= kBar; ++x) {
+      const int c = nchunks - x, j = ntiles - x;
+      if (c >= 0) in = wait(bar_done[c % kBar], (c / kBar) & 1, __LINE__);
+      if (in && j >= 0) in = wait(bar_tile[j % kBar], (j / kBar) & 1, __LINE__);
+      if (in && j >= 0 && x <= 2) in = wait(bar_s[j & 1], (j >> 1) & 1, __LINE__);
     }
   }
   if (gave_up && (lane == 0 || warp == 1)) {

@@ -696,3 +696,19 @@ def test_vocab_many_rows(dtype, dev):
     got = run_vocab(h, w, t, dl, dev)
     ls.ls_read_device_status(got[4])
     check_vocab(h, w, t, dl, 1.0, *got[:4])
+
+
+@pytest.mark.parametrize("fmt", [E4, BF])
+@pytest.mark.parametrize("q_lens,kv_lens", [([40, 3, 21], [700, 650, 90]), ([45], [3000]), ([22, 1, 2], [5, 0, 2000])])
+def test_attention_pair_with_an_empty_second_half(fmt, q_lens, kv_lens, dev):
+    """Calls planned for pairs of CTAs (more than 128 rows at most) in which a pair's second CTA has no
+    rows of its own: sequences of up to 128 rows, and last tiles with that many left."""
+    c = Case(q_lens, kv_lens, dev, hq=6, hkv=1, d=256, page=16, fmt=fmt, seed=len(q_lens))
+    first = None
+    for _ in range(5):
+        o, lse, ws = c.run()
+        ls.ls_read_device_status(ws)
+        if first is None:
+            c.check(o, lse)
+            first = o, lse
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
