@@ -231,9 +231,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // no copy may still be landing when the pair ends: the first CTA's
       // barriers count both CTAs' bytes, and the pair leaves together
+      const int last = it - kStages < 0 ? 0 : it - kStages;
       if (rank == 0)
-        for (int i = it - kStages < 0 ? 0 : it - kStages; i < it; ++i)
+        for (int i = last; i < it; ++i)
           mbar_wait(smem_u32(&bar_full[i % kStages]), (i / kStages) & 1, &never_s);
+      // nor an arrival of the products: each CTA waits for the last ones that it was sent
+      for (int i = last; ok && i < it; ++i)
+        if (!mbar_wait(smem_u32(&bar_empty[i % kStages]), (i / kStages) & 1, abortp)) {
+          fail(__LINE__);
+          ok = false;
+        }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ products

@@ -712,3 +712,17 @@ def test_attention_pair_with_an_empty_second_half(fmt, q_lens, kv_lens, dev):
             c.check(o, lse)
             first = o, lse
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("n,d,v", [(300, 8, 777), (257, 512, 257), (40, 64, 90000)])
+def test_vocab_repeats(n, d, v, dev):
+    """Fewer blocks of the inner dimension than stages, more, and many tiles a pair of CTAs: every call ends with
+    nothing on its way to a CTA that has left, and repeats itself bit for bit."""
+    h, w, t, dl = vocab_case(n, d, v, BF, seed=d)
+    first = run_vocab(h, w, t, dl, dev)
+    check_vocab(h, w, t, dl, 1.0, *first[:4])
+    for _ in range(10):
+        got = run_vocab(h, w, t, dl, dev)
+        ls.ls_read_device_status(got[4])
+        for a, b in zip(first[:4], got[:4]):
+            assert torch.equal(a, b)
