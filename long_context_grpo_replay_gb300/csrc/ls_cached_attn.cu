@@ -654,10 +654,12 @@ __device__ __forceinline__ void store_joined(int o_dtype, void* o, int64_t at, f
 // w_s = exp(lse_s - max).  A CTA has one row; its threads take four columns
 // each and share the parts in groups, so that the few rows of a decoding step
 // still have many loads in flight.  Parts without keys (lse -infinity, o not
-// written) are skipped; a NaN part makes the row NaN.
+// written) are skipped; a NaN part makes the row NaN.  The kernel is there while the
+// parts are still being written: it reads them by ordinary loads, which the wait's
+// memory clobber keeps behind it (not as data that nothing writes while it runs).
 // ===========================================================================
-__global__ void __launch_bounds__(256) cached_join_kernel(int ns, int64_t n_rows, int d, const float* __restrict__ o_parts,
-                                                          const float* __restrict__ lse_parts, int o_dtype, void* o,
+__global__ void __launch_bounds__(256) cached_join_kernel(int ns, int64_t n_rows, int d, const float* o_parts,
+                                                          const float* lse_parts, int o_dtype, void* o,
                                                           float* lse) {
   __shared__ float w[kCachedMaxParts], total_s;
   __shared__ float4 acc_s[256];
@@ -670,7 +672,7 @@ __global__ void __launch_bounds__(256) cached_join_kernel(int ns, int64_t n_rows
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int s = tid + 32 * i;
-      v[i] = s < ns ? __ldg(lse_parts + (int64_t)s * n_rows + row) : -CUDART_INF_F;
+      v[i] = s < ns ? lse_parts[(int64_t)s * n_rows + row] : -CUDART_INF_F;
       top = fmaxf(top, v[i]);
     }
 #pragma unroll
@@ -697,7 +699,7 @@ __global__ void __launch_bounds__(256) cached_join_kernel(int ns, int64_t n_rows
   for (int s = group; s < ns; s += groups) {
     const float f = w[s];
     if (f == 0.f) continue;
-    const float4 z = __ldg(reinterpret_cast<const float4*>(o_parts + ((int64_t)s * n_rows + row) * d + c));
+    const float4 z = *reinterpret_cast<const float4*>(o_parts + ((int64_t)s * n_rows + row) * d + c);
     a.x = fmaf(f, z.x, a.x), a.y = fmaf(f, z.y, a.y), a.z = fmaf(f, z.z, a.z), a.w = fmaf(f, z.w, a.w);
   }
   acc_s[tid] = a;
@@ -713,24 +715,24 @@ __global__ void __launch_bounds__(256) cached_join_kernel(int ns, int64_t n_rows
 
 // The same for many rows and few parts: one thread per four columns, which
 // reads its row's few weights itself.
-__global__ void __launch_bounds__(256) cached_join_rows_kernel(int ns, int64_t n_rows, int d, const float* __restrict__ o_parts,
-                                                               const float* __restrict__ lse_parts, int o_dtype, void* o,
+__global__ void __launch_bounds__(256) cached_join_rows_kernel(int ns, int64_t n_rows, int d, const float* o_parts,
+                                                               const float* lse_parts, int o_dtype, void* o,
                                                                float* lse) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int cols = d >> 2, c = (int)(threadIdx.x % cols) * 4;
   const int64_t row = (int64_t)blockIdx.x * (256 / cols) + threadIdx.x / cols;
   if (row >= n_rows) return;
   float top = -CUDART_INF_F;
-  for (int s = 0; s < ns; ++s) top = fmaxf(top, __ldg(lse_parts + s * n_rows + row));
+  for (int s = 0; s < ns; ++s) top = fmaxf(top, lse_parts[s * n_rows + row]);
   const float ref = top == -CUDART_INF_F ? 0.f : top;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
 #pragma unroll 4
   for (int s = 0; s < ns; ++s) {
-    const float f = expf(__ldg(lse_parts + s * n_rows + row) - ref);
+    const float f = expf(lse_parts[s * n_rows + row] - ref);
     sum += f;
     if (f == 0.f) continue;
-    const float4 z = __ldcs(reinterpret_cast<const float4*>(o_parts + (s * n_rows + row) * d + c));
+    const float4 z = *reinterpret_cast<const float4*>(o_parts + (s * n_rows + row) * d + c);
     a.x = fmaf(f, z.x, a.x), a.y = fmaf(f, z.y, a.y), a.z = fmaf(f, z.z, a.z), a.w = fmaf(f, z.w, a.w);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;

@@ -726,3 +726,27 @@ def test_vocab_repeats(n, d, v, dev):
         ls.ls_read_device_status(got[4])
         for a, b in zip(first[:4], got[:4]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt,qd", [(E4, BF), (BF, BF), (F32, F32)])
+@pytest.mark.parametrize("n", [1, 40, 150])
+def test_attention_parts_are_this_call_s(fmt, qd, n, dev):
+    """Calls one after another in one workspace, with other queries each time and the parts' place overwritten in
+    between: the joining kernel, which is launched before the parts are written, reads what this call wrote."""
+    c = Case([n], [6000], dev, hq=6, hkv=1, d=256, page=256, fmt=fmt, qd=qd, seed=n)
+    qs = [c.q, (c.q.float() * -0.5).to(qd).as_strided(c.q.shape, c.q.stride())]
+    want = []
+    for q in qs:
+        c.q = q
+        o, lse, ws = c.run(o_dtype=F32)
+        want.append((o, lse))
+    assert ws.numel() > 2 * (n * 6 * 256 * 4 + 512), "cut into parts"
+    args, outs = c.args, []
+    for i in range(40):
+        ws[256:] = 0xFF  # NaN
+        o, lse = torch.empty_like(want[0][0]), torch.empty_like(want[0][1])
+        ls.ls_cached_attn(args[0], args[1], qs[i % 2], *args[3:6], o, lse, ws)
+        outs.append((o, lse))
+    ls.ls_read_device_status(ws)
+    for i, (o, lse) in enumerate(outs):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
