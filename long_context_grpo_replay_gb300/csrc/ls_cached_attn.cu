@@ -77,6 +77,7 @@ template <typename TQ, int FMT>
 __global__ void __launch_bounds__(128) cached_simt_kernel(const CachedParams p) {
   extern __shared__ float sm[];
   __shared__ int rows_s[kSimtKeys];
+  __shared__ bool nan_s[kSimtKeys];  // e4m3: the value row is marked NaN
   const int d = p.c.head_dim, ks = d + 4;
   float* sq = sm;                        // [16][d]
   float* sk = sq + kSimtRows * d;        // [32][d + 4]
@@ -126,7 +127,11 @@ __global__ void __launch_bounds__(128) cached_simt_kernel(const CachedParams p) 
   const int nc = d / 32;
   for (int k0 = kb; k0 < ke; k0 += kSimtKeys) {
     __syncthreads();  // the previous tile is used up
-    if (tid < kSimtKeys) rows_s[tid] = k0 + tid < ke ? pool_row(p, b, kvh, k0 + tid) : -1;
+    if (tid < kSimtKeys) {
+      const int row = k0 + tid < ke ? pool_row(p, b, kvh, k0 + tid) : -1;
+      rows_s[tid] = row;
+      if constexpr (FMT == LS_CACHE_E4M3) nan_s[tid] = row >= 0 && __ldg(p.c.v_exp + row) == -128;
+    }
     __syncthreads();
     for (int x = tid * 4; x < kSimtKeys * d; x += 128 * 4) {
       const int key = x / d, c = x - key * d, row = rows_s[key];
@@ -135,7 +140,8 @@ __global__ void __launch_bounds__(128) cached_simt_kernel(const CachedParams p) 
         float ek = 1.f, ev = 1.f;
         if constexpr (FMT == LS_CACHE_E4M3) {
           ek = exp_scale(__ldg(p.c.k_exp + row));
-          ev = exp_scale(__ldg(p.c.v_exp + row));
+          // a NaN row reaches only the rows that see it: through their weights
+          ev = nan_s[key] ? 0.f : exp_scale(__ldg(p.c.v_exp + row));
         }
         a = load_cache4<FMT>(p.c.k, (int64_t)row * d + c, ek);
         v = load_cache4<FMT>(p.c.v, (int64_t)row * d + c, ev);
@@ -154,6 +160,9 @@ __global__ void __launch_bounds__(128) cached_simt_kernel(const CachedParams p) 
       }
     }
     const bool there = rows_s[lane] >= 0;
+    if constexpr (FMT == LS_CACHE_E4M3) {
+      if (nan_s[lane]) x[0] = x[1] = x[2] = x[3] = __int_as_float(0x7fffffff);
+    }
     float pr[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {

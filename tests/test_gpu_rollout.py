@@ -750,3 +750,23 @@ def test_attention_parts_are_this_call_s(fmt, qd, n, dev):
     ls.ls_read_device_status(ws)
     for i, (o, lse) in enumerate(outs):
         assert torch.equal(o, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
+
+
+@pytest.mark.parametrize("qd", [BF, F32])
+@pytest.mark.parametrize("n", [2, 12, 40])
+def test_attention_nan_e4m3_rows_reach_only_their_readers(qd, n, dev):
+    """An e4m3 row marked NaN (key or value) makes the rows that see it NaN and changes no other."""
+    c = Case([n, n], [700, 600], dev, hq=6, hkv=1, d=256, page=64, fmt=E4, qd=qd, seed=3)
+    o, lse, _ = c.run()
+    p, r = int(c.table[1, 599 // 64]), 599 % 64  # only the second sequence's last token sees it
+    for side in ("k", "v"):
+        keep = c.c[side + "_exp"][p, 0, r].clone()
+        codes = c.c[side].view(torch.uint8)[p, 0, r].clone()
+        c.c[side + "_exp"][p, 0, r] = -128
+        c.c[side].view(torch.uint8)[p, 0, r] = 0
+        o2, lse2, ws = c.run()
+        ls.ls_read_device_status(ws)
+        assert o2[-1].isnan().all() and lse2[-1].isnan().all()
+        assert torch.equal(o2[:-1], o[:-1]) and torch.equal(lse2[:-1], lse[:-1])
+        c.c[side + "_exp"][p, 0, r] = keep
+        c.c[side].view(torch.uint8)[p, 0, r] = codes
