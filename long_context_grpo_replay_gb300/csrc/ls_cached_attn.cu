@@ -250,12 +250,13 @@ __global__ void __launch_bounds__(128) cached_simt_kernel(const CachedParams p) 
 //
 // e4m3: codes become f16 (exact, one conversion per pair), the scales stay
 // out of the products: K's multiplies the score, V's exponent is added to the
-// score's exponent.  Per key the weight is
-//   w_j = 2^(x_j + ev_j - mo),   l = sum_j w_j 2^-ev_j,   o = sum_j w_j code_j / l,
-// with mo the running maximum of x_j + ev_j (base 2), so one exponential
-// serves both and f16 holds the weights whatever the scales: they are kept
-// 2^11 times their value and at most 2^15 (the maximum moves once it is
-// exceeded by 2^4), so weights keep 11 bits down to 2^-25 of the largest.
+// score's exponent.  Per key (base 2, x_j the score, ev_j the value row's exponent)
+//   w_j = 2^(x_j + ev_j - mo),   l = sum_j 2^(x_j - mx),   o = 2^(mo - mx) sum_j w_j code_j / l,
+// with mo the running maximum of x_j + ev_j.  The softmax's sum has exponentials
+// and a reference of its own, so that neither overflows or vanishes however far
+// apart the value rows' scales are; each lane keeps its own mx, which float32 lets
+// lag by 2^40.  The weights are f16, 2^11 times their value and at most 2^15 (mo
+// moves once it is exceeded by 2^4): 11 bits down to 2^-25 of the largest.
 // Queries go to f16 with a power of two per row taken out.
 // bf16: the values as they are, P rounded to bf16 once.
 //
@@ -338,11 +339,11 @@ __global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 2) cached_mma_kernel
   constexpr int NW = L::NW, ST = L::ST, RB = L::kRowBytes, CPR = L::kChunks, VD = L::VD;
   constexpr int KS = D / 16;                 // products per score block, and m-tiles of O^T
   constexpr float kOff = E4 ? 11.f : 0.f;    // weights are held 2^kOff times their value
-  constexpr float kSlack = 4.f;
+  constexpr float kSlack = 4.f, kSumSlack = 40.f;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ int8_t exps[NW][ST][32];        // K exponents of 16 keys, V exponents of 16 keys
   __shared__ uint32_t there_s[NW][ST];       // which of the 16 keys exist
-  __shared__ float2 ml[NW][8 * NT];
+  __shared__ float3 ml[NW][8 * NT];          // reference of o, of the sum, the sum
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int b = blockIdx.z, kvh = blockIdx.y;
@@ -451,11 +452,11 @@ __global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 2) cached_mma_kernel
   }
 
   float o[NT][KS][4];
-  float m[NT][2], l[NT][2];
+  float m[NT][2], mx[NT][2], l[NT][2];  // bf16: l is relative to m, mx is not used
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) m[nt][h] = -CUDART_INF_F, l[nt][h] = 0.f;
+    for (int h = 0; h < 2; ++h) m[nt][h] = mx[nt][h] = -CUDART_INF_F, l[nt][h] = 0.f;
 #pragma unroll
     for (int i = 0; i < KS; ++i)
 #pragma unroll
@@ -509,15 +510,14 @@ __global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 2) cached_mma_kernel
       }
     }
     // scores of keys g and g+8, rows 2t and 2t+1
-    float ks[2] = {1.f, 1.f}, ev[2] = {0.f, 0.f}, vi[2] = {1.f, 1.f};
+    float ks[2] = {1.f, 1.f}, ev[2] = {0.f, 0.f};
     if constexpr (E4) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        ks[h] = exp_scale(exps[warp][st][g + 8 * h]);
         const int e = exps[warp][st][16 + g + 8 * h];
-        // a NaN row reaches only the rows that see it: through the exponent
-        vi[h] = e == -128 ? 1.f : exp_scale(-e);
-        ev[h] = e == -128 ? exp_scale(e) : (float)e;
+        // a NaN row reaches only the rows that see it: through their scores
+        ks[h] = exp_scale(e == -128 ? e : exps[warp][st][g + 8 * h]);
+        ev[h] = (float)e;
       }
     }
     const int key = kb + blk * 16 + g;
@@ -531,8 +531,18 @@ __global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 2) cached_mma_kernel
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const bool sees = (there >> (g + 8 * h) & 1u) && key + 8 * h < lim[nt][r];
-          const float v = E4 ? fmaf(x[nt][2 * h + r], crow[nt][r] * ks[h], ev[h]) : x[nt][2 * h + r] * crow[nt][r];
+          const float v = x[nt][2 * h + r] * (E4 ? crow[nt][r] * ks[h] : crow[nt][r]);
           y[h] = sees ? v : -CUDART_INF_F;
+        }
+        if constexpr (E4) {
+          const float tx = fmaxf(y[0], y[1]);
+          if (tx > mx[nt][r] + kSumSlack) {
+            l[nt][r] *= ex2(mx[nt][r] - tx);
+            mx[nt][r] = tx;
+          }
+          const float rx = mx[nt][r] == -CUDART_INF_F ? 0.f : mx[nt][r];
+          l[nt][r] += ex2(y[0] - rx) + ex2(y[1] - rx);
+          y[0] += ev[0], y[1] += ev[1];
         }
         float top = fmaxf(y[0], y[1]);
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
@@ -541,7 +551,7 @@ __global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 2) cached_mma_kernel
         if (top > m[nt][r] + kSlack) {
           const float alpha = ex2(m[nt][r] - top);
           m[nt][r] = top;
-          l[nt][r] *= alpha;
+          if constexpr (!E4) l[nt][r] *= alpha;
 #pragma unroll
           for (int i = 0; i < KS; ++i) o[nt][i][r] *= alpha, o[nt][i][2 + r] *= alpha;
         }
@@ -551,7 +561,7 @@ __global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 2) cached_mma_kernel
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           w[h][r] = ex2(y[h] - ref);
-          l[nt][r] = E4 ? fmaf(w[h][r], vi[h], l[nt][r]) : l[nt][r] + w[h][r];
+          if constexpr (!E4) l[nt][r] += w[h][r];
         }
       }
       pb[nt][0] = transpose8(pack2<E4>(w[0][0], w[0][1]));
@@ -608,12 +618,19 @@ __global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 2) cached_mma_kernel
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float sum = l[nt][r];
+      // each lane's sum is relative to a reference of its own (e4m3)
+      float top = E4 ? mx[nt][r] : m[nt][r], sum = l[nt][r];
+      if constexpr (E4) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        if (mx[nt][r] != -CUDART_INF_F) sum *= ex2(mx[nt][r] - top);
+      }
       sum += __shfl_xor_sync(0xffffffffu, sum, 4);
       sum += __shfl_xor_sync(0xffffffffu, sum, 8);
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
       const int row = nt * 8 + 2 * t + r;
-      if (g == 0) ml[warp][row] = make_float2(m[nt][r], sum);
+      if (g == 0) ml[warp][row] = make_float3(m[nt][r], top, sum);
       float* dst = so + (warp * 8 * NT + row) * OS;
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
@@ -625,26 +642,29 @@ __global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 2) cached_mma_kernel
   __syncthreads();
   for (int x = tid; x < (r1 - r0) * (D / 4); x += NW * 32) {
     const int row = x / (D / 4), c = (x % (D / 4)) * 4;
-    float top = -CUDART_INF_F;
+    float top = -CUDART_INF_F, topx = -CUDART_INF_F;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) top = fmaxf(top, ml[w][row].x);
-    const float ref = top == -CUDART_INF_F ? 0.f : top;
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, ml[w][row].x), topx = fmaxf(topx, ml[w][row].y);
+    const float ref = top == -CUDART_INF_F ? 0.f : top, refx = topx == -CUDART_INF_F ? 0.f : topx;
     float sum = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      const float2 a = ml[w][row];
+      const float3 a = ml[w][row];
       // a warp that saw no key has a weight of 0, but passes a NaN on
-      const float f = a.x == -CUDART_INF_F ? (a.y != a.y ? 1.f : 0.f) : ex2(a.x - ref);
+      const float f = a.x == -CUDART_INF_F ? 0.f : ex2(a.x - ref), fx = a.y == -CUDART_INF_F ? 1.f : ex2(a.y - refx);
       const float4 z = *reinterpret_cast<const float4*>(so + (w * 8 * NT + row) * OS + c);
-      sum = fmaf(f, a.y, sum);
+      sum = fmaf(fx, a.z, sum);
       v.x = fmaf(f, z.x, v.x), v.y = fmaf(f, z.y, v.y), v.z = fmaf(f, z.z, v.z), v.w = fmaf(f, z.w, v.w);
     }
     const int r = r0 + row, i = r / p.gq, hh = r - i * p.gq;
     const int64_t out = (int64_t)(s.q0 + i) * p.hq + kvh * p.gq + hh;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    if (p.ns == 1 || sum != 0.f) write_o4(p, part, out, c, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-    if (c == 0) write_lse(p, part, out, sum == 0.f ? -CUDART_INF_F : (ref - kOff + log2f(sum)) * kLn2);
+    // from o's reference to the sum's, by halves: the whole may pass float32's range
+    const float to = ex2(0.5f * (ref - kOff - refx));
+    v.x = v.x * inv * to * to, v.y = v.y * inv * to * to, v.z = v.z * inv * to * to, v.w = v.w * inv * to * to;
+    if (p.ns == 1 || sum != 0.f) write_o4(p, part, out, c, v);
+    if (c == 0) write_lse(p, part, out, sum == 0.f ? -CUDART_INF_F : (refx + log2f(sum)) * kLn2);
   }
 }
 

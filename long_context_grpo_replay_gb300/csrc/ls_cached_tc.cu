@@ -24,8 +24,13 @@
 // largest (what that rounds, rows 2^10 times smaller and more, is 2^-33 of the
 // largest key's part of a score).  Value scales stay out of the product, whose
 // small rows may be the ones that count: y = x + ev (base 2) is the score and the
-// exponent of the value row, w = 2^(y - m) the weight that multiplies codes, l =
-// sum w 2^-ev, o = sum w code / l.  Weights are f16, held 2^11 times their value
+// exponent of the value row, w = 2^(y - m) the weight that multiplies codes.
+// Exponents are counted from the largest so far, B (of the part's tiles up to this
+// one): a tile's share of the softmax's sum is sum w 2^(B - ev) = sum 2^(x - (m - B)),
+// added in float32 with its reference m - B beside it, so that neither the sum nor
+// the weights leave float32's range at either end of the scales.  For that ev - B
+// is held at -80 at least: a value row 2^80 times smaller than the largest so far
+// counts as 2^-80 of it.  Weights are f16, held 2^11 times their value
 // and at most 2^15: 11 bits down to 2^-25 of the largest, so a sum of many small
 // weights beside a large one is not lost.  bf16: P in bf16, as in the replay
 // kernels.  Each row's maximum only moves when exceeded by 2^4
@@ -57,6 +62,7 @@ using namespace tc;
 constexpr int kBM = 128, kBN = 128, kThreads = 640;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kBar = 8;  // barriers per ring (more than chunks), and tiles of key tables
+constexpr int kValueSpan = 80;  // binades below the largest value scale that are told apart
 
 // PAIR: two CTAs (cta_group::2) share a tile of 256 rows; each has half of
 // every K tile's keys and half of every V tile's columns.
@@ -229,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
   // a key's scale: FOLD: 2^ek over the tile's largest, twice in f16; else the float32
   __shared__ __align__(16) uint32_t kh_s[E4 ? kBar : 1][kBN];
   __shared__ float kmax_s[kBar];                 // 2^(the tile's largest ek)
+  __shared__ int base_s[kBar];                   // the largest ev of the tiles so far
   __shared__ __align__(16) float ev_s[E4 ? kBar : 1][kBN], vi_s[E4 ? kBar : 1][kBN];
   __shared__ uint32_t there_s[kBar][4];
   __shared__ float top_s[2][2][kBM], back_s[kBM];
@@ -341,10 +348,24 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
           top = __reduce_max_sync(0xffffffffu, top);
           top = top == -127 ? 0 : top;
         }
+        int base = -126;  // the largest value scale of the tile's keys
+        if constexpr (E4) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) base = row[x] >= 0 && ev[x] > base ? ev[x] : base;
+          base = __reduce_max_sync(0xffffffffu, base);
+        }
         // the tables of tile j - kBar are used up once its O is done
         if (j >= kBar && !mbar_wait_lazy_warp<200>(smem_u32(&bar_tile[sl]), (j / kBar - 1) & 1)) {
           gave_up = __LINE__;
           break;
+        }
+        if constexpr (E4) {
+          // and of the tiles before, from the other warp's table
+          if (j > 0) {
+            if (!wait(bar_rows[(j - 1) % kBar], ((j - 1) / kBar) & 1, __LINE__)) break;
+            base = max(base, base_s[(j - 1) % kBar]);
+          }
+          if (lane == 0) base_s[sl] = base;
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -359,8 +380,9 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
             if constexpr (FOLD) kh_s[sl][x * 32 + lane] = h | h << 16;
             // a NaN row reaches only the rows that see it: through the exponent
             const bool nan = ev[x] == -128;
-            ev_s[sl][x * 32 + lane] = nan ? exp_scale(-128) : (float)ev[x];
-            vi_s[sl][x * 32 + lane] = nan ? 1.f : exp_scale(-ev[x]);
+            const int e = row[x] >= 0 ? max(ev[x] - base, -kValueSpan) : 0;
+            ev_s[sl][x * 32 + lane] = nan ? exp_scale(-128) : (float)e;
+            vi_s[sl][x * 32 + lane] = nan ? 1.f : exp_scale(-e);
           }
         }
         if (E4 && lane == 0) kmax_s[sl] = exp_scale(top);
@@ -597,7 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     // a row past the end has zero queries; seeing every key keeps its warp on the short path
     const int lim = row_ok ? row_limit(p, s, tok) : INT32_MAX;
     const float crow = E4 ? back_s[i] : p.scale_log2;
-    float m_run = -CUDART_INF_F, l_run = 0.f;
+    // the row's maximum, its sum and what the sum is relative to
+    float m_run = -CUDART_INF_F, l_run = 0.f, r_run = -CUDART_INF_F;
     if (r0 + q4 * 32 >= r1) {
       // a warp without rows only keeps step: its rows of P may hold anything,
       // since each row of O depends on its own row of P alone
@@ -672,7 +695,11 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       if (!ok) break;
       tc_fence_after();
       mx = fmaxf(mx, top_s[bf][hf ^ 1][i]);
-      if constexpr (!E4) mx *= crow;
+      const float base = E4 ? (float)base_s[sl] : 0.f;
+      if constexpr (E4)
+        mx += base;
+      else
+        mx *= crow;
       float alpha = 1.f;
       bool rescale = false;
       if (mx > m_run + kSlack) {
@@ -680,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
           alpha = ex2(m_run - mx);
           rescale = true;
         }
-        l_run *= alpha;
+        if constexpr (!E4) l_run *= alpha;
         m_run = mx;
       }
       if (__any_sync(0xffffffffu, rescale)) {
@@ -702,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       // a row that has seen no key keeps its reference at 0: -infinity gives a
       // weight of 0, and a NaN stays one
       const float ref = (m_run == -CUDART_INF_F ? 0.f : m_run) - kOff;
-      const uint64_t nref = f2(-ref, -ref), sc2 = f2(crow, crow);
+      const uint64_t nref = f2(base - ref, base - ref), sc2 = f2(crow, crow);
       uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
       const ulonglong2* vi = reinterpret_cast<const ulonglong2*>(&vi_s[E4 ? sl : 0][hf * 64]);
 #pragma unroll
@@ -739,7 +766,15 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       float p0, p1, p2, p3;
       f2_split(acc[0], p0, p1);
       f2_split(acc[1], p2, p3);
-      l_run += (p0 + p1) + (p2 + p3);
+      const float sum = (p0 + p1) + (p2 + p3);
+      if constexpr (E4) {
+        // the larger reference holds for both; 0 where no key was seen yet
+        const float r = m_run - base, rn = fmaxf(r_run, r), at = rn == -CUDART_INF_F ? 0.f : rn;
+        l_run = l_run * ex2(r_run - at) + sum * ex2(r - at);
+        r_run = rn;
+      } else {
+        l_run += sum;
+      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -759,6 +794,8 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     }
     const int64_t out = (int64_t)(s.q0 + tok) * p.hq + kvh * p.gq + hh;
     const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float seen = E4 ? r_run : m_run, lref = seen == -CUDART_INF_F ? 0.f : seen;
+    const float to = E4 ? ex2(m_run - seen) : 1.f;  // from O's reference to the sum's
 #pragma unroll 1
     for (int c0 = hf * (D / 2); c0 < (hf + 1) * (D / 2); c0 += 32) {
       uint32_t rr[32];
@@ -774,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       // a row without keys: its O was never weighted, and 0 times it is 0
       float v[32];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) v[c] = l == 0.f ? 0.f : __uint_as_float(rr[c]) * inv;
+      for (int c = 0; c < 32; ++c) v[c] = l == 0.f ? 0.f : __uint_as_float(rr[c]) * inv * to;
       if (p.ns > 1 || p.o_dtype == LS_DTYPE_F32) {
         float* dst = (p.ns > 1 ? p.o_parts + (int64_t)part * p.total_q * p.hq * D : static_cast<float*>(p.o)) + out * D + c0;
 #pragma unroll
@@ -788,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       }
     }
     if (row_ok && hf == 0) {
-      const float z = l == 0.f ? -CUDART_INF_F : ((m_run == -CUDART_INF_F ? 0.f : m_run) - kOff + __log2f(l)) * kLn2;
+      const float z = l == 0.f ? -CUDART_INF_F : (lref - kOff + __log2f(l)) * kLn2;
       if (p.ns > 1)
         p.lse_parts[(int64_t)part * p.total_q * p.hq + out] = z;
       else

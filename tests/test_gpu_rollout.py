@@ -770,3 +770,60 @@ def test_attention_nan_e4m3_rows_reach_only_their_readers(qd, n, dev):
         assert torch.equal(o2[:-1], o[:-1]) and torch.equal(lse2[:-1], lse[:-1])
         c.c[side + "_exp"][p, 0, r] = keep
         c.c[side].view(torch.uint8)[p, 0, r] = codes
+
+
+def shift_values(c, b, shift, rows=None):
+    """Moves the exponents of sequence b's value rows by shift [kv_len] (all heads), in the cache and the oracle."""
+    page = c.c["v"].shape[2]
+    for j in range(len(shift)):
+        c.c["v_exp"][int(c.table[b, j // page]), :, j % page] += int(shift[j])
+    c.values[b] = c.values[b] * 2.0 ** shift.to(F64)[:, None, None]
+
+
+def check_times(c, o, lse, factor, causal=True):
+    """c.check of results times a power of two, so that its absolute term stays out of it."""
+    keep = c.values
+    c.values = [v * factor for v in keep]
+    c.check((o.double() * factor).to(o.dtype), lse, causal)
+    c.values = keep
+
+
+@pytest.mark.parametrize("fmt,qd", [(E4, BF), (E4, F32)])
+@pytest.mark.parametrize("n", [1, 12, 40])
+@pytest.mark.parametrize("at", [-126, -118, -97, -60, 100])
+def test_attention_value_scales_at_their_ends(fmt, qd, n, at, dev):
+    """All value rows near one far exponent (down to the least that the cache holds), in one part and in several."""
+    for m in (1, 90, 4000):
+        c = Case([n], [m], dev, hq=6, hkv=1, d=256, page=256, fmt=fmt, qd=qd, seed=m)
+        low = min(int(c.c["v_exp"][int(c.table[0, j // 256]), 0, j % 256]) for j in range(m))
+        shift_values(c, 0, torch.full((m,), at - low))
+        o, lse, ws = c.run()
+        ls.ls_read_device_status(ws)
+        check_times(c, o, lse, 2.0 ** -(at + 8))
+
+
+@pytest.mark.parametrize("n", [1, 12, 40])
+@pytest.mark.parametrize("where", ["a part", "every other", "the first tile", "the last tile"])
+def test_attention_least_value_scales_beside_ordinary_ones(n, where, dev):
+    """Value rows at the least exponent beside ordinary rows: in a part of their own, mixed, first, last."""
+    m = 4000
+    c = Case([n], [m], dev, hq=6, hkv=1, d=256, page=256, seed=5)
+    j = torch.arange(m)
+    tiny = {"a part": j < 2000, "every other": j % 2 == 0, "the first tile": j < 128, "the last tile": j >= m - 160}[where]
+    exps = torch.tensor([int(c.c["v_exp"][int(c.table[0, x // 256]), 0, x % 256]) for x in range(m)])
+    shift_values(c, 0, torch.where(tiny, -126 - exps, torch.zeros_like(exps)))
+    for causal in (True, False):
+        o, lse, ws = c.run(causal)
+        ls.ls_read_device_status(ws)
+        c.check(o, lse, causal)
+
+
+@pytest.mark.parametrize("n", [1, 12, 40])
+def test_attention_value_scales_160_binades_apart(n, dev):
+    """Rows around 2^100 and rows around 2^-60 of like weight: the small rows' weights count in the sum all the same."""
+    m = 1500
+    c = Case([n], [m], dev, hq=6, hkv=1, d=256, page=256, seed=6)
+    shift_values(c, 0, torch.where(torch.arange(m) % 3 == 0, 100, -60))
+    o, lse, ws = c.run()
+    ls.ls_read_device_status(ws)
+    check_times(c, o, lse, 2.0 ** -100)
