@@ -319,6 +319,13 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// The maximum over the eight lanes that hold a block's keys for the same query rows.
+__device__ __forceinline__ float key_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+
 template <int D, bool E4>
 struct MmaShape {
   static constexpr int kRowBytes = D * (E4 ? 1 : 2);
@@ -524,43 +531,70 @@ __global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 2) cached_mma_kernel
     uint32_t pb[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float w[2][2];  // [key half][row]
+      float y[2][2], top[2];  // [row][key half]
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float y[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const bool sees = (there >> (g + 8 * h) & 1u) && key + 8 * h < lim[nt][r];
           const float v = x[nt][2 * h + r] * (E4 ? crow[nt][r] * ks[h] : crow[nt][r]);
-          y[h] = sees ? v : -CUDART_INF_F;
+          y[r][h] = sees ? v : -CUDART_INF_F;
         }
         if constexpr (E4) {
-          const float tx = fmaxf(y[0], y[1]);
-          if (tx > mx[nt][r] + kSumSlack) {
-            l[nt][r] *= ex2(mx[nt][r] - tx);
-            mx[nt][r] = tx;
-          }
-          const float rx = mx[nt][r] == -CUDART_INF_F ? 0.f : mx[nt][r];
-          l[nt][r] += ex2(y[0] - rx) + ex2(y[1] - rx);
-          y[0] += ev[0], y[1] += ev[1];
+          const float tx = fmaxf(y[r][0], y[r][1]), nx = tx > mx[nt][r] + kSumSlack ? tx : mx[nt][r];
+          const float at = nx == -CUDART_INF_F ? 0.f : nx;
+          l[nt][r] = fmaf(l[nt][r], ex2(mx[nt][r] - at), ex2(y[r][0] - at) + ex2(y[r][1] - at));
+          mx[nt][r] = nx;
+          y[r][0] += ev[0], y[r][1] += ev[1];
         }
-        float top = fmaxf(y[0], y[1]);
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-        if (top > m[nt][r] + kSlack) {
-          const float alpha = ex2(m[nt][r] - top);
-          m[nt][r] = top;
+        top[r] = key_max(fmaxf(y[r][0], y[r][1]));
+      }
+      if (__any_sync(0xffffffffu, top[0] > m[nt][0] + kSlack || top[1] > m[nt][1] + kSlack)) {
+        if constexpr (E4) {
+          // A value row of zeros, which the cache holds with exponent 0, adds nothing to
+          // o and must not raise the reference (below it, its weight is harmless).
+          const uint32_t none = __ballot_sync(0xffffffffu, exps[warp][st][lane] == 0) >> 16 & there;
+          if (none) {
+            uint32_t zeros = 0;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              uint32_t any = 0;
+#pragma unroll 4
+              for (int c = t; c < CPR; c += 4) {
+                const uint4 z = lds16(sv + (g + 8 * h) * RB + c * 16);
+                any |= z.x | z.y | z.z | z.w;
+              }
+              any |= __shfl_xor_sync(0xffffffffu, any, 1);
+              any |= __shfl_xor_sync(0xffffffffu, any, 2);
+              if ((none >> (g + 8 * h) & 1u) && (any & 0x7f7f7f7fu) == 0) zeros |= 1u << h;
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              if (zeros & 1u) y[r][0] = -CUDART_INF_F;
+              if (zeros & 2u) y[r][1] = -CUDART_INF_F;
+              top[r] = key_max(fmaxf(y[r][0], y[r][1]));
+            }
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (!(top[r] > m[nt][r] + kSlack)) continue;
+          const float alpha = ex2(m[nt][r] - top[r]);
+          m[nt][r] = top[r];
           if constexpr (!E4) l[nt][r] *= alpha;
 #pragma unroll
           for (int i = 0; i < KS; ++i) o[nt][i][r] *= alpha, o[nt][i][2 + r] *= alpha;
         }
+      }
+      float w[2][2];  // [key half][row]
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
         // where no key is seen yet the maximum stands at 0, so that -infinity
         // gives a weight of 0 and a NaN stays one
         const float ref = (m[nt][r] == -CUDART_INF_F ? 0.f : m[nt][r]) - kOff;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          w[h][r] = ex2(y[h] - ref);
+          w[h][r] = ex2(y[r][h] - ref);
           if constexpr (!E4) l[nt][r] += w[h][r];
         }
       }
@@ -621,9 +655,7 @@ __global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 2) cached_mma_kernel
       // each lane's sum is relative to a reference of its own (e4m3)
       float top = E4 ? mx[nt][r] : m[nt][r], sum = l[nt][r];
       if constexpr (E4) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        top = key_max(top);
         if (mx[nt][r] != -CUDART_INF_F) sum *= ex2(mx[nt][r] - top);
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 4);
@@ -661,7 +693,7 @@ __global__ void __launch_bounds__(MmaShape<D, E4>::NW * 32, 2) cached_mma_kernel
     const int64_t out = (int64_t)(s.q0 + i) * p.hq + kvh * p.gq + hh;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     // from o's reference to the sum's, by halves: the whole may pass float32's range
-    const float to = ex2(0.5f * (ref - kOff - refx));
+    const float to = top == -CUDART_INF_F ? 1.f : ex2(0.5f * (ref - kOff - refx));
     v.x = v.x * inv * to * to, v.y = v.y * inv * to * to, v.z = v.z * inv * to * to, v.w = v.w * inv * to * to;
     if (p.ns == 1 || sum != 0.f) write_o4(p, part, out, c, v);
     if (c == 0) write_lse(p, part, out, sum == 0.f ? -CUDART_INF_F : (refx + log2f(sum)) * kLn2);

@@ -350,6 +350,27 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
         }
         int base = -126;  // the largest value scale of the tile's keys
         if constexpr (E4) {
+          // A value row of zeros, which the cache holds with exponent 0, adds nothing
+          // to O and must not raise the base: it counts as the smallest.  Whether a
+          // row with this exponent is one, its codes say (mostly the first few).
+          uint32_t zero = 0;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) zero |= row[x] >= 0 && ev[x] == 0 ? 1u << x : 0u;
+          if (__any_sync(0xffffffffu, zero != 0)) {
+            const uint4* codes = static_cast<const uint4*>(p.c.v);
+#pragma unroll 1
+            for (int c = 0; c < D / 16 && __any_sync(0xffffffffu, zero != 0); c += 2) {
+              uint4 z[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                z[x] = zero >> (x >> 1) & 1u ? __ldg(codes + (int64_t)row[x >> 1] * (D / 16) + c + (x & 1)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                if ((z[x].x | z[x].y | z[x].z | z[x].w) & 0x7f7f7f7fu) zero &= ~(1u << (x >> 1));
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) ev[x] = zero >> x & 1u ? -126 : ev[x];
+          }
 #pragma unroll
           for (int x = 0; x < 4; ++x) base = row[x] >= 0 && ev[x] > base ? ev[x] : base;
           base = __reduce_max_sync(0xffffffffu, base);

@@ -827,3 +827,58 @@ def test_attention_value_scales_160_binades_apart(n, dev):
     o, lse, ws = c.run()
     ls.ls_read_device_status(ws)
     check_times(c, o, lse, 2.0 ** -100)
+
+
+def one_loud_key(c, at, loud):
+    """Queries 16 in dimension 0; keys 0 but for key `at`, which is `loud` there: its score is loud, the others' 0."""
+    m, page, d = c.keys[0].shape[0], c.c["k"].shape[2], c.d
+    q = torch.zeros_like(c.q_host)
+    q[..., 0] = 16.0
+    c.q_host, c.q = q, q.to(c.dev)
+    k = torch.zeros(m, 1, d, dtype=F64)
+    k[at, 0, 0] = loud
+    codes, exps = ref.quantise(k)
+    for j in range(m):
+        p, r = int(c.table[0, j // page]), j % page
+        c.c["k"].view(torch.uint8)[p, :, r] = codes[j].to(c.dev)
+        c.c["k_exp"][p, :, r] = exps[j].to(c.dev)
+    c.keys[0] = ref.dequantise(codes, exps)
+
+
+def zero_values(c, which):
+    """Value rows `which` of the first sequence as the cache writes zeros."""
+    page = c.c["v"].shape[2]
+    for j in which:
+        p, r = int(c.table[0, j // page]), j % page
+        c.c["v"].view(torch.uint8)[p, :, r] = 128 if j % 2 else 0  # -0 and 0
+        c.c["v_exp"][p, :, r] = 0
+        c.values[0][j] = 0
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 12, 50])
+def test_attention_a_zero_value_row_above_many(n, d, dev):
+    """A key whose weight is e^17 of the others' and whose value row is zeros: the output is the others' small
+    sum, whatever the scale of their values."""
+    for at, shift in ((7, -5), (1999, -20), (700, 0)):
+        c = Case([n], [2000], dev, hq=6, hkv=1, d=d, page=256, seed=4, q_scale=0.0)
+        one_loud_key(c, at, 17.0 * 16 / 16 * math.sqrt(d) / 16)
+        shift_values(c, 0, torch.full((2000,), shift))
+        zero_values(c, [at])
+        o, lse, ws = c.run(False)
+        ls.ls_read_device_status(ws)
+        check_times(c, o, lse, 2.0 ** -(shift - 24), False)
+
+
+@pytest.mark.parametrize("n", [1, 12, 50])
+@pytest.mark.parametrize("where", ["all", "the first tiles", "the last tiles", "every other"])
+def test_attention_zero_value_rows(n, where, dev):
+    """Value rows of zeros: all of them (o is 0, lse as ever), whole tiles, every other; the others far below 1."""
+    m = 1400
+    c = Case([n], [m], dev, hq=6, hkv=1, d=256, page=256, seed=7)
+    shift_values(c, 0, torch.full((m,), -30))
+    zero_values(c, {"all": range(m), "the first tiles": range(300), "the last tiles": range(1100, m),
+                    "every other": range(0, m, 2)}[where])
+    o, lse, ws = c.run()
+    ls.ls_read_device_status(ws)
+    check_times(c, o, lse, 2.0 ** 30)
