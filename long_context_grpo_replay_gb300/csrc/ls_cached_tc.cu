@@ -21,8 +21,8 @@
 //
 // A key's scale multiplies its scores; a pair, whose softmax is what there is
 // least of, folds it into the key's f16 values instead, relative to the tile's
-// largest (what that rounds, rows 2^10 times smaller and more, is 2^-33 of the
-// largest key's part of a score).  Value scales stay out of the product, whose
+// largest, where no key of the tile lies more than 15 binades below it: codes down
+// to 2^-9 times 2^-15 are f16 numbers, so the fold is exact.  Value scales stay out of the product, whose
 // small rows may be the ones that count: y = x + ev (base 2) is the score and the
 // exponent of the value row, w = 2^(y - m) the weight that multiplies codes.
 // Exponents are counted from the largest so far, B (of the part's tiles up to this
@@ -232,9 +232,9 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       bar_last, bar_pair[4], bar_drain;
   __shared__ uint32_t tmem_base_s;
   __shared__ int row_s[kBar][kBN];
-  // a key's scale: FOLD: 2^ek over the tile's largest, twice in f16; else the float32
+  // a key's scale: folded: 2^ek over the tile's largest, twice in f16; else the float32
   __shared__ __align__(16) uint32_t kh_s[E4 ? kBar : 1][kBN];
-  __shared__ float kmax_s[kBar];                 // 2^(the tile's largest ek)
+  __shared__ float kmax_s[kBar];                 // FOLD: 2^(the tile's largest ek), 0 for a tile that is not folded
   __shared__ int base_s[kBar];                   // the largest ev of the tiles so far
   __shared__ __align__(16) float ev_s[E4 ? kBar : 1][kBN], vi_s[E4 ? kBar : 1][kBN];
   __shared__ uint32_t there_s[kBar][4];
@@ -342,10 +342,18 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
           }
         }
         int top = -127;  // the largest scale of the tile's keys
-        if constexpr (E4) {
+        bool folded = false;
+        if constexpr (E4 && FOLD) {
+          int low = 127;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) top = row[x] >= 0 && ek[x] > top ? ek[x] : top;
+          for (int x = 0; x < 4; ++x) {
+            const bool in = row[x] >= 0 && ek[x] != -128;
+            top = in && ek[x] > top ? ek[x] : top;
+            low = in && ek[x] < low ? ek[x] : low;
+          }
           top = __reduce_max_sync(0xffffffffu, top);
+          low = __reduce_min_sync(0xffffffffu, low);
+          folded = top - low <= 15;  // also where there is none
           top = top == -127 ? 0 : top;
         }
         int base = -126;  // the largest value scale of the tile's keys
@@ -394,11 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
           const uint32_t m = __ballot_sync(0xffffffffu, row[x] >= 0);
           if (lane == 0) there_s[sl][x] = m;
           if constexpr (E4) {
-            if constexpr (!FOLD) kh_s[sl][x * 32 + lane] = __float_as_uint(exp_scale(ek[x]));
-            // 2^(ek - top) in f16 bits: normal to 2^-14, subnormal to 2^-24, then 0
-            const int dk = row[x] >= 0 ? top - ek[x] : 25;
-            const uint32_t h = ek[x] == -128 ? 0x7fffu : dk <= 14 ? (uint32_t)(15 - dk) << 10 : dk <= 24 ? 1u << (24 - dk) : 0u;
-            if constexpr (FOLD) kh_s[sl][x * 32 + lane] = h | h << 16;
+            // 2^(ek - top) in f16 bits, or 2^ek
+            const int dk = row[x] >= 0 ? top - ek[x] : 0;
+            const uint32_t h = ek[x] == -128 ? 0x7fffu : dk <= 14 ? (uint32_t)(15 - dk) << 10 : 0x200u;
+            kh_s[sl][x * 32 + lane] = folded ? h | h << 16 : __float_as_uint(exp_scale(ek[x]));
             // a NaN row reaches only the rows that see it: through the exponent
             const bool nan = ev[x] == -128;
             const int e = row[x] >= 0 ? max(ev[x] - base, -kValueSpan) : 0;
@@ -406,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
             vi_s[sl][x * 32 + lane] = nan ? 1.f : exp_scale(-e);
           }
         }
-        if (E4 && lane == 0) kmax_s[sl] = exp_scale(top);
+        if (E4 && lane == 0) kmax_s[sl] = folded ? exp_scale(top) : 0.f;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bar_rows[sl]));
       }
@@ -489,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
     int pc, rr, rs;      // of the chunk to load next
     const char* src = nullptr;
     const int* rows = nullptr;
-    const uint32_t* scales = nullptr;  // e4m3: of the rows of a K chunk
+    const uint32_t* scales = nullptr;  // of the rows of a K chunk that is folded
     auto source = [&](int c) -> bool {  // and waits for its rows
       int j;
       bool is_v;
@@ -508,7 +515,10 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       src = static_cast<const char*>(is_v ? p.c.v : p.c.k) +
             ((c % L::NCH) * L::CW + pc * PC + (PAIR && is_v ? rank * (D / 2) : 0)) * ES;
       rows = &row_s[j % kBar][rr + (PAIR && !is_v ? rank * 64 : 0)];
-      return wait(bar_rows[j % kBar], (j / kBar) & 1, __LINE__);
+      const bool in = wait(bar_rows[j % kBar], (j / kBar) & 1, __LINE__);
+      if constexpr (E4 && FOLD)
+        if (kmax_s[j % kBar] == 0.f) scales = nullptr;
+      return in;
     };
     // e4m3: the pieces of the next chunk; each is loaded as soon as its place is
     // converted, so that a group always has about a chunk in flight
@@ -671,18 +681,22 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
         }
       }
       if constexpr (E4) {
-        const float ct = FOLD ? crow * kmax_s[sl] : crow;
+        const bool by_key = !FOLD || kmax_s[sl] == 0.f;  // the keys' scales are still to be multiplied
+        const float ct = by_key ? crow : crow * kmax_s[sl];
         const uint64_t c2 = f2(ct, ct);
         const ulonglong2* kf = reinterpret_cast<const ulonglong2*>(&kh_s[sl][hf * 64]);
         const ulonglong2* ev = reinterpret_cast<const ulonglong2*>(&ev_s[sl][hf * 64]);
+        if (by_key) {
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const ulonglong2 e = ev[c];
-          if constexpr (!FOLD) {
+          for (int c = 0; c < 16; ++c) {
             const ulonglong2 f = kf[c];
             y[2 * c] = f2_mul(y[2 * c], f.x);
             y[2 * c + 1] = f2_mul(y[2 * c + 1], f.y);
           }
+        }
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const ulonglong2 e = ev[c];
           y[2 * c] = f2_fma(y[2 * c], c2, e.x);
           y[2 * c + 1] = f2_fma(y[2 * c + 1], c2, e.y);
         }

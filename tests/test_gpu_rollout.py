@@ -882,3 +882,27 @@ def test_attention_zero_value_rows(n, where, dev):
     o, lse, ws = c.run()
     ls.ls_read_device_status(ws)
     check_times(c, o, lse, 2.0 ** 30)
+
+
+@pytest.mark.parametrize("n", [1, 12, 40])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("down", [-4, -8, -10, -12, -20, -40, -100])
+def test_attention_quiet_keys_beside_zero_rows(n, d, down, dev):
+    """Keys 2^down of ordinary ones, with queries that make up for it, in tiles that also hold key rows of zeros
+    (written with exponent 0): the quiet keys' scores stay as they are."""
+    m = 700
+    c = Case([n], [m], dev, hq=8, hkv=1, d=d, page=256, seed=d, q_scale=2.0 ** -down)
+    page = 256
+    for j in range(m):
+        p, r = int(c.table[0, j // page]), j % page
+        if j % 7 == 0:
+            c.c["k"].view(torch.uint8)[p, :, r] = 0
+            c.c["k_exp"][p, :, r] = 0
+            c.keys[0][j] = 0
+        else:
+            c.c["k_exp"][p, :, r] += down
+            c.keys[0][j] *= 2.0 ** down
+    for causal in (True, False):
+        o, lse, ws = c.run(causal)
+        ls.ls_read_device_status(ws)
+        c.check(o, lse, causal)
