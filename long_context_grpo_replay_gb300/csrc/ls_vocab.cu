@@ -163,6 +163,10 @@ struct Product {
   }
 };
 
+// The number of this CTA's tile along the vocabulary, which may have more than the
+// 65,535 of a grid's second dimension: the third counts those.
+__device__ __forceinline__ uint32_t n_tile_of() { return blockIdx.z * gridDim.y + blockIdx.y; }
+
 // Forward: per row and the columns of one warp, (maximum, sum of
 // 2^(x - maximum)) of the logits in base 2, and the target's logit.
 template <int TM, int TX, typename T>
@@ -171,7 +175,9 @@ __global__ void __launch_bounds__(256, 2) vocab_fwd_kernel(const ls_vocab_desc d
   using P = Product<TM, TX, T, T>;
   constexpr int kLanes = TX < 32 ? TX : 32;  // of a warp that share a row; a row's warps leave statistics of their own
   __shared__ __align__(16) P sm;
-  const int64_t m0 = (int64_t)blockIdx.x * P::TILE_M, n0 = (int64_t)blockIdx.y * P::TILE_N;
+  const uint32_t n_tile = n_tile_of();
+  const int64_t m0 = (int64_t)blockIdx.x * P::TILE_M, n0 = (int64_t)n_tile * P::TILE_N;
+  if (n0 >= B.n) return;
   float acc[TM][TM];
   sm.run(A, B, m0, n0, 0, d.hidden, acc);
   const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
@@ -198,7 +204,7 @@ __global__ void __launch_bounds__(256, 2) vocab_fwd_kernel(const ls_vocab_desc d
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (threadIdx.x % kLanes == 0 && row < d.n_rows)
-      parts[((int64_t)blockIdx.y * (TX / kLanes) + threadIdx.x % TX / kLanes) * d.n_rows + row] = make_float2(top, sum);
+      parts[((int64_t)n_tile * (TX / kLanes) + threadIdx.x % TX / kLanes) * d.n_rows + row] = make_float2(top, sum);
   }
 }
 
@@ -248,7 +254,9 @@ __global__ void __launch_bounds__(256, 2) vocab_slope_kernel(const ls_vocab_desc
                                                           const float* d_logp, int64_t v0, int64_t np, float* out) {
   using P = Product<TM, TX, T, T>;
   __shared__ __align__(16) P sm;
-  const int64_t m0 = (int64_t)blockIdx.x * P::TILE_M, n0 = (int64_t)blockIdx.y * P::TILE_N;
+  const uint32_t n_tile = n_tile_of();
+  const int64_t m0 = (int64_t)blockIdx.x * P::TILE_M, n0 = (int64_t)n_tile * P::TILE_N;
+  if (n0 >= B.n) return;
   float acc[TM][TM];
   sm.run(A, B, m0, n0, 0, d.hidden, acc);
   const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
@@ -351,9 +359,11 @@ int64_t simt_per_split(const ls_vocab_desc& d) {
 }
 
 template <typename F>
-cudaError_t with_tile(int64_t m, int64_t n, Tile t, F f) {
-  const dim3 grid((unsigned)((m + tile_m(t) - 1) / tile_m(t)), (unsigned)((n + tile_n(t) - 1) / tile_n(t)));
-  if ((n + tile_n(t) - 1) / tile_n(t) > 65535) return cudaErrorInvalidConfiguration;
+cudaError_t with_tile(int64_t m, int64_t n, Tile t, bool layered, F f) {
+  const int64_t mt = (m + tile_m(t) - 1) / tile_m(t), nt = (n + tile_n(t) - 1) / tile_n(t), layers = (nt + 65534) / 65535;
+  if (mt > INT32_MAX || layers > (layered ? 65535 : 1)) return cudaErrorInvalidConfiguration;
+  // as many tiles a layer, so that a few may lie past the end
+  const dim3 grid((unsigned)mt, (unsigned)((nt + layers - 1) / layers), (unsigned)layers);
   using std::integral_constant;
   if (t == kWide)
     f(integral_constant<int, 4>{}, integral_constant<int, 64>{}, grid);
@@ -378,8 +388,9 @@ cudaError_t simt_fwd(const VocabParams& p, cudaStream_t s) {
   int n_tiles = 0;
   {
     LaunchScope ls(kKVocabSimt, s);
-    const cudaError_t e = with_tile(d.n_rows, d.vocab, pick_tile(d.n_rows, d.vocab), [&](auto tm, auto tx, dim3 grid) {
-      n_tiles = (int)grid.y * (tx.value < 32 ? 1 : tx.value / 32);
+    const Tile t = pick_tile(d.n_rows, d.vocab);
+    const cudaError_t e = with_tile(d.n_rows, d.vocab, t, true, [&](auto tm, auto tx, dim3 grid) {
+      n_tiles = (int)((d.vocab + tile_n(t) - 1) / tile_n(t)) * (tx.value < 32 ? 1 : tx.value / 32);
       vocab_fwd_kernel<tm.value, tx.value, T><<<grid, 256, 0, s>>>(d, A, B, p.targets, parts, hit);
     });
     if (e != cudaSuccess) return e;
@@ -400,7 +411,7 @@ cudaError_t simt_bwd(const VocabParams& p, cudaStream_t s) {
   for (int64_t v0 = 0; v0 < d.vocab; v0 += piece) {
     const int64_t np = d.vocab - v0 < piece ? d.vocab - v0 : piece;
     LaunchScope ls(kKVocabSimt, s);
-    cudaError_t e = with_tile(d.n_rows, np, pick_tile(d.n_rows, np), [&](auto tm, auto tx, dim3 grid) {
+    cudaError_t e = with_tile(d.n_rows, np, pick_tile(d.n_rows, np), true, [&](auto tm, auto tx, dim3 grid) {
       vocab_slope_kernel<tm.value, tx.value, T><<<grid, 256, 0, s>>>(d, operand(h, d.h_stride, 1, d.n_rows),
                                                            operand(w + v0 * d.w_stride, d.w_stride, 1, np), p.targets,
                                                            p.lse_in, p.d_logp, v0, np, slope);
@@ -409,7 +420,7 @@ cudaError_t simt_bwd(const VocabParams& p, cudaStream_t s) {
     if (p.dh) {
       const auto A = operand(static_cast<const float*>(slope), np, 1, d.n_rows);
       const auto B = operand(w + v0 * d.w_stride, 1, d.w_stride, d.hidden);
-      e = with_tile(d.n_rows, d.hidden, dh_tile(d), [&](auto tm, auto tx, dim3 grid) {
+      e = with_tile(d.n_rows, d.hidden, dh_tile(d), false, [&](auto tm, auto tx, dim3 grid) {
         ls.more_kernels(1);
         grid.z = (unsigned)((np + per - 1) / per);  // a shorter last piece has fewer
         if (direct)
@@ -422,7 +433,7 @@ cudaError_t simt_bwd(const VocabParams& p, cudaStream_t s) {
     if (p.dw) {
       const auto A = operand(static_cast<const float*>(slope), 1, np, np);
       const auto B = operand(h, 1, d.h_stride, d.hidden);
-      e = with_tile(np, d.hidden, pick_tile(np, d.hidden), [&](auto tm, auto tx, dim3 grid) {
+      e = with_tile(np, d.hidden, pick_tile(np, d.hidden), false, [&](auto tm, auto tx, dim3 grid) {
         ls.more_kernels(1);
         vocab_product_kernel<tm.value, tx.value, float, T, T><<<grid, 256, 0, s>>>(A, B, d.n_rows, d.n_rows, false, static_cast<T*>(p.dw) + v0 * d.hidden);
       });

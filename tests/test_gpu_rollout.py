@@ -906,3 +906,35 @@ def test_attention_quiet_keys_beside_zero_rows(n, d, down, dev):
         o, lse, ws = c.run(causal)
         ls.ls_read_device_status(ws)
         c.check(o, lse, causal)
+
+
+@pytest.mark.parametrize("n,d,v", [(20, 4, 65535 * 64 + 70), (1, 1, 65535 * 256 + 300)])
+def test_vocab_of_many_tiles(n, d, v, dev):
+    """More tiles of the vocabulary than a grid's second dimension holds."""
+    g = torch.Generator(device=dev).manual_seed(0)
+    h, w = torch.randn(n, d, generator=g, device=dev), torch.randn(v, d, generator=g, device=dev)
+    t = torch.randint(0, v, (n,), generator=g, device=dev)
+    t[0] = v - 1
+    dl = torch.randn(n, generator=g, device=dev)
+    desc = ls.vocab_desc(h, w)
+    ws = torch.zeros(ls.ls_vocab_logprob_workspace_size(desc, True), dtype=torch.uint8, device=dev)
+    logp, lse, dh, dw = torch.empty(n, device=dev), torch.empty(n, device=dev), torch.empty_like(h), torch.empty_like(w)
+    ls.ls_vocab_logprob_fwd(desc, h, w, t, logp, lse, ws)
+    ls.ls_vocab_logprob_bwd(desc, h, w, t, lse, dl, dh, dw, ws)
+    ls.ls_read_device_status(ws)
+    x = h.double() @ w.double().T
+    wl = torch.logsumexp(x, 1)
+    p = torch.exp(x - wl[:, None])
+    top = float(x.abs().max())
+    # a logit of d terms, and a sum of v terms of which each partial sum is rounded
+    dlse = (d + 4) * 2.0 ** -23 * top + 2.0 ** -16
+    assert (lse.double() - wl).abs().max() <= dlse
+    assert (logp.double() - (x.gather(1, t[:, None])[:, 0] - wl)).abs().max() <= 2 * dlse
+    slope = -p * dl.double()[:, None]
+    slope[torch.arange(n), t] += dl.double()
+    del x
+    mags = slope.abs()
+    err = (dh.double() - slope @ w.double()).abs()
+    assert (err <= 4 * dlse * (mags @ w.double().abs()) + 1e-30).all()
+    err = (dw.double() - slope.T @ h.double()).abs()
+    assert (err <= 4 * dlse * (mags.T @ h.double().abs()) + 1e-30).all()
