@@ -93,6 +93,7 @@ class KvCache(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("pool_pages", ctypes.c_int64),
                 ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
                 ("v_exp", ctypes.c_void_p)]
+    on_gpu = True  # kv_cache_from clears it for pools in host memory, which the calls refuse
 
 
 class CachedAttnDesc(ctypes.Structure):
@@ -445,6 +446,11 @@ def _want(t, dtype, shape, name):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _refuse_host():
+    """The kernels read addresses: a tensor of the host's must not reach them."""
+    raise ValueError("all tensors, and a cache's pools, must be on the GPU")
+
+
 def _token_stride(t, name):
     """Elements from one token to the next of a [n, heads, d] tensor whose heads are contiguous."""
     n, heads, d = t.shape
@@ -470,7 +476,9 @@ def kv_cache_from(k, v, k_exp=None, v_exp=None) -> KvCache:
         _want(k_exp, torch.int8, k.shape[:3], "k_exp")
         _want(v_exp, torch.int8, k.shape[:3], "v_exp")
     pages, hkv, page, d = k.shape
-    return KvCache(fmt, hkv, d, page, pages, _ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp))
+    cache = KvCache(fmt, hkv, d, page, pages, _ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp))
+    cache.on_gpu = all(t is None or t.is_cuda for t in (k, v, k_exp, v_exp))
+    return cache
 
 
 def _cache_rows(cache, slots, k, v):
@@ -486,8 +494,11 @@ def _cache_rows(cache, slots, k, v):
 def ls_cache_write(cache, k, v, slots, ws=None, stream=None):
     """Token t's rows of k, v [n, Hkv, d] (any token stride) into slot slots[t] (see ls.h)."""
     n = _cache_rows(cache, slots, k, v)
+    k_stride, v_stride = _token_stride(k, "k"), _token_stride(v, "v")
+    if not (k.is_cuda and v.is_cuda and slots.is_cuda and cache.on_gpu and (ws is None or ws.is_cuda)):
+        _refuse_host()
     _check(lib().ls_cache_write(cache, _dtype_code(k.dtype), k.data_ptr(), v.data_ptr(),
-                                _token_stride(k, "k"), _token_stride(v, "v"), slots.data_ptr(),
+                                k_stride, v_stride, slots.data_ptr(),
                                 n, _ptr(ws), 0 if ws is None else _nbytes(ws), _stream(stream)))
 
 
@@ -496,6 +507,8 @@ def ls_cache_read(cache, slots, k, v, ws=None, stream=None):
     n = _cache_rows(cache, slots, k, v)
     if not (k.is_contiguous() and v.is_contiguous()):
         raise ValueError("k and v must be contiguous")
+    if not (k.is_cuda and v.is_cuda and slots.is_cuda and cache.on_gpu and (ws is None or ws.is_cuda)):
+        _refuse_host()
     _check(lib().ls_cache_read(cache, slots.data_ptr(), n, _dtype_code(k.dtype), k.data_ptr(),
                                v.data_ptr(), _ptr(ws), 0 if ws is None else _nbytes(ws),
                                _stream(stream)))
@@ -529,6 +542,9 @@ def ls_cached_attn(desc, cache, q, q_start, kv_len, page_table, o, lse, ws, stre
     _want(kv_len, torch.int64, (desc.batch,), "kv_len")
     pages = page_table.shape[-1]
     _want(page_table, torch.int32, (desc.batch, pages), "page_table")
+    if not (q.is_cuda and q_start.is_cuda and kv_len.is_cuda and page_table.is_cuda and o.is_cuda and lse.is_cuda and
+            ws.is_cuda and cache.on_gpu):
+        _refuse_host()
     _check(lib().ls_cached_attn(desc, cache, q.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
                                 page_table.data_ptr(), pages, o.data_ptr(), lse.data_ptr(),
                                 ws.data_ptr(), _nbytes(ws), _stream(stream)))
@@ -569,6 +585,8 @@ def _vocab_check(desc, h, w, targets, *rows):
 def ls_vocab_logprob_fwd(desc, h, w, targets, logp, lse, ws, stream=None):
     """logp of targets [n] and the rows' lse, without the logits (see ls.h)."""
     _vocab_check(desc, h, w, targets, logp, lse)
+    if not all(t.is_cuda for t in (h, w, targets, logp, lse, ws)):
+        _refuse_host()
     _check(lib().ls_vocab_logprob_fwd(ctypes.byref(desc), _ptr(h), _ptr(w), _ptr(targets), _ptr(logp),
                                       _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
 
@@ -579,6 +597,8 @@ def ls_vocab_logprob_bwd(desc, h, w, targets, lse, d_logp, dh, dw, ws, stream=No
     for t, like, name in ((dh, h, "dh"), (dw, w, "dw")):
         if t is not None:
             _want(t, like.dtype, like.shape, name)
+    if not all(t is None or t.is_cuda for t in (h, w, targets, lse, d_logp, dh, dw, ws)):
+        _refuse_host()
     _check(lib().ls_vocab_logprob_bwd(ctypes.byref(desc), _ptr(h), _ptr(w), _ptr(targets), _ptr(lse),
                                       _ptr(d_logp), _ptr(dh), _ptr(dw), _ptr(ws), _nbytes(ws),
                                       _stream(stream)))

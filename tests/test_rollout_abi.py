@@ -148,3 +148,27 @@ def test_binding_checks_tensors(ls):
     with pytest.raises(TypeError):
         ls.ls_vocab_logprob_fwd(vd, h, torch.zeros(10, 64), torch.zeros(3, dtype=torch.int32), torch.zeros(3),
                                 torch.zeros(3), torch.zeros(1))
+
+
+def test_binding_refuses_host_tensors(ls):
+    """Calls that are right but for tensors in host memory raise before anything is launched."""
+    bf, i64 = torch.bfloat16, torch.int64
+    k = torch.zeros(2, 4, 16, 64, dtype=bf)
+    c = ls.kv_cache_from(k, k.clone())
+    rows, slots = torch.zeros(3, 4, 64, dtype=bf), torch.zeros(3, dtype=i64)
+    q, ws = torch.zeros(3, 8, 64, dtype=bf), torch.zeros(1 << 20, dtype=torch.uint8)
+    d = ls.cached_attn_desc(q, q, 3, 1, 32)
+    h, w, n = torch.zeros(3, 64), torch.zeros(10, 64), lambda: torch.zeros(3)
+    vd = ls.vocab_desc(h, w)
+    attn = (q, torch.arange(4, dtype=torch.int32), torch.ones(3, dtype=i64), torch.zeros(3, 2, dtype=torch.int32),
+            q.clone(), torch.zeros(3, 8), ws)
+    on_gpu = ls.KvCache(*(getattr(c, f) for f, _ in ls.KvCache._fields_))  # the caller's word for its addresses
+    for cache in (c, on_gpu):
+        for call in (lambda: ls.ls_cache_write(cache, rows, rows, slots), lambda: ls.ls_cache_read(cache, slots, rows, rows),
+                     lambda: ls.ls_cached_attn(d, cache, *attn)):
+            with pytest.raises(ValueError, match="GPU"):
+                call()
+    with pytest.raises(ValueError, match="GPU"):
+        ls.ls_vocab_logprob_fwd(vd, h, w, slots, n(), n(), ws)
+    with pytest.raises(ValueError, match="GPU"):
+        ls.ls_vocab_logprob_bwd(vd, h, w, slots, n(), n(), h.clone(), w.clone(), ws)
