@@ -435,17 +435,18 @@ LS_API ls_status ls_cache_read(const ls_kv_cache* cache, const int64_t* slots, i
  * keys up to kv_len[b] - n + i, else all; o is the softmax's mean of V, lse
  * its natural log-sum-exp (scale included).  A token that sees no key
  * gives o = 0, lse = -infinity.  Rows of the pages past kv_len may hold
- * anything; a NaN in a key that a token sees makes that token's rows NaN (in
- * a bf16 or float32 value row, which weights of 0 multiply too, perhaps also
- * those of the sequence's earlier tokens in the call).  Without causal, several members' tokens over
- * a prompt that they share are one sequence; a float32 o and lse are then
- * parts for ls_lse_merge.
+ * anything; a NaN in a key that a token sees makes that token's rows NaN (a NaN
+ * or an infinity in a bf16 or float32 value row, which weights of 0 multiply too,
+ * perhaps also those of the sequence's earlier tokens in the call).  An E4M3 value
+ * row more than 2^80 times smaller than the sequence's largest may count as 2^-80
+ * of that.  Without causal, several members' tokens over a prompt that they
+ * share are one sequence; a float32 o and lse are then parts for ls_lse_merge.
  *   q_dtype / o_dtype: o_dtype is q_dtype or LS_DTYPE_F32.
- *   max_q, max_kv: upper bounds of the lengths, for planning and the
- *     workspace; a longer sequence of queries is refused on the device (its
- *     keys are not read, its o and lse hold nothing of use, the status word
- *     says so), a longer kv_len is computed, more slowly.  kv_len is at most pages_per_seq * S_p (more is
- *     cut there and reported).
+ *   max_q, max_kv: upper bounds of the lengths (max_q <= total_q <= batch *
+ *     max_q), for planning and the workspace; a longer sequence of queries is
+ *     refused on the device (its keys are not read, its o and lse hold nothing of
+ *     use, the status word says so), a longer kv_len is computed, more slowly.
+ *     kv_len is at most pages_per_seq * S_p (more is cut there and reported).
  *   q_stride: elements from one token of q to the next (a multiple of 8, at
  *     least Hq * d); o is contiguous. */
 typedef struct {

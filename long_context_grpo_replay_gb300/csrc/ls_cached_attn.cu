@@ -261,8 +261,9 @@ __global__ void __launch_bounds__(128) cached_simt_kernel(const CachedParams p) 
 // bf16: the values as they are, P rounded to bf16 once.
 //
 // Measured (24/4 heads, d 256, e4m3): 1,000,003 keys in 300 us (6.85 TB/s, a copy's
-// rate); 32 sequences up to 16,384 keys in 114 us (5.3 TB/s); 8 sequences of 1 to 5
-// tokens over bf16 pages of 16, 8 x 128, in 39 us.
+// rate); 32 sequences up to 16,384 keys in 116.5 us (5.2 TB/s; 132 where every value
+// row is zeros and is looked at); 8 sequences of 1 to 5 tokens over bf16 pages of 16,
+// 8 x 128, in 38 us.
 // ===========================================================================
 template <bool E4>
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -813,13 +814,15 @@ cudaError_t run_mma(const CachedParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Most rows that this kernel takes; more go to cached_tc_kernel.  By time on 100,000
-// keys (24/4 heads for d 256, 32/8 else), this kernel against that one: e4m3, d 256:
-// 12 rows 63 against 70 us, 18 rows 86 against 72; d 128: 24 rows 74 against 84, 28
-// rows 117 against 84; d 64: 32 rows 63 against 74, 48 rows 104 against 74.  bf16, d
-// 256: 12 rows 100 against 90 (6 rows of 8 sequences 70 and 70); d 128: 8 sequences of
-// up to 20 rows 43 against 49, 28 rows of one 121 against 88; d 64: 8 of up to 20 rows
-// 51 against 43.
+// Most rows that this kernel takes; more go to cached_tc_kernel.  By time (24/4 heads
+// for d 256, 32/8 else), this kernel against that one, for one sequence of 100,000
+// keys, 8 of 12,000 and one of 3,000.  At the most rows: e4m3, d 256, 12 rows: 68
+// against 72 us, 61 against 90, 20 and 20; d 128, 24 rows: 74 against 86, 90 against
+// 123, 20 and 20; d 64, 32 rows: 66 against 78, 72 against 113, 18 and 18.  bf16, d
+// 256, 6 rows: 96 against 90, 90 against 98, 16 against 18; d 128, 24 rows: 96 against
+// 88, 102 against 107, 18 and 18; d 64, 16 rows: 55 against 59, 57 against 90, 14
+// against 16.  Beyond, on 100,000 keys: e4m3, d 256, 18 rows 86 against 72; d 128, 28
+// rows 117 against 84; d 64, 48 rows 104 against 74; bf16, d 128, 28 rows 121 against 88.
 template <int D, bool E4>
 constexpr int kMmaRows = E4 ? (D == 256 ? 16 : D == 128 ? 24 : 32) : (D == 256 ? 8 : D == 128 ? 24 : 16);
 

@@ -43,9 +43,10 @@
 // unrolled loops and inlined timers a tile of e4m3 keys took 11,500 cycles,
 // most of them the issuing thread's misses (61 % hits).
 //
-// Measured (24/4 heads, d 256): 2048 tokens over 32,768 e4m3 keys 1.32 ms = 1.2
-// PFLOP/s (tensor pipe 61 % busy, issue slots 61 %); 8 tokens over 262,144 keys
-// 153 us = 3.5 TB/s (bound by filling the f16 tiles), in bf16 5.9 TB/s.
+// Measured (24/4 heads, d 256): 2048 tokens over 32,768 e4m3 keys 1.33 ms = 1.2
+// PFLOP/s (tensor pipe 60 % busy, issue slots 64 %), 1.39 where no tile is folded, 2.3
+// where every value row is zeros; in bf16 1.23 ms.  8 tokens over 262,144 keys 154 us
+// = 3.5 TB/s (bound by filling the f16 tiles), in bf16 183 us = 5.9 TB/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
