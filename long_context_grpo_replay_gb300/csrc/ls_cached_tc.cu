@@ -763,9 +763,10 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
         tmem_wait_st();
       }
       // a row that has seen no key keeps its reference at 0: -infinity gives a
-      // weight of 0, and a NaN stays one
-      const float ref = (m_run == -CUDART_INF_F ? 0.f : m_run) - kOff;
-      const uint64_t nref = f2(base - ref, base - ref), sc2 = f2(crow, crow);
+      // weight of 0, and a NaN stays one.  e4m3: r is the sum's reference too, so
+      // that what its subtraction rounds stays out of the result
+      const float r = m_run - base, ref = kOff - (m_run == -CUDART_INF_F ? 0.f : r);
+      const uint64_t nref = f2(ref, ref), sc2 = f2(crow, crow);
       uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
       const ulonglong2* vi = reinterpret_cast<const ulonglong2*>(&vi_s[E4 ? sl : 0][hf * 64]);
 #pragma unroll
@@ -805,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       const float sum = (p0 + p1) + (p2 + p3);
       if constexpr (E4) {
         // the larger reference holds for both; 0 where no key was seen yet
-        const float r = m_run - base, rn = fmaxf(r_run, r), at = rn == -CUDART_INF_F ? 0.f : rn;
+        const float rn = fmaxf(r_run, r), at = rn == -CUDART_INF_F ? 0.f : rn;
         l_run = l_run * ex2(r_run - at) + sum * ex2(r - at);
         r_run = rn;
       } else {
@@ -861,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1) cached_tc_kernel(const CachedPara
       }
     }
     if (row_ok && hf == 0) {
-      const float z = l == 0.f ? -CUDART_INF_F : (lref - kOff + __log2f(l)) * kLn2;
+      const float z = l == 0.f ? -CUDART_INF_F : (lref + log2f(E4 ? l * 0x1p-11f : l)) * kLn2;
       if (p.ns > 1)
         p.lse_parts[(int64_t)part * p.total_q * p.hq + out] = z;
       else

@@ -938,3 +938,20 @@ def test_vocab_of_many_tiles(n, d, v, dev):
     assert (err <= 4 * dlse * (mags @ w.double().abs()) + 1e-30).all()
     err = (dw.double() - slope.T @ h.double()).abs()
     assert (err <= 4 * dlse * (mags.T @ h.double().abs()) + 1e-30).all()
+
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("n", [1, 12, 40])
+@pytest.mark.parametrize("values", ["ordinary", "zero", "least", "large"])
+def test_attention_lse_of_a_few_keys(n, d, values, dev):
+    """One to five keys with scores near 0: lse is the logarithm of their number, whatever the values' scale."""
+    for m in (1, 2, 3, 5):
+        c = Case([n], [m], dev, hq=8, hkv=1, d=d, page=4, seed=m, q_scale=2.0 ** -20)
+        at = {"ordinary": 0, "zero": 0, "least": -116, "large": 100}[values]
+        shift_values(c, 0, torch.full((m,), at))
+        if values == "zero":
+            zero_values(c, range(m))
+        for causal in (True, False):
+            o, lse, ws = c.run(causal)
+            ls.ls_read_device_status(ws)
+            check_times(c, o, lse, 2.0 ** -at, causal)
