@@ -79,7 +79,8 @@ typedef enum {
   LS_ERR_WORKSPACE_TOO_SMALL = 3,
   LS_ERR_CUDA = 4,               /* a CUDA runtime/driver call failed */
   LS_ERR_DEVICE_BOUNDS = 5,      /* device saw a page id, slot, length or target out of range */
-  LS_ERR_DEVICE_TIMEOUT = 6      /* a device-side bounded wait ran out */
+  LS_ERR_DEVICE_TIMEOUT = 6,     /* a device-side bounded wait ran out */
+  LS_ERR_OUT_OF_PAGES = 7        /* sequences could not grow: no free page, or their table's row ended */
 } ls_status;
 
 typedef enum { LS_DTYPE_F32 = 0, LS_DTYPE_BF16 = 1 } ls_dtype;
@@ -518,6 +519,125 @@ LS_API ls_status ls_vocab_logprob_bwd(const ls_vocab_desc* desc, const void* h, 
                                       const int64_t* targets, const float* lse,
                                       const float* d_logp, void* dh, void* dw, void* ws,
                                       size_t ws_bytes, void* stream);
+
+/* Pages of a paged cache, kept on the device: which pages a sequence has, and
+ * who else has them.  One book serves the caches of all layers whose pages are
+ * numbered alike.
+ *   refs int32 [pool_pages]: how many table entries name the page, 0 if free;
+ *   page_table int32 [n_seqs][pages_per_seq], kv_len int64 [n_seqs]: as
+ *   ls_cached_attn takes them (a run of rows of a table is a table).  A sequence
+ *   of n tokens has its first ceil(n / S_p) entries; the others mean nothing.
+ * A new book is all zeros.  Page ids outside the pool in a table are left out
+ * and reported.  A call whose lists are not valid (a sequence out of range or
+ * named twice, a length out of range, q_start not rising from 0 to total_q)
+ * changes nothing but the results for the caller (slots and copies all -1), and
+ * is reported.  ws: ls_pages_workspace_size() bytes, for one call at a time. */
+typedef struct {
+  int32_t page_size;
+  int32_t n_seqs;
+  int32_t pages_per_seq;
+  int32_t pool_pages;
+  int32_t* refs;
+  int32_t* page_table;
+  int64_t* kv_len;
+} ls_page_book;
+
+LS_API ls_status ls_pages_workspace_size(const ls_page_book* book, size_t* bytes);
+
+/* Sequences drop tokens from their ends and take slots for new ones (a step of
+ * a rollout: the rejected drafts go, the next ones come).  For each i < n,
+ * sequence seqs[i] (i where seqs is NULL) keeps its first keep[i] tokens (all
+ * where keep is NULL) and grows by q_start[i+1] - q_start[i] (nothing where
+ * q_start is NULL); slots[t], t in q_start's order, gets the slot of each new
+ * token, as ls_cache_write takes it.  First all pages that are dropped lose a
+ * reference; then pages are taken in order of i, each time the free page of the
+ * lowest number.  A sequence that grows inside a page that others name too gets
+ * a page of its own for it: copies[i] = (from, to, rows), which the caller hands
+ * to ls_cache_copy_pages for every layer's cache before it writes; -1s where
+ * nothing is to be copied.  Where the free pages do not reach, or the table's
+ * row ends, the sequence does not grow (slots -1, which ls_cache_write leaves
+ * out), and the status word says so (LS_ERR_OUT_OF_PAGES); later ones still do
+ * if they need no page.
+ *   keep int64 [n]; q_start int32 [n+1]; slots int64 [total_q]; copies int32 [n][3]. */
+LS_API ls_status ls_pages_advance(const ls_page_book* book, int32_t n, const int32_t* seqs,
+                                  const int64_t* keep, const int32_t* q_start, int64_t total_q,
+                                  int64_t* slots, int32_t* copies, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/* Frees the pages of sequences seqs[i] (all n_seqs where seqs is NULL): length 0. */
+LS_API ls_status ls_pages_release(const ls_page_book* book, int32_t n, const int32_t* seqs,
+                                  void* ws, size_t ws_bytes, void* stream);
+
+/* Sequence dst[i] becomes the first lens[i] tokens (lens NULL: all) of sequence
+ * src[i], without a copy: its own pages are freed, src's gain a reference.  (The
+ * page that both end in is copied when one of them grows.)  The same src may be
+ * named many times; a dst must be named once and be no src. */
+LS_API ls_status ls_pages_fork(const ls_page_book* book, int32_t n, const int32_t* src,
+                               const int32_t* dst, const int64_t* lens, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/* Moves the pages in use to the front of the pool: with A of them, the k-th one
+ * numbered A or more goes to the k-th free one below A.  table_out and refs_out
+ * get the book's table and references after the moves (they may be the book's
+ * own); copies int32 [pool_pages / 2][3] gets the moves for ls_cache_copy_pages,
+ * -1s after the last. */
+LS_API ls_status ls_pages_compact(const ls_page_book* book, int32_t* table_out, int32_t* refs_out,
+                                  int32_t* copies, void* ws, size_t ws_bytes, void* stream);
+
+/* Copies rows of pages within a cache, K and V: for each i < n, the first
+ * copies[i][2] rows of page copies[i][0] to page copies[i][1], for every head.
+ * A negative page leaves the entry out; one past the pool, or more rows than a
+ * page has, is left out and reported (ws: the status word, or NULL).  A page
+ * must not be written by two entries, nor be read by one and written by another. */
+LS_API ls_status ls_cache_copy_pages(const ls_kv_cache* cache, const int32_t* copies, int64_t n,
+                                     void* ws, size_t ws_bytes, void* stream);
+
+/* Recurrent step of the gated-DeltaNet state (the layer of ls_gdn_replay_fwd),
+ * for one or a few new tokens of each sequence: the decoding of the layers that
+ * keep a fixed-size state.  Each sequence has a slot in a pool of states; its
+ * tokens t = q_start[b] .. q_start[b+1]-1 move the state on in order,
+ *   S <- exp(g_t) S;  S <- S + b_t (v_t - S k_t) k_t^T;  o_t = S q_t,
+ * from the state in slot state_in[b] (-1: a state of zeros) to slot
+ * state_out[b] (-1, or state_out NULL: not kept; the same slot: in place).  So a
+ * group forks the captured prompt's state by reading one slot and writing
+ * several, drafted tokens run ahead of a state that stays, and the accepted ones
+ * move it on by a second call with n_use.  A sequence without tokens copies its
+ * state.  A slot that is written must not be read or written by another
+ * sequence of the call.  All sums are float32.
+ *   dtype: of q, k, v and o; states, g and beta are float32.
+ *   key_heads divides heads: value head h takes q and k of head
+ *     h / (heads / key_heads).  q, k [total_q][key_heads][dk], v [total_q][heads][dv],
+ *     token strides in elements, multiples of 8 (rows of one projection as they
+ *     lie); g, beta [total_q][heads] and o [total_q][heads][dv] contiguous.
+ *   states [n_states][heads][dv][dk].  dk = dv = 128.
+ *   max_q: upper bound of a sequence's tokens (max_q <= total_q <= batch * max_q). */
+typedef struct {
+  int32_t dtype;
+  int32_t heads;
+  int32_t key_heads;
+  int32_t dk;
+  int32_t dv;
+  int32_t batch;
+  int32_t max_q;
+  int32_t reserved;
+  int64_t total_q;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  int64_t n_states;
+} ls_gdn_decode_desc;
+
+/* q_start int32 [batch+1], from 0 to total_q; n_use int32 [batch] or NULL: only
+ * the first n_use[b] tokens of sequence b count (the others' rows of o stay as
+ * they were); state_in int32 [batch]; state_out int32 [batch] or NULL; o or NULL.
+ * ws: 256 bytes, the status word, or NULL.  A sequence whose state_in, token
+ * range or n_use is out of range is left out and reported; a state_out past the
+ * pool is not written and reported. */
+LS_API ls_status ls_gdn_decode(const ls_gdn_decode_desc* desc, float* states, const void* q,
+                               const void* k, const void* v, const float* g, const float* beta,
+                               const int32_t* q_start, const int32_t* n_use,
+                               const int32_t* state_in, const int32_t* state_out, void* o, void* ws,
+                               size_t ws_bytes, void* stream);
 
 /* Synchronises the stream, then reports the device status word of ws
  * (LS_OK, LS_ERR_DEVICE_BOUNDS or LS_ERR_DEVICE_TIMEOUT) and clears it. */

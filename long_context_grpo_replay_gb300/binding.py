@@ -27,6 +27,8 @@ __all__ = [
     "kv_cache_from", "cached_attn_desc", "vocab_desc", "ls_cache_write", "ls_cache_read",
     "ls_cached_attn_workspace_size", "ls_cached_attn", "ls_vocab_logprob_workspace_size",
     "ls_vocab_logprob_fwd", "ls_vocab_logprob_bwd",
+    "PageBook", "page_book", "ls_pages_workspace_size", "ls_pages_advance", "ls_pages_release", "ls_pages_fork",
+    "ls_pages_compact", "ls_cache_copy_pages", "GdnDecodeDesc", "gdn_decode_desc", "ls_gdn_decode",
 ]
 
 LS_DTYPE_F32 = 0
@@ -43,6 +45,8 @@ EXPORTED_SYMBOLS = [
     "ls_gdn_workspace_size", "ls_gdn_replay_fwd", "ls_gdn_replay_bwd", "ls_stage_pages",
     "ls_cache_write", "ls_cache_read", "ls_cached_attn_workspace_size", "ls_cached_attn",
     "ls_vocab_logprob_workspace_size", "ls_vocab_logprob_fwd", "ls_vocab_logprob_bwd",
+    "ls_pages_workspace_size", "ls_pages_advance", "ls_pages_release", "ls_pages_fork", "ls_pages_compact",
+    "ls_cache_copy_pages", "ls_gdn_decode",
 ]
 
 
@@ -110,6 +114,21 @@ class VocabDesc(ctypes.Structure):
                 ("logit_scale", ctypes.c_float)]
 
 
+class PageBook(ctypes.Structure):
+    _fields_ = [("page_size", ctypes.c_int32), ("n_seqs", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
+                ("pool_pages", ctypes.c_int32), ("refs", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p)]
+    device = None  # page_book sets the tensors' device
+
+
+class GdnDecodeDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("heads", ctypes.c_int32), ("key_heads", ctypes.c_int32),
+                ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("max_q", ctypes.c_int32), ("reserved", ctypes.c_int32), ("total_q", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("n_states", ctypes.c_int64)]
+
+
 def library_path() -> Path:
     return Path(os.environ.get("LS_LIBRARY",
                                Path(__file__).resolve().parent / "_lib" / "libls.so"))
@@ -164,6 +183,13 @@ def lib() -> ctypes.CDLL:
         "ls_vocab_logprob_workspace_size": [ctypes.POINTER(VocabDesc), I32, ctypes.POINTER(SZ)],
         "ls_vocab_logprob_fwd": [ctypes.POINTER(VocabDesc), P, P, P, P, P, P, SZ, P],
         "ls_vocab_logprob_bwd": [ctypes.POINTER(VocabDesc), P, P, P, P, P, P, P, P, SZ, P],
+        "ls_pages_workspace_size": [ctypes.POINTER(PageBook), ctypes.POINTER(SZ)],
+        "ls_pages_advance": [ctypes.POINTER(PageBook), I32, P, P, P, I64, P, P, P, SZ, P],
+        "ls_pages_release": [ctypes.POINTER(PageBook), I32, P, P, SZ, P],
+        "ls_pages_fork": [ctypes.POINTER(PageBook), I32, P, P, P, P, SZ, P],
+        "ls_pages_compact": [ctypes.POINTER(PageBook), P, P, P, P, SZ, P],
+        "ls_cache_copy_pages": [ctypes.POINTER(KvCache), P, I64, P, SZ, P],
+        "ls_gdn_decode": [ctypes.POINTER(GdnDecodeDesc), P, P, P, P, P, P, P, P, P, P, P, P, SZ, P],
         "ls_read_device_status": [P, SZ, P],
         "ls_clear_device_status": [P, SZ, P],
         "ls_trace_enable": [I32],
@@ -602,6 +628,164 @@ def ls_vocab_logprob_bwd(desc, h, w, targets, lse, d_logp, dh, dw, ws, stream=No
     _check(lib().ls_vocab_logprob_bwd(ctypes.byref(desc), _ptr(h), _ptr(w), _ptr(targets), _ptr(lse),
                                       _ptr(d_logp), _ptr(dh), _ptr(dw), _ptr(ws), _nbytes(ws),
                                       _stream(stream)))
+
+
+def _one_gpu(*ts):
+    """All tensors (None aside) on the current device: the kernels read addresses, and run where the stream is."""
+    import torch
+    dev = ts[0].get_device()
+    if dev < 0:
+        _refuse_host()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            if not t.is_cuda:
+                _refuse_host()
+            raise ValueError("all tensors must be on one device")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on device {dev}, not on the current one")
+
+
+def page_book(refs, page_table, kv_len, page_size) -> PageBook:
+    """The book of a pool's pages: refs int32 [pool_pages], page_table int32 [n_seqs, pages_per_seq], kv_len
+    int64 [n_seqs].  The book holds addresses: keep the tensors alive."""
+    import torch
+    _want(refs, torch.int32, (refs.numel(),), "refs")
+    _want(kv_len, torch.int64, (kv_len.numel(),), "kv_len")
+    _want(page_table, torch.int32, (kv_len.numel(), page_table.shape[-1]), "page_table")
+    book = PageBook(page_size, kv_len.shape[0], page_table.shape[1], refs.shape[0], _ptr(refs), _ptr(page_table),
+                    _ptr(kv_len))
+    devs = {t.get_device() for t in (refs, page_table, kv_len)}
+    if len(devs) != 1:
+        raise ValueError("all tensors must be on one device")
+    book.device = devs.pop()
+    return book
+
+
+def ls_pages_workspace_size(book) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ls_pages_workspace_size(ctypes.byref(book), ctypes.byref(out)))
+    return out.value
+
+
+def _on_book(book, ws, *ts):
+    """ws and ts (None aside) on the book's device, the current one."""
+    _one_gpu(ws, *ts)
+    if book.device is not None and ws.get_device() != book.device:
+        if book.device < 0:
+            _refuse_host()
+        raise ValueError("all tensors must be on one device")
+
+
+def ls_pages_advance(book, q_start, slots, copies, ws, seqs=None, keep=None, stream=None):
+    """Sequences seqs[i] (None: 0 .. n-1) keep their first keep[i] tokens (None: all) and take slots for
+    q_start[i+1] - q_start[i] new ones (q_start None: nothing, with slots and copies None); see ls.h."""
+    import torch
+    if q_start is not None:
+        n = q_start.shape[0] - 1
+        _want(q_start, torch.int32, (n + 1,), "q_start")
+        _want(slots, torch.int64, (slots.numel(),), "slots")
+        _want(copies, torch.int32, (n, 3), "copies")
+    else:
+        if slots is not None or copies is not None:
+            raise ValueError("slots and copies go with q_start")
+        n = len(keep if keep is not None else seqs if seqs is not None else ())
+    if seqs is not None:
+        _want(seqs, torch.int32, (n,), "seqs")
+    if keep is not None:
+        _want(keep, torch.int64, (n,), "keep")
+    _on_book(book, ws, q_start, slots, copies, seqs, keep)
+    _check(lib().ls_pages_advance(book, n, _ptr(seqs), _ptr(keep), _ptr(q_start), 0 if slots is None else slots.shape[0],
+                                  _ptr(slots), _ptr(copies), ws.data_ptr(), _nbytes(ws), _stream(stream)))
+
+
+def ls_pages_release(book, ws, seqs=None, stream=None):
+    """Frees the pages of sequences seqs (None: of all); see ls.h."""
+    import torch
+    n = 0 if seqs is None else seqs.numel()
+    if seqs is not None:
+        _want(seqs, torch.int32, (n,), "seqs")
+    _on_book(book, ws, seqs)
+    if seqs is None or n:  # an empty list has no address, and names no sequence
+        _check(lib().ls_pages_release(book, n, _ptr(seqs), ws.data_ptr(), _nbytes(ws), _stream(stream)))
+
+
+def ls_pages_fork(book, src, dst, ws, lens=None, stream=None):
+    """Sequences dst[i] become the first lens[i] tokens (None: all) of sequences src[i]; see ls.h."""
+    import torch
+    n = src.numel()
+    _want(src, torch.int32, (n,), "src")
+    _want(dst, torch.int32, (n,), "dst")
+    if lens is not None:
+        _want(lens, torch.int64, (n,), "lens")
+    _on_book(book, ws, src, dst, lens)
+    _check(lib().ls_pages_fork(book, n, src.data_ptr(), dst.data_ptr(), _ptr(lens), ws.data_ptr(), _nbytes(ws),
+                               _stream(stream)))
+
+
+def ls_pages_compact(book, table_out, refs_out, copies, ws, stream=None):
+    """The book's table and references with the pages in use at the front of the pool, and the moves
+    copies [pool_pages // 2, 3] for ls_cache_copy_pages; see ls.h."""
+    import torch
+    _want(table_out, torch.int32, (book.n_seqs, book.pages_per_seq), "table_out")
+    _want(refs_out, torch.int32, (book.pool_pages,), "refs_out")
+    _want(copies, torch.int32, (book.pool_pages // 2, 3), "copies")
+    _on_book(book, ws, table_out, refs_out, copies)
+    _check(lib().ls_pages_compact(book, table_out.data_ptr(), refs_out.data_ptr(), copies.data_ptr(), ws.data_ptr(),
+                                  _nbytes(ws), _stream(stream)))
+
+
+def ls_cache_copy_pages(cache, copies, ws=None, stream=None):
+    """The first copies[i][2] rows of page copies[i][0] to page copies[i][1], K and V (see ls.h)."""
+    import torch
+    _want(copies, torch.int32, (copies.shape[0], 3), "copies")
+    _one_gpu(copies, ws)
+    if not cache.on_gpu:
+        _refuse_host()
+    _check(lib().ls_cache_copy_pages(cache, copies.data_ptr(), copies.shape[0], _ptr(ws),
+                                     0 if ws is None else _nbytes(ws), _stream(stream)))
+
+
+def gdn_decode_desc(q, k, v, states, batch, max_q) -> GdnDecodeDesc:
+    """Desc of ls_gdn_decode for q, k [total_q, key_heads, 128] and v [total_q, heads, 128] of one dtype
+    (any token stride that is a multiple of 8) and states [n_states, heads, 128, 128]."""
+    if q.shape != k.shape or q.dtype != k.dtype or v.dtype != q.dtype or v.shape[0] != q.shape[0]:
+        raise ValueError("q and k must share shape, and q, k and v dtype and tokens")
+    if states.dim() != 4 or states.shape[1] != v.shape[1] or not states.is_contiguous():
+        raise ValueError("states must be contiguous [n_states, heads, dv, dk]")
+    _want_f32(states)
+    if states.shape[2] != v.shape[2] or states.shape[3] != q.shape[2]:
+        raise ValueError("the states' rows and columns must be v's and k's dimensions")
+    return GdnDecodeDesc(_dtype_code(q.dtype), v.shape[1], q.shape[1], q.shape[2], v.shape[2], batch, max_q, 0,
+                         q.shape[0], _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"),
+                         states.shape[0])
+
+
+def ls_gdn_decode(desc, states, q, k, v, g, beta, q_start, state_in, state_out, o=None, ws=None, n_use=None,
+                  stream=None):
+    """New tokens of each sequence through its recurrent state, from slot state_in[b] to slot state_out[b]
+    (None: not kept); see ls.h."""
+    import torch
+    n, hk, dk = desc.total_q, desc.key_heads, desc.dk
+    shape = (n, desc.heads, desc.dv)
+    if q.shape != (n, hk, dk) or k.shape != (n, hk, dk) or v.shape != shape or _token_stride(q, "q") != desc.q_stride or \
+            _token_stride(k, "k") != desc.k_stride or _token_stride(v, "v") != desc.v_stride or \
+            _dtype_code(q.dtype) != desc.dtype or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v are not the tensors of the desc")
+    _want(states, torch.float32, (desc.n_states, desc.heads, desc.dv, dk), "states")
+    _want(g, torch.float32, (n, desc.heads), "g")
+    _want(beta, torch.float32, (n, desc.heads), "beta")
+    _want(q_start, torch.int32, (desc.batch + 1,), "q_start")
+    _want(state_in, torch.int32, (desc.batch,), "state_in")
+    if state_out is not None:
+        _want(state_out, torch.int32, (desc.batch,), "state_out")
+    if n_use is not None:
+        _want(n_use, torch.int32, (desc.batch,), "n_use")
+    if o is not None:
+        _want(o, q.dtype, shape, "o")
+    _one_gpu(states, q, k, v, g, beta, q_start, state_in, state_out, o, ws, n_use)
+    _check(lib().ls_gdn_decode(desc, states.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                               beta.data_ptr(), q_start.data_ptr(), _ptr(n_use), state_in.data_ptr(), _ptr(state_out),
+                               _ptr(o), _ptr(ws), 0 if ws is None else _nbytes(ws), _stream(stream)))
 
 
 def ls_read_device_status(ws, stream=None):

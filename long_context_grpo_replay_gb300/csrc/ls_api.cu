@@ -66,7 +66,8 @@ const char* kKernelNames[kNumKernelIds] = {
     "page_write",  "simt_fwd",   "tc_fwd",     "lse_merge", "bwd_preprocess",
     "simt_bwd_dq", "tc_bwd_dq",  "simt_dkdv",  "tc_dkdv",   "dq_reduce",
     "gdn_fwd",     "gdn_bwd",    "stage_pages", "cache_write", "cache_read",
-    "cached_simt", "cached_mma", "cached_tc", "cached_join", "vocab_simt", "vocab_tc", "vocab_reduce"};
+    "cached_simt", "cached_mma", "cached_tc", "cached_join", "vocab_simt", "vocab_tc", "vocab_reduce",
+    "gdn_decode", "pages", "page_copy"};
 
 }  // namespace
 
@@ -820,6 +821,9 @@ ls_status ls_read_device_status(void* ws, size_t ws_bytes, void* stream) {
   if (word & kStatusBadIndex)
     return fail(LS_ERR_DEVICE_BOUNDS, "a slot, length or target was out of range (status 0x%x)",
                 word);
+  if (word & kStatusNoPages)
+    return fail(LS_ERR_OUT_OF_PAGES, "a sequence could not grow: no free page, or its table's row ended (status 0x%x)",
+                word);
   return LS_OK;
 }
 
@@ -838,6 +842,7 @@ const char* ls_status_string(ls_status st) {
     case LS_ERR_CUDA: return "LS_ERR_CUDA";
     case LS_ERR_DEVICE_BOUNDS: return "LS_ERR_DEVICE_BOUNDS";
     case LS_ERR_DEVICE_TIMEOUT: return "LS_ERR_DEVICE_TIMEOUT";
+    case LS_ERR_OUT_OF_PAGES: return "LS_ERR_OUT_OF_PAGES";
   }
   return "LS_ERR_UNKNOWN";
 }

@@ -15,6 +15,7 @@ enum : uint32_t {
   kStatusBadPage = 1u,   // a page-table entry pointed outside the pool
   kStatusTimeout = 2u,   // a bounded device wait gave up
   kStatusBadIndex = 4u,  // a slot, length or target was out of range
+  kStatusNoPages = 8u,   // a sequence could not grow
 };
 
 // Bytes at the head of the workspace reserved for the status word.
@@ -51,6 +52,9 @@ enum KernelId : int32_t {
   kKVocabSimt,
   kKVocabTc,
   kKVocabReduce,
+  kKGdnDecode,
+  kKPages,
+  kKPageCopy,
   kNumKernelIds
 };
 
@@ -157,6 +161,7 @@ void set_last_error(const char* msg);
 
 ls_status fail(ls_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 ls_status check_ws(const void* ws, size_t ws_bytes, size_t need);
+ls_status check_cache(const ls_kv_cache* c);
 int device_sms();
 bool device_is_sm100_family();
 bool force_simt();  // LS_FORCE_SIMT is set
@@ -271,5 +276,53 @@ cudaError_t launch_vocab_simt_bwd(const VocabParams& p, cudaStream_t s);
 size_t vocab_tc_scratch(const ls_vocab_desc& d, bool with_grad);
 cudaError_t launch_vocab_tc_fwd(const VocabParams& p, cudaStream_t s);
 cudaError_t launch_vocab_tc_bwd(const VocabParams& p, cudaStream_t s);
+
+// Recurrent step of the gated-DeltaNet state (ls_gdn_decode.cu).
+struct GdnDecodeParams {
+  ls_gdn_decode_desc d;
+  float* states;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const float* beta;
+  const int32_t* q_start;
+  const int32_t* n_use;
+  const int32_t* state_in;
+  const int32_t* state_out;
+  void* o;
+  uint32_t* status;
+};
+cudaError_t launch_gdn_decode(const GdnDecodeParams& p, cudaStream_t s);
+
+// Pages of a cache (ls_pages.cu).  The work arrays lie after the status header.
+struct PagesParams {
+  ls_page_book b;
+  int32_t n;
+  const int32_t* seqs;   // advance; fork: the destinations
+  const int32_t* src;    // fork
+  const int64_t* keep;   // advance; fork: lengths
+  const int32_t* q_start;
+  int64_t total_q;
+  int64_t* slots;
+  int32_t* copies;
+  int32_t* table_out;
+  int32_t* refs_out;
+  bool drop_all;         // advance: keep nothing
+  int32_t* list;         // [pool_pages] free pages in order
+  int32_t* high;         // [pool_pages] compact: pages that move, in order
+  int32_t* rank;         // [pool_pages] compact: their places in `high`
+  int32_t* owner;        // [n_seqs]
+  int32_t* begin;        // [n_seqs] advance: first of its pages in `list`
+  int32_t* need;         // [n_seqs] advance: pages it takes, and two flags
+  int32_t* kept;         // [n_seqs] advance: tokens it keeps
+  uint32_t* status;
+};
+size_t pages_scratch(const ls_page_book& b);
+cudaError_t launch_pages_advance(const PagesParams& p, cudaStream_t s);
+cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t s);
+cudaError_t launch_pages_compact(const PagesParams& p, cudaStream_t s);
+cudaError_t launch_page_copy(const ls_kv_cache& c, const int32_t* copies, int64_t n, uint32_t* status,
+                             cudaStream_t s);
 
 }  // namespace ls

@@ -29,26 +29,6 @@ bool known_dtype(int32_t t) { return t == LS_DTYPE_F32 || t == LS_DTYPE_BF16; }
       return fail(LS_ERR_CUDA, "%s: %s", what, cudaGetErrorString(_e));           \
   } while (0)
 
-ls_status check_cache(const ls_kv_cache* c) {
-  if (!c) return fail(LS_ERR_INVALID_ARGUMENT, "cache is NULL");
-  if (c->format != LS_CACHE_F32 && c->format != LS_CACHE_BF16 && c->format != LS_CACHE_E4M3)
-    return fail(LS_ERR_INVALID_ARGUMENT, "cache format %d is not an ls_cache_format", c->format);
-  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
-    return fail(LS_ERR_UNSUPPORTED, "head_dim=%d: supported are 64, 128, 256", c->head_dim);
-  if (c->hkv < 1 || c->page_size < 1 || c->pool_pages < 1)
-    return fail(LS_ERR_INVALID_ARGUMENT, "cache hkv, page_size and pool_pages must be >= 1");
-  if (c->hkv > 65535) return fail(LS_ERR_UNSUPPORTED, "hkv %d > 65535", c->hkv);
-  if (!c->k || !c->v) return fail(LS_ERR_INVALID_ARGUMENT, "cache pools must be non-NULL");
-  if (!aligned(c->k, 16) || !aligned(c->v, 16))
-    return fail(LS_ERR_INVALID_ARGUMENT, "cache pools must be 16-byte aligned");
-  if (c->format == LS_CACHE_E4M3 && (!c->k_exp || !c->v_exp))
-    return fail(LS_ERR_INVALID_ARGUMENT, "an E4M3 cache needs k_exp and v_exp");
-  // rows are numbered in 32 bits by the kernels (their byte offsets in 64)
-  if (c->pool_pages > INT32_MAX / c->hkv / c->page_size)
-    return fail(LS_ERR_UNSUPPORTED, "a pool of more than 2^31-1 rows");
-  return LS_OK;
-}
-
 ls_status status_word(void* ws, size_t ws_bytes, uint32_t** status) {
   *status = nullptr;
   if (!ws) return LS_OK;
@@ -194,6 +174,27 @@ size_t vocab_need(const ls_vocab_desc& d, bool with_grad) {
 }
 
 }  // namespace
+
+ls_status check_cache(const ls_kv_cache* c) {
+  if (!c) return fail(LS_ERR_INVALID_ARGUMENT, "cache is NULL");
+  if (c->format != LS_CACHE_F32 && c->format != LS_CACHE_BF16 && c->format != LS_CACHE_E4M3)
+    return fail(LS_ERR_INVALID_ARGUMENT, "cache format %d is not an ls_cache_format", c->format);
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+    return fail(LS_ERR_UNSUPPORTED, "head_dim=%d: supported are 64, 128, 256", c->head_dim);
+  if (c->hkv < 1 || c->page_size < 1 || c->pool_pages < 1)
+    return fail(LS_ERR_INVALID_ARGUMENT, "cache hkv, page_size and pool_pages must be >= 1");
+  if (c->hkv > 65535) return fail(LS_ERR_UNSUPPORTED, "hkv %d > 65535", c->hkv);
+  if (!c->k || !c->v) return fail(LS_ERR_INVALID_ARGUMENT, "cache pools must be non-NULL");
+  if (!aligned(c->k, 16) || !aligned(c->v, 16))
+    return fail(LS_ERR_INVALID_ARGUMENT, "cache pools must be 16-byte aligned");
+  if (c->format == LS_CACHE_E4M3 && (!c->k_exp || !c->v_exp))
+    return fail(LS_ERR_INVALID_ARGUMENT, "an E4M3 cache needs k_exp and v_exp");
+  // rows are numbered in 32 bits by the kernels (their byte offsets in 64)
+  if (c->pool_pages > INT32_MAX / c->hkv / c->page_size)
+    return fail(LS_ERR_UNSUPPORTED, "a pool of more than 2^31-1 rows");
+  return LS_OK;
+}
+
 }  // namespace ls
 
 using namespace ls;
