@@ -592,6 +592,61 @@ LS_API ls_status ls_pages_compact(const ls_page_book* book, int32_t* table_out, 
 LS_API ls_status ls_cache_copy_pages(const ls_kv_cache* cache, const int32_t* copies, int64_t n,
                                      void* ws, size_t ws_bytes, void* stream);
 
+/* Verification of drafted tokens against the target's logits, and the draw of
+ * the token after them, from given random numbers: the tokens that come out are
+ * distributed as if each had been drawn from the target.  Rows lie as the query
+ * tokens of ls_cached_attn: sequence b has rows r = q_start[b] .. q_start[b+1]-1,
+ * tokens[r] its last token and then its drafts, and logits row r is for the
+ * token after tokens[r], so that it judges the draft tokens[r+1].  With
+ *   p_r(v) = exp(logit_scale * logits[r][v] - lse_r)   (1 / temperature in logit_scale)
+ * and q_r = draft_probs[r] what that draft was drawn from (draft_probs NULL: q_r is 1
+ * at the draft), the drafts are accepted while u[r] * q_r(x) < p_r(x).  At the row
+ * where that ends the next token is the least v with
+ *   sum_{j <= v} w_j > u_next[b] * sum_j w_j,
+ * w = max(p - q, 0) after a rejection (p where that is 0 everywhere) and p after the
+ * last draft.  So a sequence of n rows has 1 to n tokens come out: emitted[r] =
+ * accepted drafts, then the new token, then -1s; logp[r] = log p_r(emitted[r]), 0
+ * where there is none; n_emitted[b] their number; keep[b] = kv_len[b] - n +
+ * n_emitted[b], the tokens whose keys stay valid (what ls_pages_advance keeps and, as
+ * n_use, n_emitted makes ls_gdn_decode keep).  A sequence without rows has none:
+ * n_emitted 0, keep its kv_len.  Rows that judge no draft may hold anything in
+ * draft_probs and u.
+ *   logits may be -infinity or the type's lowest value (a masked token).  A row
+ *     that has no distribution (all -infinity, or a NaN or +infinity in it) accepts
+ *     nothing; where it had to give the next token, emitted is -1 there, n_emitted
+ *     counts the drafts before it, keep their keys and the last token's, and the
+ *     status word says so.  A draft outside [0, vocab) is rejected and reported.
+ *   The weights of the draw are good to 2^-31 each and their sums exact,
+ *     so that the token is the definition's also in a vocabulary of 10^5; an
+ *     acceptance within about 2^-20 of its border may fall either way.
+ *   dtype: of logits; draft_probs is float32.  Strides in elements, any. */
+typedef struct {
+  int32_t dtype;
+  int32_t vocab;
+  int32_t batch;
+  int32_t max_q;
+  int64_t total_q;
+  int64_t logits_stride;
+  int64_t draft_stride;
+  float logit_scale;
+} ls_verify_desc;
+
+LS_API ls_status ls_draft_verify_workspace_size(const ls_verify_desc* desc, size_t* bytes);
+
+/* logits [total_q][vocab], draft_probs [total_q][vocab] or NULL, tokens int64
+ * [total_q], q_start int32 [batch+1] from 0 to total_q, u float32 [total_q] and u_next
+ * float32 [batch] in [0, 1); n_emitted int32 [batch], emitted int64 [total_q], logp
+ * float32 [total_q] or NULL; kv_len and keep int64 [batch], or keep NULL.  max_q is an
+ * upper bound of a sequence's rows (max_q <= total_q <= batch * max_q); a sequence with
+ * more, or with rows outside [0, total_q), is left out (n_emitted 0, its rows of emitted
+ * and logp as they were, keep its kv_len) and reported. */
+LS_API ls_status ls_draft_verify(const ls_verify_desc* desc, const void* logits,
+                                 const float* draft_probs, const int64_t* tokens,
+                                 const int32_t* q_start, const float* u, const float* u_next,
+                                 const int64_t* kv_len, int32_t* n_emitted, int64_t* emitted,
+                                 float* logp, int64_t* keep, void* ws, size_t ws_bytes,
+                                 void* stream);
+
 /* Recurrent step of the gated-DeltaNet state (the layer of ls_gdn_replay_fwd),
  * for one or a few new tokens of each sequence: the decoding of the layers that
  * keep a fixed-size state.  Each sequence has a slot in a pool of states; its

@@ -28,7 +28,8 @@ __all__ = [
     "ls_cached_attn_workspace_size", "ls_cached_attn", "ls_vocab_logprob_workspace_size",
     "ls_vocab_logprob_fwd", "ls_vocab_logprob_bwd",
     "PageBook", "page_book", "ls_pages_workspace_size", "ls_pages_advance", "ls_pages_release", "ls_pages_fork",
-    "ls_pages_compact", "ls_cache_copy_pages", "GdnDecodeDesc", "gdn_decode_desc", "ls_gdn_decode",
+    "ls_pages_compact", "ls_cache_copy_pages", "VerifyDesc", "verify_desc", "ls_draft_verify_workspace_size",
+    "ls_draft_verify", "GdnDecodeDesc", "gdn_decode_desc", "ls_gdn_decode",
 ]
 
 LS_DTYPE_F32 = 0
@@ -46,7 +47,7 @@ EXPORTED_SYMBOLS = [
     "ls_cache_write", "ls_cache_read", "ls_cached_attn_workspace_size", "ls_cached_attn",
     "ls_vocab_logprob_workspace_size", "ls_vocab_logprob_fwd", "ls_vocab_logprob_bwd",
     "ls_pages_workspace_size", "ls_pages_advance", "ls_pages_release", "ls_pages_fork", "ls_pages_compact",
-    "ls_cache_copy_pages", "ls_gdn_decode",
+    "ls_cache_copy_pages", "ls_draft_verify_workspace_size", "ls_draft_verify", "ls_gdn_decode",
 ]
 
 
@@ -121,6 +122,12 @@ class PageBook(ctypes.Structure):
     device = None  # page_book sets the tensors' device
 
 
+class VerifyDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("vocab", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("max_q", ctypes.c_int32), ("total_q", ctypes.c_int64), ("logits_stride", ctypes.c_int64),
+                ("draft_stride", ctypes.c_int64), ("logit_scale", ctypes.c_float)]
+
+
 class GdnDecodeDesc(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("heads", ctypes.c_int32), ("key_heads", ctypes.c_int32),
                 ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("batch", ctypes.c_int32),
@@ -189,6 +196,8 @@ def lib() -> ctypes.CDLL:
         "ls_pages_fork": [ctypes.POINTER(PageBook), I32, P, P, P, P, SZ, P],
         "ls_pages_compact": [ctypes.POINTER(PageBook), P, P, P, P, SZ, P],
         "ls_cache_copy_pages": [ctypes.POINTER(KvCache), P, I64, P, SZ, P],
+        "ls_draft_verify_workspace_size": [ctypes.POINTER(VerifyDesc), ctypes.POINTER(SZ)],
+        "ls_draft_verify": [ctypes.POINTER(VerifyDesc), P, P, P, P, P, P, P, P, P, P, P, P, SZ, P],
         "ls_gdn_decode": [ctypes.POINTER(GdnDecodeDesc), P, P, P, P, P, P, P, P, P, P, P, P, SZ, P],
         "ls_read_device_status": [P, SZ, P],
         "ls_clear_device_status": [P, SZ, P],
@@ -743,6 +752,56 @@ def ls_cache_copy_pages(cache, copies, ws=None, stream=None):
         _refuse_host()
     _check(lib().ls_cache_copy_pages(cache, copies.data_ptr(), copies.shape[0], _ptr(ws),
                                      0 if ws is None else _nbytes(ws), _stream(stream)))
+
+
+def verify_desc(logits, batch, max_q, draft_probs=None, logit_scale=1.0) -> VerifyDesc:
+    """Desc of ls_draft_verify for logits [total_q, vocab] and draft_probs of their shape in float32, or None."""
+    stride = 0
+    if draft_probs is not None:
+        _want_f32(draft_probs)
+        if draft_probs.shape != logits.shape:
+            raise ValueError("draft_probs must have the logits' shape")
+        stride = _rows(draft_probs, "draft_probs")
+    return VerifyDesc(_dtype_code(logits.dtype), logits.shape[1], batch, max_q, logits.shape[0], _rows(logits, "logits"),
+                      stride, logit_scale)
+
+
+def ls_draft_verify_workspace_size(desc) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ls_draft_verify_workspace_size(ctypes.byref(desc), ctypes.byref(out)))
+    return out.value
+
+
+def ls_draft_verify(desc, logits, tokens, q_start, u, u_next, n_emitted, emitted, logp, ws, draft_probs=None, kv_len=None,
+                    keep=None, stream=None):
+    """Drafts against the target's logits and the token after them (see ls.h); logp and keep may be None."""
+    import torch
+    n, b = desc.total_q, desc.batch
+    if logits.shape != (n, desc.vocab) or _dtype_code(logits.dtype) != desc.dtype or _rows(logits, "logits") != desc.logits_stride:
+        raise ValueError("logits is not the tensor of the desc")
+    if draft_probs is not None:
+        if draft_probs.shape != logits.shape or _rows(draft_probs, "draft_probs") != desc.draft_stride:
+            raise ValueError("draft_probs is not the tensor of the desc")
+        _want_f32(draft_probs)
+    elif desc.draft_stride:
+        raise ValueError("the desc has draft_probs")
+    _want(tokens, torch.int64, (n,), "tokens")
+    _want(q_start, torch.int32, (b + 1,), "q_start")
+    _want(u, torch.float32, (n,), "u")
+    _want(u_next, torch.float32, (b,), "u_next")
+    _want(n_emitted, torch.int32, (b,), "n_emitted")
+    _want(emitted, torch.int64, (n,), "emitted")
+    if logp is not None:
+        _want(logp, torch.float32, (n,), "logp")
+    if keep is not None:
+        if kv_len is None:
+            raise ValueError("keep needs kv_len")
+        _want(keep, torch.int64, (b,), "keep")
+        _want(kv_len, torch.int64, (b,), "kv_len")
+    _one_gpu(logits, tokens, q_start, u, u_next, n_emitted, emitted, logp, ws, draft_probs, kv_len, keep)
+    _check(lib().ls_draft_verify(desc, logits.data_ptr(), _ptr(draft_probs), tokens.data_ptr(), q_start.data_ptr(), u.data_ptr(),
+                                 u_next.data_ptr(), _ptr(kv_len), n_emitted.data_ptr(), emitted.data_ptr(), _ptr(logp),
+                                 _ptr(keep), ws.data_ptr(), _nbytes(ws), _stream(stream)))
 
 
 def gdn_decode_desc(q, k, v, states, batch, max_q) -> GdnDecodeDesc:

@@ -22,7 +22,7 @@ LIB = LIBDIR / "libls.so"
 SOURCES = ["ls_api.cu", "ls_simt.cu", "ls_tc_fwd.cu", "ls_tc_bwd.cu", "ls_tc_dkdv.cu", "ls_noalloc.cu",
            "ls_gdn.cu", "ls_gdn_cp.cu", "ls_rollout_api.cu", "ls_cache.cu", "ls_cached_attn.cu",
            "ls_cached_tc.cu", "ls_vocab.cu", "ls_vocab_tc.cu", "ls_drafts_api.cu",
-           "ls_gdn_decode.cu", "ls_pages.cu"]
+           "ls_gdn_decode.cu", "ls_pages.cu", "ls_verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -67,7 +67,7 @@ const char* kKernelNames[kNumKernelIds] = {
     "simt_bwd_dq", "tc_bwd_dq",  "simt_dkdv",  "tc_dkdv",   "dq_reduce",
     "gdn_fwd",     "gdn_bwd",    "stage_pages", "cache_write", "cache_read",
     "cached_simt", "cached_mma", "cached_tc", "cached_join", "vocab_simt", "vocab_tc", "vocab_reduce",
-    "gdn_decode", "pages", "page_copy"};
+    "gdn_decode", "pages", "page_copy", "verify_rows", "verify_draw"};
 
 }  // namespace
 

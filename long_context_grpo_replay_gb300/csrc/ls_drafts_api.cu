@@ -1,6 +1,7 @@
 // Host side of the entry points of a rollout with drafted tokens: pages of a
-// cache and the recurrent step of the gated-DeltaNet state.  Validation and
-// dispatch; the kernels are in ls_pages.cu and ls_gdn_decode.cu.
+// cache, verification of drafts and the recurrent step of the gated-DeltaNet
+// state.  Validation and dispatch; the kernels are in ls_pages.cu, ls_verify.cu
+// and ls_gdn_decode.cu.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -98,6 +99,24 @@ ls_status pages_params(const ls_page_book* b, int64_t n, void* ws, size_t ws_byt
   return LS_OK;
 }
 
+ls_status check_verify(const ls_verify_desc* d) {
+  if (!d) return fail(LS_ERR_INVALID_ARGUMENT, "desc is NULL");
+  if (!known_dtype(d->dtype))
+    return fail(LS_ERR_INVALID_ARGUMENT, "dtype %d is not LS_DTYPE_F32 or LS_DTYPE_BF16", d->dtype);
+  if (d->vocab < 1) return fail(LS_ERR_INVALID_ARGUMENT, "vocab < 1");
+  if (d->vocab > (1 << 30)) return fail(LS_ERR_UNSUPPORTED, "vocab %d > 2^30", d->vocab);
+  LS_CHECK(check_tokens(d->batch, d->total_q, d->max_q));
+  if (d->logits_stride < d->vocab) return fail(LS_ERR_INVALID_ARGUMENT, "logits_stride must be at least vocab");
+  if (!(d->logit_scale > 0.f) || !std::isfinite(d->logit_scale))
+    return fail(LS_ERR_INVALID_ARGUMENT, "logit_scale must be finite and > 0");
+  if (d->total_q * verify_chunks(*d) > INT32_MAX) return fail(LS_ERR_UNSUPPORTED, "total_q * vocab too large");
+  return LS_OK;
+}
+
+size_t verify_need(const ls_verify_desc& d) {
+  return kWsHeader + (size_t)d.total_q * verify_chunks(d) * sizeof(float2);
+}
+
 }  // namespace
 }  // namespace ls
 
@@ -192,6 +211,54 @@ ls_status ls_cache_copy_pages(const ls_kv_cache* cache, const int32_t* copies, i
   uint32_t* status;
   LS_CHECK(status_word(ws, ws_bytes, &status));
   LS_CUDA(launch_page_copy(*cache, copies, n, status, static_cast<cudaStream_t>(stream)), "page copy launch");
+  return LS_OK;
+}
+
+ls_status ls_draft_verify_workspace_size(const ls_verify_desc* desc, size_t* bytes) {
+  LS_CHECK(check_verify(desc));
+  if (!bytes) return fail(LS_ERR_INVALID_ARGUMENT, "bytes is NULL");
+  *bytes = verify_need(*desc);
+  return LS_OK;
+}
+
+ls_status ls_draft_verify(const ls_verify_desc* desc, const void* logits, const float* draft_probs,
+                          const int64_t* tokens, const int32_t* q_start, const float* u,
+                          const float* u_next, const int64_t* kv_len, int32_t* n_emitted,
+                          int64_t* emitted, float* logp, int64_t* keep, void* ws, size_t ws_bytes,
+                          void* stream) {
+  LS_CHECK(check_verify(desc));
+  if (desc->batch == 0) return LS_OK;
+  if (!q_start || !n_emitted || !u_next) return fail(LS_ERR_INVALID_ARGUMENT, "q_start, u_next and n_emitted must be non-NULL");
+  if (desc->total_q > 0 && (!logits || !tokens || !u || !emitted))
+    return fail(LS_ERR_INVALID_ARGUMENT, "logits, tokens, u and emitted must be non-NULL");
+  if (keep && !kv_len) return fail(LS_ERR_INVALID_ARGUMENT, "keep needs kv_len");
+  if (draft_probs && desc->draft_stride < desc->vocab)
+    return fail(LS_ERR_INVALID_ARGUMENT, "draft_stride must be at least vocab");
+  if (!aligned(logits, desc->dtype == LS_DTYPE_F32 ? 4 : 2) || !aligned(draft_probs, 4) || !aligned(tokens, 8) ||
+      !aligned(q_start, 4) || !aligned(u, 4) || !aligned(u_next, 4) || !aligned(kv_len, 8) || !aligned(n_emitted, 4) ||
+      !aligned(emitted, 8) || !aligned(logp, 4) || !aligned(keep, 8))
+    return fail(LS_ERR_INVALID_ARGUMENT, "buffers must be aligned to their elements");
+  LS_CHECK(check_ws(ws, ws_bytes, verify_need(*desc)));
+  VerifyParams p{};
+  p.d = *desc;
+  const double c = (double)desc->logit_scale * 1.4426950408889634074;
+  p.c = (float)c;
+  p.c_low = (float)(c - (double)p.c);
+  p.logits = logits;
+  p.probs = draft_probs;
+  p.tokens = tokens;
+  p.q_start = q_start;
+  p.u = u;
+  p.u_next = u_next;
+  p.kv_len = kv_len;
+  p.n_emitted = n_emitted;
+  p.emitted = emitted;
+  p.logp = logp;
+  p.keep = keep;
+  p.chunks = verify_chunks(*desc);
+  p.status = static_cast<uint32_t*>(ws);
+  p.parts = reinterpret_cast<float2*>(static_cast<char*>(ws) + kWsHeader);
+  LS_CUDA(launch_draft_verify(p, static_cast<cudaStream_t>(stream)), "draft verification launch");
   return LS_OK;
 }
 

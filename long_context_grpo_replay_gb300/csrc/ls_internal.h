@@ -55,6 +55,8 @@ enum KernelId : int32_t {
   kKGdnDecode,
   kKPages,
   kKPageCopy,
+  kKVerifyRows,
+  kKVerifyDraw,
   kNumKernelIds
 };
 
@@ -294,6 +296,28 @@ struct GdnDecodeParams {
   uint32_t* status;
 };
 cudaError_t launch_gdn_decode(const GdnDecodeParams& p, cudaStream_t s);
+
+// Verification of drafted tokens (ls_verify.cu).
+struct VerifyParams {
+  ls_verify_desc d;
+  float c, c_low;  // logit_scale * log2(e), and what its rounding to float32 left
+  const void* logits;
+  const float* probs;
+  const int64_t* tokens;
+  const int32_t* q_start;
+  const float* u;
+  const float* u_next;
+  const int64_t* kv_len;
+  int32_t* n_emitted;
+  int64_t* emitted;
+  float* logp;
+  int64_t* keep;
+  float2* parts;  // [total_q][chunks] (maximum, sum of the others' exponentials relative to it)
+  int32_t chunks;
+  uint32_t* status;
+};
+int verify_chunks(const ls_verify_desc& d);
+cudaError_t launch_draft_verify(const VerifyParams& p, cudaStream_t s);
 
 // Pages of a cache (ls_pages.cu).  The work arrays lie after the status header.
 struct PagesParams {

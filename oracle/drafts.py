@@ -1,6 +1,6 @@
 """Float64 definitions of the operators of a rollout with drafted tokens, written from
 their formulas (torch on the CPU; no code shared with the CUDA path): the recurrent step
-of the gated-DeltaNet state and the book of a cache's pages."""
+of the gated-DeltaNet state, the book of a cache's pages and the verification of drafts."""
 from __future__ import annotations
 
 import torch
@@ -93,3 +93,48 @@ class Book:
             self.refs[b], self.refs[a] = self.refs[a], 0
         self.table = [[to.get(p, p) for p in row] for row in self.table]
         return moves
+
+
+def verify(logits, probs, tokens, q_start, u, u_next, scale):
+    """Per sequence (emitted tokens, their log-probabilities, how near the nearest decision was to its border:
+    of an acceptance relative to p, of the draw relative to all weights).  logits, probs in any type on any
+    device; a sequence whose row has no distribution ends with the token None."""
+    out = []
+    for b in range(len(q_start) - 1):
+        toks, logp, near = [], [], float("inf")
+        for r in range(q_start[b], q_start[b + 1]):
+            x = logits[r].to(F64) * scale
+            x = x - x.max()          # before the logarithm: 64 bits lose log(n) beside a row of the type's lowest value
+            lse = torch.logsumexp(x, 0)
+            p = torch.exp(x - lse)
+            valid = bool(torch.isfinite(lse))
+            if r + 1 < q_start[b + 1]:
+                d = int(tokens[r + 1])
+                inside = 0 <= d < len(x)
+                q = probs[r].to(F64) if probs is not None else torch.zeros_like(p)
+                if probs is None and inside:
+                    q[d] = 1.0
+                if inside and valid:
+                    side = float(u[r]) * float(q[d]), float(p[d])
+                    near = min(near, abs(side[0] - side[1]) / max(*side, 1e-300))
+                    if side[0] < side[1]:
+                        toks.append(d), logp.append(float(x[d] - lse))
+                        continue
+                rest = (p - q).clamp(min=0)
+                if float(rest.sum()) > 2.0 ** -30:
+                    w = rest
+                else:
+                    w = p
+            else:
+                w = p
+            if not valid:
+                toks.append(None), logp.append(0.0)
+                break
+            upto = torch.cumsum(w, 0)
+            edge = float(u_next[b]) * float(upto[-1])
+            t = min(int((upto <= edge).sum()), len(x) - 1)
+            near = min(near, float((upto - edge).abs().min() / upto[-1]) * 2 ** 10 if len(x) > 1 else 1.0)
+            toks.append(t), logp.append(float(x[t] - lse))
+            break
+        out.append((toks, logp, near))
+    return out
