@@ -1,4 +1,4 @@
-// A cluster of C blocks as one team of threads (C = 1: a block alone).
+// A cluster of C blocks as one team of threads (C = 1: a block alone; C = 0: the launch says how many).
 #pragma once
 
 #include <stdint.h>
@@ -12,6 +12,12 @@ struct Cluster {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
+  }
+  static __device__ __forceinline__ uint32_t size() {
+    if constexpr (C != 0) return C;
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return n;
   }
   // Every thread of the cluster arrives; what each wrote before, to shared or
   // global memory, all may read after.

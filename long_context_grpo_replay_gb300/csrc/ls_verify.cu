@@ -5,24 +5,28 @@
 //   next token: least v with sum_{j<=v} w_j > u sum_j w_j,  w = max(p - q, 0) or p.
 //
 // Two kernels.  verify_rows_kernel reads every logit once: a (maximum, sum) pair
-// for each row and 16 KB of it, in base 2.  verify_draw_kernel, a cluster of eight
+// for each row and 16 KB of it, in base 2.  verify_draw_kernel, a cluster of up to eight
 // blocks for each sequence, joins them, tests the drafts and draws from the one
 // row where they end.
 //
 // The draw compares u with a running sum that has a step for every token, 10^5
 // of them in [0, 1): with sums good to 2^-24 one draw in a hundred would give a
-// neighbour of the definition's token.  So the draw's weights are formed anew as
-// integers in units of about 2^-61, whose sums do not depend on their order:
-//   w = 2^(n + j/256) (1 + d),  s log2(e) (z - max) = n + j/256 + r, |r| <= 2^-9,
-//   d = 2^r - 1 by three terms (the fourth is below 2^-42),
-// the argument as a pair of floats (a difference and a product with their exact
-// remainders), 2^(j/256) from a table (Tang's method: P. T. P. Tang, Table-driven
-// implementation of the exponential function, ACM TOMS 15, 1989), d in float32:
-// at most 2^-31 of each weight (2^-34.6 on average).  After a rejection w = max(e - q Z, 0) needs Z, the sum of
-// all e, before the first of them is known: the pass takes the row's float32 sum
-// Z0, and as Z is within 2^-20 of it, each partial sum is put right afterwards by
-// (Z - Z0) times the sum of its q where e > q Z0 (tokens within 2^-20 of that
-// border weigh 2^-20 of theirs, so that their side does not matter).
+// neighbour of the definition's token.  So the draw's weights are formed anew, to
+// 2^-31 of each or better, and summed without loss:
+//   e = 2^(s log2(e) (z - max)) = 2^(k/256) (1 + d),  d = 2^f - 1,  |f| <= 2^-8,
+// k/256 being z's product rounded to that grid less the maximum's (both exact),
+// f what is left of both, formed by fused multiply-adds; 2^(j/256) comes from a
+// table of pairs (Tang's method: P. T. P. Tang, Table-driven implementation of the
+// exponential function, ACM TOMS 15, 1989) and d from three terms (the fourth is
+// below 2^-38).  A weight, scaled so that all of them sum to less than 1, is split
+// at 2^-22: sums of the upper parts are exact in float32, those of the lower ones,
+// 2^-8.5 of the weights at most, good to 2^-32 of theirs.  Beyond a thread they are
+// integers in units of 2^-61, whose sums do not depend on their order.
+//   After a rejection w = max(e - q Z, 0) needs Z, the sum of all e, before the
+// first of them is known: the pass takes the row's float32 sum Z0, and as Z is
+// within 2^-20 of it, each partial sum is put right afterwards by (Z - Z0) times the
+// sum of its q where e > q Z0 (tokens within 2^-20 of that border weigh 2^-20 of
+// theirs, so that their side does not matter).
 #include <cuda_bf16.h>
 
 #include "ls_cluster.cuh"
@@ -33,13 +37,14 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kChunkBytes = 16384, kVectors = kChunkBytes / 16, kEach = kVectors / kThreads;
-constexpr int kCluster = 8, kSegments = kCluster * kWarps;
+constexpr int kMaxCluster = 8;
+constexpr int kTile = 256;  // elements a warp takes at a time in the draw, eight a lane
 
 // ---------------------------------------------------------------- 2^(j/256)
 struct Table {
-  uint64_t v[256];
+  float2 v[256];  // as a pair: its 24 upper bits, and the rest
 };
-// 2^(j/256) * 2^61, from square roots of 2 in integers (each off by less than 2^-60).
+// From square roots of 2 in integers of 62 bits (each off by less than 2^-60).
 constexpr uint64_t root(uint64_t x) {  // sqrt(x * 2^62)
   const unsigned __int128 n = (unsigned __int128)x << 62;
   uint64_t r = 0;
@@ -58,7 +63,8 @@ constexpr Table make_table() {
     uint64_t y = 1ull << 62;
     for (int i = 0; i < 8; ++i)
       if (j >> i & 1) y = (uint64_t)((unsigned __int128)y * roots[i] >> 62);
-    t.v[j] = (y + 1) >> 1;
+    const uint64_t upper = (y + (1ull << 38)) >> 39;
+    t.v[j] = float2{(float)upper * 0x1p-23f, (float)((int64_t)y - (int64_t)(upper << 39)) * 0x1p-62f};
   }
   return t;
 }
@@ -149,55 +155,49 @@ __global__ void __launch_bounds__(kThreads) verify_rows_kernel(const VerifyParam
 
 // ---------------------------------------------------------------- the draw
 struct Row {
-  float top;      // the row's maximum
+  float base;      // taken off every logit first: 0, or the maximum where the products would leave the grid
+  float bias;      // 1.5 * 2^15 less the maximum's product on the grid of 2^-8
+  float rest;      // the rest of that product
+  float least;     // below it a weight is 0 (2^-62 of the largest)
   float c, c_low;
-  int32_t k;      // weights are e * 2^(61 - k), Z in [2^60, 2^61) of them
-  uint32_t z0;    // 24 bits: Z0 = z0 * 2^37
+  uint32_t scale;  // exponent bits of 2^-k, with 2^-k Z in [0.5, 1)
+  float z0;        // 2^-k Z0
 };
+constexpr uint32_t kGrid = 0x47400000u;  // 1.5 * 2^15: a float near it is a multiple of 2^-8
 
-// e = 2^(c (z - top)) in the row's units.
-__device__ __forceinline__ uint64_t weight(float z, const Row& r, const uint64_t* table) {
-  const float s = z - r.top, back = s - z, rest = (z - (s - back)) - (r.top + back);
-  const float hi = s * r.c;
-  if (!(hi > -62.f)) return 0;
-  const float lo = fmaf(s, r.c, -hi) + fmaf(s, r.c_low, rest * r.c);
-  const float t = hi + 49152.f;  // 1.5 * 2^15: rounds to a multiple of 2^-8
-  const int k = __float_as_int(t) - __float_as_int(49152.f);
-  const float f = (hi - (t - 49152.f)) + lo;
-  const uint64_t w = table[k & 255];
-  const float d = f * fmaf(f, fmaf(f, 0.0555041087f, 0.240226507f), 0.693147181f);  // 2^f - 1: powers of ln 2
-  const float wide = __uint_as_float(0x3f000000u + (uint32_t)(w >> 38));            // the table's value in [1, 2)
-  const int64_t more = (int64_t)__float2int_rn(d * wide * 0x1p39f) << 22;
-  const int shift = r.k - (k >> 8);
-  return shift > 63 ? 0 : (w + more) >> shift;
+__device__ __forceinline__ Row make_row(float top, float sum, float c, float c_low) {
+  Row r;
+  r.c = c, r.c_low = c_low;
+  r.base = fabsf(top) * c > 8192.f ? top : 0.f;
+  const float m = top - r.base, hi = m * c;
+  const float grid = rintf(hi * 256.f) * 0x1p-8f;
+  r.rest = (hi - grid) + fmaf(m, c_low, fmaf(m, c, -hi));
+  r.bias = __uint_as_float(kGrid) - grid;
+  r.least = fmaxf(m - 62.f / c, -3.402823466e38f);
+  const uint32_t bits = __float_as_uint(sum);
+  r.scale = (253u - (bits >> 23)) << 23;                         // 127 - (exponent + 1)
+  r.z0 = __uint_as_float((bits & 0x7fffffu) | 0x3f000000u);
+  return r;
 }
 
-// q as m * 2^(e - 150); not a number below 2 (or NaN): more than any weight.
-struct Share {
-  uint32_t m;
-  int32_t e;
-};
-__device__ __forceinline__ Share share(float q) {
-  const uint32_t u = __float_as_uint(q), e = u >> 23;
-  Share s;
-  s.e = (int32_t)e;
-  s.m = e == 0 || e > 255 ? 0 : (u & 0x7fffffu) | 0x800000u;  // below 2^-126, or with a sign: 0
-  return s;
+// e = 2^(c (z - top)) in the row's units, as a sum of two floats: the lower one is
+// up to 2^-8.5 of the upper.
+__device__ __forceinline__ void weight(float z, const Row& r, const float2* table, float& upper, float& lower) {
+  const float v = z - r.base, s = fmaxf(v, r.least);
+  const float t = fmaf(s, r.c, r.bias);
+  const float f = fmaf(s, r.c, r.bias - t) + fmaf(s, r.c_low, -r.rest);
+  const uint32_t k = __float_as_uint(t);
+  const float2 w = table[k & 255u];
+  const float d = f * fmaf(f, fmaf(f, 0.0555041087f, 0.240226507f), 0.693147181f);  // powers of ln 2 over factorials
+  const float scale = v >= r.least ? __uint_as_float(((k & 0xffffff00u) << 15) + r.scale) : 0.f;
+  upper = w.x * scale;
+  lower = fmaf(w.x, d, w.y) * scale;
 }
-__device__ __forceinline__ int64_t times_z0(Share q, uint32_t z0) {
-  if (q.m == 0) return 0;
-  if (q.e >= 128) return INT64_MAX;
-  const uint64_t x = (uint64_t)q.m * z0;
-  const int shift = q.e - 113;
-  return shift >= 0 ? (int64_t)(x << shift) : shift < -63 ? 0 : (int64_t)(x >> -shift);
-}
-__device__ __forceinline__ int64_t times_z(Share q, uint64_t z) {
-  if (q.m == 0) return 0;
-  if (q.e >= 128) return INT64_MAX;
-  const uint64_t x = __umul64hi((uint64_t)q.m << 40, z);
-  const int shift = q.e - 126;
-  return shift >= 0 ? (int64_t)(x << shift) : shift < -63 ? 0 : (int64_t)(x >> -shift);
-}
+// The multiples of 2^-22 nearest to x in [0, 1).
+__device__ __forceinline__ float on_grid(float x) { return (x + 3.f) - 3.f; }
+
+// 2^61 times a sum of two floats below 1.
+__device__ __forceinline__ int64_t fixed(float a, float b) { return __float2ll_rn(a * 0x1p61f) + __float2ll_rn(b * 0x1p61f); }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
 #pragma unroll
@@ -230,28 +230,79 @@ __device__ __forceinline__ uint64_t part_of(float u, uint64_t c) {
   return 126 - e > 63 ? 0 : x >> (126 - e);
 }
 
-// Four elements from p, or fewer before `end`, as floats (zeros after it).
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, int at, int end, bool whole, float (&x)[4]) {
-  if (whole && at + 4 <= end) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 a = *reinterpret_cast<const float4*>(p + at);
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    } else {
-      const uint2 a = *reinterpret_cast<const uint2*>(p + at);
-      x[0] = __uint_as_float(a.x << 16), x[1] = __uint_as_float(a.x & 0xffff0000u);
-      x[2] = __uint_as_float(a.y << 16), x[3] = __uint_as_float(a.y & 0xffff0000u);
-    }
+// Eight logits of a row's elements v .. v+7 (16-byte aligned where all are in the row), -infinity outside it.
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, int v, int end, float (&x)[8]) {
+  if (v >= 0 && v + 8 <= end) {
+    unpack(*reinterpret_cast<const uint4*>(p + v), x);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = at + i < end ? value(p[at + i]) : 0.f;
+    for (int i = 0; i < 8; ++i) x[i] = v + i >= 0 && v + i < end ? __bfloat162float(p[v + i]) : -INFINITY;
   }
+}
+__device__ __forceinline__ void load8(const float* p, int v, int end, float (&x)[8]) {
+  if (v >= 0 && v + 8 <= end) {
+    const float4 a = *reinterpret_cast<const float4*>(p + v), b = *reinterpret_cast<const float4*>(p + v + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v + i >= 0 && v + i < end ? p[v + i] : -INFINITY;
+  }
+}
+// The drafts' probabilities beside them, in any alignment; what is not above 0 counts as 0.
+__device__ __forceinline__ void load8_share(const float* p, int v, int end, bool whole, float (&x)[8]) {
+  if (whole && v >= 0 && v + 8 <= end)
+    load8(p, v, end, x);
+  else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v + i >= 0 && v + i < end ? p[v + i] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = fmaxf(x[i], 0.f);
+}
+
+struct Sums {
+  uint64_t e, w;  // of all weights, and of those that the draw is from
+  float q;
+};
+// This lane's part of a segment: elements lo .. lo + each of the row, the first of them aligned.
+template <bool Q, typename T>
+__device__ __forceinline__ Sums segment(const T* z, const float* q, bool whole, int lo, int each, int end, const Row& r,
+                                        const float2* table) {
+  const int lane = threadIdx.x & 31;
+  float e0 = 0.f, e1 = 0.f, w0 = 0.f, w1 = 0.f, sum_q = 0.f;
+  for (int v = lo + lane * 8, stop = min(end, lo + each); v < stop; v += kTile) {
+    float x[8], y[8];
+    load8(z, v, end, x);
+    if constexpr (Q) load8_share(q, v, end, whole, y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float a, b;
+      weight(x[i], r, table, a, b);
+      const float a0 = on_grid(a), a1 = (a - a0) + b;
+      e0 += a0, e1 += a1;
+      if constexpr (Q) {
+        const float s = y[i] * r.z0, s0 = on_grid(s);
+        const float x0 = a0 - s0, x1 = a1 - ((s - s0) + fmaf(y[i], r.z0, -s));
+        if (x0 + x1 > 0.f) w0 += x0, w1 += x1, sum_q += y[i];
+      }
+    }
+  }
+  Sums s;
+  s.e = (uint64_t)fixed(e0, e1);
+  if constexpr (Q) {
+    const int64_t w = fixed(w0, w1);
+    s.w = w > 0 ? (uint64_t)w : 0;
+  } else {
+    s.w = s.e;
+  }
+  s.q = sum_q;
+  return s;
 }
 
 template <typename T>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) verify_draw_kernel(const VerifyParams p) {
-  using Team = Cluster<kCluster>;
-  __shared__ uint64_t table[256];
+__global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyParams p) {
+  using Team = Cluster<0>;
+  __shared__ float2 table[256];
   __shared__ float2 row_of[kWarps];
   __shared__ int passes[kWarps];
   __shared__ uint64_t seg_e[kWarps], seg_w[kWarps], scan[kWarps];
@@ -259,7 +310,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) ver
   __shared__ int picked, use_p;
   __shared__ uint64_t target, z_all;
   const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = Team::rank();
+  const uint32_t rank = Team::rank(), blocks = Team::size();
   table[tid] = kExp2.v[tid];
   const int64_t first = p.q_start[b], n64 = p.q_start[b + 1] - first;
   const bool bad = first < 0 || n64 < 0 || first + n64 > p.d.total_q || n64 > p.d.max_q;
@@ -324,40 +375,27 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) ver
     }
   }
   if (!some) return;  // all blocks of the cluster
-  Row w;
-  w.top = row.x, w.c = p.c, w.c_low = p.c_low;
-  w.k = (int)(__float_as_uint(row.y) >> 23) - 126;
-  w.z0 = (__float_as_uint(row.y) & 0x7fffffu) | 0x800000u;
+  const Row w = make_row(row.x, row.y, p.c, p.c_low);
   const T* z = logits + r * p.d.logits_stride;
   const float* q = p.probs && rejected ? p.probs + r * p.d.draft_stride : nullptr;
   const int64_t draft = rejected && !p.probs ? p.tokens[r + 1] : -1;
-  const bool whole = (reinterpret_cast<uintptr_t>(z) & (4 * sizeof(T) - 1)) == 0 && (reinterpret_cast<uintptr_t>(q) & 15) == 0;
-  // each warp its segment
-  const int each = (V + kSegments * 128 - 1) / (kSegments * 128) * 128;
+  // each warp its segment of the row; segments begin where 16-byte pieces do, `shift` elements before the row
+  const int shift = (int)(reinterpret_cast<uintptr_t>(z) & 15) / (int)sizeof(T);
+  const bool whole = (reinterpret_cast<uintptr_t>(q - shift) & 15) == 0;
+  const int segments = (int)blocks * kWarps, tiles = (V + shift + kTile - 1) / kTile;
+  const int each = (tiles + segments - 1) / segments * kTile;
   {
-    const int64_t lo = (int64_t)((int)rank * kWarps + warp) * each;
-    const int end = (int)(lo + each < V ? lo + each : V);
-    uint64_t sum_e = 0, sum_w = 0;
-    float sum_q = 0.f;
-    for (int64_t at = lo + lane * 4; at < end; at += 128) {
-      float x[4], y[4] = {0.f, 0.f, 0.f, 0.f};
-      load4(z, (int)at, end, whole, x);
-      if (q) load4(q, (int)at, end, whole, y);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (at + i >= end) continue;
-        const uint64_t e = weight(x[i], w, table);
-        sum_e += e;
-        if (q) {
-          const int64_t over = (int64_t)e - times_z0(share(y[i]), w.z0);
-          if (over > 0) sum_w += (uint64_t)over, sum_q += y[i];
-        } else if (at + i != draft) {
-          sum_w += e;
-        }
-      }
+    const int64_t lo = (int64_t)((int)rank * kWarps + warp) * each - shift;
+    Sums s{};
+    if (lo < V) s = q ? segment<true>(z, q, whole, (int)lo, each, V, w, table) : segment<false>(z, q, whole, (int)lo, each, V, w, table);
+    s.e = warp_sum(s.e), s.w = warp_sum(s.w), s.q = warp_sum(s.q);
+    if (draft >= 0 && draft >= lo && draft < lo + each && draft < V) {
+      float a, b;
+      weight(value(z[draft]), w, table, a, b);
+      const uint64_t x = (uint64_t)fixed(a, b);
+      s.w = s.w > x ? s.w - x : 0;
     }
-    sum_e = warp_sum(sum_e), sum_w = warp_sum(sum_w), sum_q = warp_sum(sum_q);
-    if (lane == 0) seg_e[warp] = sum_e, seg_w[warp] = sum_w, seg_q[warp] = sum_q;
+    if (lane == 0) seg_e[warp] = s.e, seg_w[warp] = s.w, seg_q[warp] = s.q;
   }
   Team::sync();
   if (warp == 0) {  // two segments a lane, neighbours
@@ -366,12 +404,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) ver
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int s = 2 * lane + i;
-      e[i] = Team::at(seg_e + s % kWarps, s / kWarps);
-      x[i] = Team::at(seg_w + s % kWarps, s / kWarps);
-      sq[i] = Team::at(seg_q + s % kWarps, s / kWarps);
+      const bool in = s < segments;
+      e[i] = in ? Team::at(seg_e + s % kWarps, s / kWarps) : 0;
+      x[i] = in ? Team::at(seg_w + s % kWarps, s / kWarps) : 0;
+      sq[i] = in ? Team::at(seg_q + s % kWarps, s / kWarps) : 0.f;
     }
     const uint64_t all = warp_sum(e[0] + e[1]);
-    const float off = (float)((int64_t)all - ((int64_t)w.z0 << 37));
+    const float off = (float)((int64_t)all - fixed(w.z0, 0.f));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int64_t fixed = q ? (int64_t)x[i] - __float2ll_rn(off * sq[i]) : (int64_t)x[i];
@@ -393,18 +432,20 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) ver
   __syncthreads();
   // the block that holds the segment looks into it
   if (picked / kWarps == (int)rank) {
-    const int64_t lo64 = (int64_t)picked * each;
-    const int lo = (int)lo64, end = (int)(lo64 + each < V ? lo64 + each : V);
-    const int per = (each + kThreads - 1) / kThreads;
-    const uint64_t all = z_all;
+    const int64_t from = (int64_t)picked * each - shift;
+    const int lo = from > 0 ? (int)from : 0, end = (int)(from + each < V ? from + each : V);
+    const int per = each / kThreads;
+    const float z_hi = (float)z_all * 0x1p-61f, z_lo = (float)((int64_t)z_all - fixed(z_hi, 0.f)) * 0x1p-61f;
     auto weigh = [&](int v) -> uint64_t {
-      const uint64_t e = weight(value(z[v]), w, table);
-      if (use_p) return e;
-      if (q) {
-        const int64_t over = (int64_t)e - times_z(share(q[v]), all);
-        return over > 0 ? (uint64_t)over : 0;
-      }
-      return v == draft ? 0 : e;
+      float a, b;
+      weight(value(z[v]), w, table, a, b);
+      if (use_p || !q) return v == draft && !use_p ? 0 : (uint64_t)fixed(a, b);
+      const float y = fmaxf(q[v], 0.f), s = y * z_hi, t = fmaf(y, z_lo, fmaf(y, z_hi, -s));
+      const float a0 = on_grid(a), s0 = on_grid(s);
+      const float x0 = a0 - s0, x1 = ((a - a0) + b) - ((s - s0) + t);
+      if (!(x0 + x1 > 0.f)) return 0;
+      const int64_t x = fixed(x0, x1);
+      return x > 0 ? (uint64_t)x : 0;
     };
     uint64_t sum = 0;
     int last = -1;  // the last token of this thread's that weighs anything
@@ -440,7 +481,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) ver
     }
     if (found >= 0) {
       p.emitted[r] = found;
-      if (p.logp) p.logp[r] = (value(z[found]) - w.top) * p.d.logit_scale - logf(row.y);
+      if (p.logp) p.logp[r] = (value(z[found]) - row.x) * p.d.logit_scale - logf(row.y);
     }
   }
   Team::sync();  // the sums are read by other blocks
@@ -465,12 +506,17 @@ cudaError_t launch_draft_verify(const VerifyParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   LaunchScope ls(kKVerifyDraw, s);
-  const dim3 grid(kCluster, p.d.batch);
-  if (p.d.dtype == LS_DTYPE_F32)
-    verify_draw_kernel<float><<<grid, kThreads, 0, s>>>(p);
-  else
-    verify_draw_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  // Blocks of a sequence: as many as let all sequences' run at once, three an SM.
+  int blocks = kMaxCluster;
+  while (blocks > 1 && (int64_t)blocks * p.d.batch > 4 * device_sms()) blocks /= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks, p.d.batch), cfg.blockDim = dim3(kThreads), cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = blocks, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+  cfg.attrs = &at, cfg.numAttrs = 1;
+  return p.d.dtype == LS_DTYPE_F32 ? cudaLaunchKernelEx(&cfg, verify_draw_kernel<float>, p)
+                                   : cudaLaunchKernelEx(&cfg, verify_draw_kernel<__nv_bfloat16>, p);
 }
 
 }  // namespace ls

@@ -148,7 +148,7 @@ def test_nothing_left_after_a_rejection(cuda_device):
 
 
 def test_probabilities_that_are_none(cuda_device):
-    """Rows of q with zeros, ones, infinities, NaN and negative numbers in places: a weight is never negative."""
+    """Rows of q with zeros, ones, infinities, NaN and negative numbers in places: what is not above 0 counts as 0."""
     m = make([2] * 6, 900, torch.float32, seed=10)
     m["u"][:] = 0.999999
     for b, x in enumerate((0.0, 1.0, math.inf, math.nan, -1.0, 3.0)):
@@ -158,8 +158,8 @@ def test_probabilities_that_are_none(cuda_device):
     count, out, _, _ = run(m)
     assert count.tolist() == [1] * 6
     probs = m["probs"].clone()
-    probs[m["q_start"][4], 100:500] = torch.where(probs[m["q_start"][4], 100:500] < 0, 0.0, probs[m["q_start"][4], 100:500])
-    probs[probs.isnan() | probs.isinf()] = 3.0
+    probs[probs.isnan() | (probs < 0)] = 0.0
+    probs[probs.isinf()] = 3.0
     check(dict(m, probs=probs), run(dict(m, probs=probs)))
     assert torch.equal(out, run(dict(m, probs=probs))[1])
 
