@@ -105,6 +105,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) verify_rows_kernel(const VerifyParams p) {
   constexpr int E = 16 / sizeof(T);
   __shared__ float2 warps[kWarps];
+  asm volatile("griddepcontrol.launch_dependents;");  // the draw's blocks set up while the last rows are read
   const int chunk = blockIdx.x % p.chunks, tid = threadIdx.x;
   const int64_t r = blockIdx.x / p.chunks;
   const T* row = static_cast<const T*>(p.logits) + r * p.d.logits_stride;
@@ -196,8 +197,15 @@ __device__ __forceinline__ void weight(float z, const Row& r, const float2* tabl
 // The multiples of 2^-22 nearest to x in [0, 1).
 __device__ __forceinline__ float on_grid(float x) { return (x + 3.f) - 3.f; }
 
-// 2^61 times a sum of two floats below 1.
-__device__ __forceinline__ int64_t fixed(float a, float b) { return __float2ll_rn(a * 0x1p61f) + __float2ll_rn(b * 0x1p61f); }
+// 2^61 times a float below 2, towards 0, by its bits (a conversion to 64 bits runs on the slow double pipe).
+__device__ __forceinline__ int64_t fixed(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const int shift = (int)((u >> 23) & 255u) - 89;  // the 24 bits count 2^(e - 150)
+  const uint64_t m = (u & 0x7fffffu) | 0x800000u;
+  const int64_t y = (int64_t)(shift >= 0 ? m << shift : shift > -24 ? m >> -shift : 0);
+  return (int32_t)u < 0 ? -y : y;
+}
+__device__ __forceinline__ int64_t fixed(float a, float b) { return fixed(a) + fixed(b); }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
 #pragma unroll
@@ -230,62 +238,88 @@ __device__ __forceinline__ uint64_t part_of(float u, uint64_t c) {
   return 126 - e > 63 ? 0 : x >> (126 - e);
 }
 
-// Eight logits of a row's elements v .. v+7 (16-byte aligned where all are in the row), -infinity outside it.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, int v, int end, float (&x)[8]) {
-  if (v >= 0 && v + 8 <= end) {
-    unpack(*reinterpret_cast<const uint4*>(p + v), x);
+// Elements v .. v+7 of a row, as they lie; `outside` for those before or after it.
+// whole: p + v is 16-byte aligned.
+template <typename T>
+struct Raw8 {
+  uint32_t w[2 * sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* p, int v, int end, bool whole, uint32_t outside) {
+  Raw8<T> r;
+  if (whole && v >= 0 && v + 8 <= end) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      const uint4 a = reinterpret_cast<const uint4*>(p + v)[i];
+      r.w[4 * i] = a.x, r.w[4 * i + 1] = a.y, r.w[4 * i + 2] = a.z, r.w[4 * i + 3] = a.w;
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = v + i >= 0 && v + i < end ? __bfloat162float(p[v + i]) : -INFINITY;
-  }
-}
-__device__ __forceinline__ void load8(const float* p, int v, int end, float (&x)[8]) {
-  if (v >= 0 && v + 8 <= end) {
-    const float4 a = *reinterpret_cast<const float4*>(p + v), b = *reinterpret_cast<const float4*>(p + v + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
+    for (int i = 0; i < 2 * (int)sizeof(T); ++i) r.w[i] = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = v + i >= 0 && v + i < end ? p[v + i] : -INFINITY;
+    for (int i = 0; i < 8; ++i) {
+      uint32_t x = outside;
+      if (v + i >= 0 && v + i < end) {
+        if constexpr (sizeof(T) == 4)
+          x = reinterpret_cast<const uint32_t*>(p)[v + i];
+        else
+          x = reinterpret_cast<const uint16_t*>(p)[v + i];
+      }
+      if constexpr (sizeof(T) == 4)
+        r.w[i] = x;
+      else
+        r.w[i / 2] |= x << (16 * (i & 1));
+    }
   }
+  return r;
 }
-// The drafts' probabilities beside them, in any alignment; what is not above 0 counts as 0.
-__device__ __forceinline__ void load8_share(const float* p, int v, int end, bool whole, float (&x)[8]) {
-  if (whole && v >= 0 && v + 8 <= end)
-    load8(p, v, end, x);
-  else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = v + i >= 0 && v + i < end ? p[v + i] : 0.f;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaxf(x[i], 0.f);
+template <typename T>
+__device__ __forceinline__ float element(const Raw8<T>& r, int i) {
+  if constexpr (sizeof(T) == 4)
+    return __uint_as_float(r.w[i]);
+  else
+    return __uint_as_float(i & 1 ? r.w[i / 2] & 0xffff0000u : r.w[i / 2] << 16);
 }
+// A row's logits, and the drafts' probabilities beside them (null: none).
+template <typename T>
+struct Source {
+  const T* z;
+  const float* q;
+  int end;
+  bool whole;  // q is aligned where z is
+  __device__ __forceinline__ Raw8<T> logits(int v) const { return load8(z, v, end, true, sizeof(T) == 4 ? 0xff800000u : 0xff80u); }
+  __device__ __forceinline__ Raw8<float> shares(int v) const { return load8(q, v, end, whole, 0u); }
+};
 
 struct Sums {
   uint64_t e, w;  // of all weights, and of those that the draw is from
   float q;
 };
-// This lane's part of a segment: elements lo .. lo + each of the row, the first of them aligned.
+// This lane's part of the elements lo .. stop-1 (lo where a 16-byte piece begins, perhaps before the row).
 template <bool Q, typename T>
-__device__ __forceinline__ Sums segment(const T* z, const float* q, bool whole, int lo, int each, int end, const Row& r,
-                                        const float2* table) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ Sums segment(const Source<T>& src, int lo, int stop, const Row& r, const float2* table) {
   float e0 = 0.f, e1 = 0.f, w0 = 0.f, w1 = 0.f, sum_q = 0.f;
-  for (int v = lo + lane * 8, stop = min(end, lo + each); v < stop; v += kTile) {
-    float x[8], y[8];
-    load8(z, v, end, x);
-    if constexpr (Q) load8_share(q, v, end, whole, y);
+  int v = lo + (threadIdx.x & 31) * 8;
+  Raw8<T> x = src.logits(v);
+  Raw8<float> y{};
+  if constexpr (Q) y = src.shares(v);
+  for (; v < stop; v += kTile) {
+    const Raw8<T> x1 = src.logits(v + kTile);  // under this tile's arithmetic
+    Raw8<float> y1{};
+    if constexpr (Q) y1 = src.shares(v + kTile);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float a, b;
-      weight(x[i], r, table, a, b);
+      weight(element(x, i), r, table, a, b);
       const float a0 = on_grid(a), a1 = (a - a0) + b;
       e0 += a0, e1 += a1;
       if constexpr (Q) {
-        const float s = y[i] * r.z0, s0 = on_grid(s);
-        const float x0 = a0 - s0, x1 = a1 - ((s - s0) + fmaf(y[i], r.z0, -s));
-        if (x0 + x1 > 0.f) w0 += x0, w1 += x1, sum_q += y[i];
+        const float q = fmaxf(element(y, i), 0.f), s = q * r.z0, s0 = on_grid(s);
+        const float d0 = a0 - s0, d1 = a1 - ((s - s0) + fmaf(q, r.z0, -s));
+        if (d0 + d1 > 0.f) w0 += d0, w1 += d1, sum_q += q;
       }
     }
+    x = x1, y = y1;
   }
   Sums s;
   s.e = (uint64_t)fixed(e0, e1);
@@ -300,7 +334,7 @@ __device__ __forceinline__ Sums segment(const T* z, const float* q, bool whole, 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kThreads, 4) verify_draw_kernel(const VerifyParams p) {
   using Team = Cluster<0>;
   __shared__ float2 table[256];
   __shared__ float2 row_of[kWarps];
@@ -324,6 +358,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyParam
   }
   const int n = (int)n64, V = p.d.vocab;
   const T* logits = static_cast<const T*>(p.logits);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' pairs are there
   // the drafts, a warp a row, up to the first that does not pass
   int stop = -1;
   float2 row{};
@@ -381,13 +416,14 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyParam
   const int64_t draft = rejected && !p.probs ? p.tokens[r + 1] : -1;
   // each warp its segment of the row; segments begin where 16-byte pieces do, `shift` elements before the row
   const int shift = (int)(reinterpret_cast<uintptr_t>(z) & 15) / (int)sizeof(T);
-  const bool whole = (reinterpret_cast<uintptr_t>(q - shift) & 15) == 0;
+  const Source<T> src{z, q, V, (reinterpret_cast<uintptr_t>(q - shift) & 15) == 0};
   const int segments = (int)blocks * kWarps, tiles = (V + shift + kTile - 1) / kTile;
   const int each = (tiles + segments - 1) / segments * kTile;
   {
     const int64_t lo = (int64_t)((int)rank * kWarps + warp) * each - shift;
+    const int stop = (int)(lo + each < V ? lo + each : V);
     Sums s{};
-    if (lo < V) s = q ? segment<true>(z, q, whole, (int)lo, each, V, w, table) : segment<false>(z, q, whole, (int)lo, each, V, w, table);
+    if (lo < V) s = q ? segment<true>(src, (int)lo, stop, w, table) : segment<false>(src, (int)lo, stop, w, table);
     s.e = warp_sum(s.e), s.w = warp_sum(s.w), s.q = warp_sum(s.q);
     if (draft >= 0 && draft >= lo && draft < lo + each && draft < V) {
       float a, b;
@@ -410,7 +446,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyParam
       sq[i] = in ? Team::at(seg_q + s % kWarps, s / kWarps) : 0.f;
     }
     const uint64_t all = warp_sum(e[0] + e[1]);
-    const float off = (float)((int64_t)all - fixed(w.z0, 0.f));
+    const float off = (float)((int64_t)all - fixed(w.z0));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int64_t fixed = q ? (int64_t)x[i] - __float2ll_rn(off * sq[i]) : (int64_t)x[i];
@@ -433,52 +469,68 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const VerifyParam
   // the block that holds the segment looks into it
   if (picked / kWarps == (int)rank) {
     const int64_t from = (int64_t)picked * each - shift;
-    const int lo = from > 0 ? (int)from : 0, end = (int)(from + each < V ? from + each : V);
-    const int per = each / kThreads;
-    const float z_hi = (float)z_all * 0x1p-61f, z_lo = (float)((int64_t)z_all - fixed(z_hi, 0.f)) * 0x1p-61f;
-    auto weigh = [&](int v) -> uint64_t {
-      float a, b;
-      weight(value(z[v]), w, table, a, b);
-      if (use_p || !q) return v == draft && !use_p ? 0 : (uint64_t)fixed(a, b);
-      const float y = fmaxf(q[v], 0.f), s = y * z_hi, t = fmaf(y, z_lo, fmaf(y, z_hi, -s));
-      const float a0 = on_grid(a), s0 = on_grid(s);
-      const float x0 = a0 - s0, x1 = ((a - a0) + b) - ((s - s0) + t);
-      if (!(x0 + x1 > 0.f)) return 0;
-      const int64_t x = fixed(x0, x1);
-      return x > 0 ? (uint64_t)x : 0;
-    };
-    uint64_t sum = 0;
-    int last = -1;  // the last token of this thread's that weighs anything
-    const int a0 = lo + tid * per, a1 = a0 + per < end ? a0 + per : end;
-    for (int v = a0; v < a1; ++v) {
-      const uint64_t x = weigh(v);
-      if (x) last = v;
-      sum += x;
-    }
-    uint64_t upto = warp_prefix(sum);
-    if (lane == 31) scan[warp] = upto;
-    passes[warp] = __reduce_max_sync(0xffffffffu, last);
-    __syncthreads();
-    uint64_t total = 0;
-    int most = -1;
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) upto += scan[i];
-      total += scan[i];
-      most = max(most, passes[i]);
-    }
-    // the segment's own sum may differ from the corrected one by rounding: its last token then
-    const uint64_t t = target < total ? target : total - 1;
-    int found = -1;
-    if (total == 0) {
-      if (tid == 0) found = lo;
-    } else if (t < upto && t >= upto - sum) {
-      uint64_t run = upto - sum;
-      for (int v = a0; v < a1 && found < 0; ++v) {
-        run += weigh(v);
-        if (run > t) found = v;
+    const int stop = (int)(from + each < V ? from + each : V);
+    const bool over_q = q && !use_p;
+    const int but = use_p ? -1 : (int)draft;
+    const float z_hi = (float)z_all * 0x1p-61f, z_lo = (float)((int64_t)z_all - fixed(z_hi)) * 0x1p-61f;
+    uint64_t t = target;  // of what the tiles before did not reach
+    int found = -1, last = -1;  // the last token so far that weighs anything
+    for (int64_t lo = from; lo < stop && found == -1; lo += kThreads * 8) {
+      const int v = (int)lo + tid * 8;
+      uint64_t x[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0;
+      if (v < stop) {
+        const Raw8<T> raw = src.logits(v);
+        Raw8<float> share{};
+        if (over_q) share = src.shares(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float a, b;
+          weight(element(raw, i), w, table, a, b);
+          int64_t e = 0;
+          if (over_q) {
+            const float y = fmaxf(element(share, i), 0.f), s = y * z_hi, rest = fmaf(y, z_lo, fmaf(y, z_hi, -s));
+            const float a0 = on_grid(a), s0 = on_grid(s), d0 = a0 - s0, d1 = ((a - a0) + b) - ((s - s0) + rest);
+            if (d0 + d1 > 0.f) e = fixed(d0, d1);
+          } else if (v + i != but) {
+            e = fixed(a, b);
+          }
+          if (v + i < stop && e > 0) x[i] = (uint64_t)e, sum += x[i];
+        }
       }
-      if (found < 0) found = most;
+      int mine = -1;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (x[i]) mine = v + i;
+      uint64_t upto = warp_prefix(sum);
+      if (lane == 31) scan[warp] = upto;
+      const int most = __reduce_max_sync(0xffffffffu, mine);
+      if (lane == 0) passes[warp] = most;
+      __syncthreads();
+      uint64_t total = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) upto += scan[i];
+        total += scan[i];
+        last = max(last, passes[i]);
+      }
+      if (t < total) {
+        found = -2;  // in this tile, by one thread
+        uint64_t run = upto - sum;
+        if (t >= run && t < upto)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            run += x[i];
+            if (found < 0 && run > t) found = v + i;
+          }
+      } else {
+        t -= total;
+      }
+      __syncthreads();
     }
+    // The segment's own sum may fall short of the corrected one by rounding: its last token then.
+    if (found == -1 && tid == 0) found = last >= 0 ? last : max((int)from, 0);
     if (found >= 0) {
       p.emitted[r] = found;
       if (p.logp) p.logp[r] = (value(z[found]) - row.x) * p.d.logit_scale - logf(row.y);
@@ -511,10 +563,12 @@ cudaError_t launch_draft_verify(const VerifyParams& p, cudaStream_t s) {
   while (blocks > 1 && (int64_t)blocks * p.d.batch > 4 * device_sms()) blocks /= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(blocks, p.d.batch), cfg.blockDim = dim3(kThreads), cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = blocks, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
-  cfg.attrs = &at, cfg.numAttrs = 1;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = blocks, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at, cfg.numAttrs = p.d.total_q > 0 ? 2 : 1;
   return p.d.dtype == LS_DTYPE_F32 ? cudaLaunchKernelEx(&cfg, verify_draw_kernel<float>, p)
                                    : cudaLaunchKernelEx(&cfg, verify_draw_kernel<__nv_bfloat16>, p);
 }
