@@ -134,6 +134,7 @@ class GdnDecodeDesc(ctypes.Structure):
                 ("max_q", ctypes.c_int32), ("reserved", ctypes.c_int32), ("total_q", ctypes.c_int64),
                 ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
                 ("n_states", ctypes.c_int64)]
+    layout = None  # gdn_decode_desc sets q's, k's and v's shapes and strides
 
 
 def library_path() -> Path:
@@ -639,19 +640,35 @@ def ls_vocab_logprob_bwd(desc, h, w, targets, lse, d_logp, dh, dw, ws, stream=No
                                       _stream(stream)))
 
 
+# The calls below are made once a step and layer, so their checks are one expression each where everything
+# is right; what is wrong is looked for afterwards, by the functions that name it.
+_torch = None
+
+
+def _lazy_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 def _one_gpu(*ts):
     """All tensors (None aside) on the current device: the kernels read addresses, and run where the stream is."""
     import torch
-    dev = ts[0].get_device()
-    if dev < 0:
+    ts = [t for t in ts if t is not None]
+    if not all(t.is_cuda for t in ts):
         _refuse_host()
-    for t in ts:
-        if t is not None and t.get_device() != dev:
-            if not t.is_cuda:
-                _refuse_host()
-            raise ValueError("all tensors must be on one device")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on device {dev}, not on the current one")
+    if len({t.get_device() for t in ts}) > 1:
+        raise ValueError("all tensors must be on one device")
+    if ts[0].get_device() != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on device {ts[0].get_device()}, not on the current one")
+
+
+def _stream_of(stream, dev):
+    """The stream's handle; the current one of device `dev` where it is None."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def page_book(refs, page_table, kv_len, page_size) -> PageBook:
@@ -678,38 +695,47 @@ def ls_pages_workspace_size(book) -> int:
 
 def _on_book(book, ws, *ts):
     """ws and ts (None aside) on the book's device, the current one."""
+    if book.device is not None and book.device < 0:
+        _refuse_host()
     _one_gpu(ws, *ts)
     if book.device is not None and ws.get_device() != book.device:
-        if book.device < 0:
-            _refuse_host()
         raise ValueError("all tensors must be on one device")
 
 
 def ls_pages_advance(book, q_start, slots, copies, ws, seqs=None, keep=None, stream=None):
     """Sequences seqs[i] (None: 0 .. n-1) keep their first keep[i] tokens (None: all) and take slots for
     q_start[i+1] - q_start[i] new ones (q_start None: nothing, with slots and copies None); see ls.h."""
-    import torch
+    torch = _torch or _lazy_torch()
+    i32 = torch.int32
     if q_start is not None:
-        n = q_start.shape[0] - 1
-        _want(q_start, torch.int32, (n + 1,), "q_start")
-        _want(slots, torch.int64, (slots.numel(),), "slots")
-        _want(copies, torch.int32, (n, 3), "copies")
+        n, total = q_start.shape[0] - 1, slots.shape[0]
+        if not (q_start.dtype is i32 and copies.dtype is i32 and slots.dtype is torch.int64 and q_start.is_contiguous() and
+                slots.is_contiguous() and copies.is_contiguous() and copies.shape == (n, 3) and q_start.dim() == slots.dim() == 1):
+            _want(q_start, i32, (n + 1,), "q_start")
+            _want(slots, torch.int64, (slots.numel(),), "slots")
+            _want(copies, i32, (n, 3), "copies")
+        at = q_start.data_ptr(), total, slots.data_ptr(), copies.data_ptr()
     else:
         if slots is not None or copies is not None:
             raise ValueError("slots and copies go with q_start")
         n = len(keep if keep is not None else seqs if seqs is not None else ())
+        at = None, 0, None, None
     if seqs is not None:
-        _want(seqs, torch.int32, (n,), "seqs")
+        _want(seqs, i32, (n,), "seqs")
     if keep is not None:
         _want(keep, torch.int64, (n,), "keep")
-    _on_book(book, ws, q_start, slots, copies, seqs, keep)
-    _check(lib().ls_pages_advance(book, n, _ptr(seqs), _ptr(keep), _ptr(q_start), 0 if slots is None else slots.shape[0],
-                                  _ptr(slots), _ptr(copies), ws.data_ptr(), _nbytes(ws), _stream(stream)))
+    dev = ws.get_device()
+    if dev < 0 or dev != book.device or dev != torch._C._cuda_getDevice() or \
+            (q_start is not None and not q_start.get_device() == slots.get_device() == copies.get_device() == dev) or \
+            (seqs is not None and seqs.get_device() != dev) or (keep is not None and keep.get_device() != dev):
+        _on_book(book, ws, q_start, slots, copies, seqs, keep)
+    _check(lib().ls_pages_advance(book, n, None if seqs is None else seqs.data_ptr(), None if keep is None else keep.data_ptr(),
+                                  *at, ws.data_ptr(), _nbytes(ws), _stream_of(stream, dev)))
 
 
 def ls_pages_release(book, ws, seqs=None, stream=None):
     """Frees the pages of sequences seqs (None: of all); see ls.h."""
-    import torch
+    torch = _torch or _lazy_torch()
     n = 0 if seqs is None else seqs.numel()
     if seqs is not None:
         _want(seqs, torch.int32, (n,), "seqs")
@@ -720,15 +746,20 @@ def ls_pages_release(book, ws, seqs=None, stream=None):
 
 def ls_pages_fork(book, src, dst, ws, lens=None, stream=None):
     """Sequences dst[i] become the first lens[i] tokens (None: all) of sequences src[i]; see ls.h."""
-    import torch
+    torch = _torch or _lazy_torch()
     n = src.numel()
-    _want(src, torch.int32, (n,), "src")
-    _want(dst, torch.int32, (n,), "dst")
+    if not (src.dtype is dst.dtype is torch.int32 and src.dim() == dst.dim() == 1 and dst.shape[0] == n and
+            src.is_contiguous() and dst.is_contiguous()):
+        _want(src, torch.int32, (n,), "src")
+        _want(dst, torch.int32, (n,), "dst")
     if lens is not None:
         _want(lens, torch.int64, (n,), "lens")
-    _on_book(book, ws, src, dst, lens)
+    dev = ws.get_device()
+    if dev < 0 or not dev == book.device == src.get_device() == dst.get_device() == torch._C._cuda_getDevice() or \
+            (lens is not None and lens.get_device() != dev):
+        _on_book(book, ws, src, dst, lens)
     _check(lib().ls_pages_fork(book, n, src.data_ptr(), dst.data_ptr(), _ptr(lens), ws.data_ptr(), _nbytes(ws),
-                               _stream(stream)))
+                               _stream_of(stream, dev)))
 
 
 def ls_pages_compact(book, table_out, refs_out, copies, ws, stream=None):
@@ -745,13 +776,15 @@ def ls_pages_compact(book, table_out, refs_out, copies, ws, stream=None):
 
 def ls_cache_copy_pages(cache, copies, ws=None, stream=None):
     """The first copies[i][2] rows of page copies[i][0] to page copies[i][1], K and V (see ls.h)."""
-    import torch
+    torch = _torch or _lazy_torch()
     _want(copies, torch.int32, (copies.shape[0], 3), "copies")
-    _one_gpu(copies, ws)
-    if not cache.on_gpu:
-        _refuse_host()
+    dev = copies.get_device()
+    if dev < 0 or not cache.on_gpu or dev != torch._C._cuda_getDevice() or (ws is not None and ws.get_device() != dev):
+        if not cache.on_gpu:
+            _refuse_host()
+        _one_gpu(copies, ws)
     _check(lib().ls_cache_copy_pages(cache, copies.data_ptr(), copies.shape[0], _ptr(ws),
-                                     0 if ws is None else _nbytes(ws), _stream(stream)))
+                                     0 if ws is None else _nbytes(ws), _stream_of(stream, dev)))
 
 
 def verify_desc(logits, batch, max_q, draft_probs=None, logit_scale=1.0) -> VerifyDesc:
@@ -775,8 +808,9 @@ def ls_draft_verify_workspace_size(desc) -> int:
 def ls_draft_verify(desc, logits, tokens, q_start, u, u_next, n_emitted, emitted, logp, ws, draft_probs=None, kv_len=None,
                     keep=None, stream=None):
     """Drafts against the target's logits and the token after them (see ls.h); logp and keep may be None."""
-    import torch
+    torch = _torch or _lazy_torch()
     n, b = desc.total_q, desc.batch
+    f32, i32, i64 = torch.float32, torch.int32, torch.int64
     if logits.shape != (n, desc.vocab) or _dtype_code(logits.dtype) != desc.dtype or _rows(logits, "logits") != desc.logits_stride:
         raise ValueError("logits is not the tensor of the desc")
     if draft_probs is not None:
@@ -785,23 +819,33 @@ def ls_draft_verify(desc, logits, tokens, q_start, u, u_next, n_emitted, emitted
         _want_f32(draft_probs)
     elif desc.draft_stride:
         raise ValueError("the desc has draft_probs")
-    _want(tokens, torch.int64, (n,), "tokens")
-    _want(q_start, torch.int32, (b + 1,), "q_start")
-    _want(u, torch.float32, (n,), "u")
-    _want(u_next, torch.float32, (b,), "u_next")
-    _want(n_emitted, torch.int32, (b,), "n_emitted")
-    _want(emitted, torch.int64, (n,), "emitted")
+    if not ((tokens.dtype, emitted.dtype, q_start.dtype, n_emitted.dtype, u.dtype, u_next.dtype) == (i64, i64, i32, i32, f32, f32) and
+            tokens.shape == emitted.shape == u.shape == (n,) and q_start.shape == (b + 1,) and u_next.shape == n_emitted.shape == (b,) and
+            tokens.is_contiguous() and emitted.is_contiguous() and q_start.is_contiguous() and n_emitted.is_contiguous() and
+            u.is_contiguous() and u_next.is_contiguous()):
+        _want(tokens, i64, (n,), "tokens")
+        _want(q_start, i32, (b + 1,), "q_start")
+        _want(u, f32, (n,), "u")
+        _want(u_next, f32, (b,), "u_next")
+        _want(n_emitted, i32, (b,), "n_emitted")
+        _want(emitted, i64, (n,), "emitted")
     if logp is not None:
-        _want(logp, torch.float32, (n,), "logp")
+        _want(logp, f32, (n,), "logp")
     if keep is not None:
         if kv_len is None:
             raise ValueError("keep needs kv_len")
-        _want(keep, torch.int64, (b,), "keep")
-        _want(kv_len, torch.int64, (b,), "kv_len")
-    _one_gpu(logits, tokens, q_start, u, u_next, n_emitted, emitted, logp, ws, draft_probs, kv_len, keep)
-    _check(lib().ls_draft_verify(desc, logits.data_ptr(), _ptr(draft_probs), tokens.data_ptr(), q_start.data_ptr(), u.data_ptr(),
-                                 u_next.data_ptr(), _ptr(kv_len), n_emitted.data_ptr(), emitted.data_ptr(), _ptr(logp),
-                                 _ptr(keep), ws.data_ptr(), _nbytes(ws), _stream(stream)))
+        _want(keep, i64, (b,), "keep")
+        _want(kv_len, i64, (b,), "kv_len")
+    dev = ws.get_device()
+    if dev < 0 or not (dev == logits.get_device() == tokens.get_device() == q_start.get_device() == u.get_device() ==
+                       u_next.get_device() == n_emitted.get_device() == emitted.get_device() == torch._C._cuda_getDevice()) or \
+            (logp is not None and logp.get_device() != dev) or (draft_probs is not None and draft_probs.get_device() != dev) or \
+            (keep is not None and not keep.get_device() == kv_len.get_device() == dev):
+        _one_gpu(logits, tokens, q_start, u, u_next, n_emitted, emitted, logp, ws, draft_probs, kv_len, keep)
+    _check(lib().ls_draft_verify(desc, logits.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(), tokens.data_ptr(),
+                                 q_start.data_ptr(), u.data_ptr(), u_next.data_ptr(), None if keep is None else kv_len.data_ptr(),
+                                 n_emitted.data_ptr(), emitted.data_ptr(), None if logp is None else logp.data_ptr(),
+                                 None if keep is None else keep.data_ptr(), ws.data_ptr(), _nbytes(ws), _stream_of(stream, dev)))
 
 
 def gdn_decode_desc(q, k, v, states, batch, max_q) -> GdnDecodeDesc:
@@ -814,15 +858,14 @@ def gdn_decode_desc(q, k, v, states, batch, max_q) -> GdnDecodeDesc:
     _want_f32(states)
     if states.shape[2] != v.shape[2] or states.shape[3] != q.shape[2]:
         raise ValueError("the states' rows and columns must be v's and k's dimensions")
-    return GdnDecodeDesc(_dtype_code(q.dtype), v.shape[1], q.shape[1], q.shape[2], v.shape[2], batch, max_q, 0,
+    desc = GdnDecodeDesc(_dtype_code(q.dtype), v.shape[1], q.shape[1], q.shape[2], v.shape[2], batch, max_q, 0,
                          q.shape[0], _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"),
                          states.shape[0])
+    desc.layout = q.shape, k.shape, v.shape, q.stride(), k.stride(), v.stride()
+    return desc
 
 
-def ls_gdn_decode(desc, states, q, k, v, g, beta, q_start, state_in, state_out, o=None, ws=None, n_use=None,
-                  stream=None):
-    """New tokens of each sequence through its recurrent state, from slot state_in[b] to slot state_out[b]
-    (None: not kept); see ls.h."""
+def _gdn_decode_check(desc, states, q, k, v, g, beta, q_start, state_in, state_out, o, n_use):
     import torch
     n, hk, dk = desc.total_q, desc.key_heads, desc.dk
     shape = (n, desc.heads, desc.dv)
@@ -841,10 +884,34 @@ def ls_gdn_decode(desc, states, q, k, v, g, beta, q_start, state_in, state_out, 
         _want(n_use, torch.int32, (desc.batch,), "n_use")
     if o is not None:
         _want(o, q.dtype, shape, "o")
-    _one_gpu(states, q, k, v, g, beta, q_start, state_in, state_out, o, ws, n_use)
+
+
+def ls_gdn_decode(desc, states, q, k, v, g, beta, q_start, state_in, state_out, o=None, ws=None, n_use=None,
+                  stream=None):
+    """New tokens of each sequence through its recurrent state, from slot state_in[b] to slot state_out[b]
+    (None: not kept); see ls.h."""
+    torch = _torch or _lazy_torch()
+    n, b, h = desc.total_q, desc.batch, desc.heads
+    f32, i32, dt = torch.float32, torch.int32, q.dtype
+    if not ((q.shape, k.shape, v.shape, q.stride(), k.stride(), v.stride()) == desc.layout and _CODES.get(dt) == desc.dtype and
+            (k.dtype, v.dtype, states.dtype, g.dtype, beta.dtype, q_start.dtype, state_in.dtype) == (dt, dt, f32, f32, f32, i32, i32) and
+            states.shape == (desc.n_states, h, desc.dv, desc.dk) and g.shape == beta.shape == (n, h) and q_start.shape == (b + 1,) and
+            state_in.shape == (b,) and states.is_contiguous() and g.is_contiguous() and beta.is_contiguous() and
+            q_start.is_contiguous() and state_in.is_contiguous() and
+            (state_out is None or (state_out.dtype is i32 and state_out.shape == (b,) and state_out.is_contiguous())) and
+            (n_use is None or (n_use.dtype is i32 and n_use.shape == (b,) and n_use.is_contiguous())) and
+            (o is None or (o.dtype is dt and o.shape == v.shape and o.is_contiguous()))):
+        _gdn_decode_check(desc, states, q, k, v, g, beta, q_start, state_in, state_out, o, n_use)
+    dev = states.get_device()
+    if dev < 0 or not (dev == q.get_device() == k.get_device() == v.get_device() == g.get_device() == beta.get_device() ==
+                       q_start.get_device() == state_in.get_device() == torch._C._cuda_getDevice()) or \
+            (state_out is not None and state_out.get_device() != dev) or (n_use is not None and n_use.get_device() != dev) or \
+            (o is not None and o.get_device() != dev) or (ws is not None and ws.get_device() != dev):
+        _one_gpu(states, q, k, v, g, beta, q_start, state_in, state_out, o, ws, n_use)
     _check(lib().ls_gdn_decode(desc, states.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-                               beta.data_ptr(), q_start.data_ptr(), _ptr(n_use), state_in.data_ptr(), _ptr(state_out),
-                               _ptr(o), _ptr(ws), 0 if ws is None else _nbytes(ws), _stream(stream)))
+                               beta.data_ptr(), q_start.data_ptr(), None if n_use is None else n_use.data_ptr(), state_in.data_ptr(),
+                               None if state_out is None else state_out.data_ptr(), None if o is None else o.data_ptr(),
+                               None if ws is None else ws.data_ptr(), 0 if ws is None else _nbytes(ws), _stream_of(stream, dev)))
 
 
 def ls_read_device_status(ws, stream=None):

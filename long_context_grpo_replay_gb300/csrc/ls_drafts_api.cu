@@ -57,6 +57,7 @@ ls_status check_gdn_decode(const ls_gdn_decode_desc* d) {
   if (d->dk != 128 || d->dv != 128)
     return fail(LS_ERR_UNSUPPORTED, "dk=%d dv=%d: supported is 128", d->dk, d->dv);
   LS_CHECK(check_tokens(d->batch, d->total_q, d->max_q));
+  if ((int64_t)d->batch * d->heads > INT32_MAX / 2) return fail(LS_ERR_UNSUPPORTED, "batch * heads too large");
   if (d->n_states < 1 || d->n_states > INT32_MAX)
     return fail(LS_ERR_INVALID_ARGUMENT, "n_states must be 1 .. 2^31-1");
   const int64_t key = (int64_t)d->key_heads * d->dk, val = (int64_t)d->heads * d->dv;

@@ -2,137 +2,276 @@
 // sequence move its state S [dv][dk] on (the recurrence of ls_gdn.cu),
 //   u = S k,  w = v - a u,  S <- a S + b w k^T,  o = S q,  a = exp(g).
 //
-// A row of S needs k, q and its own element of v alone, so rows are spread over
-// the whole device: a CTA takes 32 rows of one (sequence, head), eight lanes a
-// row with sixteen columns each in registers, all of a CTA's 16 KB loaded before
-// the first use.  The tokens then run over the registers; row products are
-// sixteen FMAs and three shuffles.
-#include <cuda_bf16.h>
-
+// A token does 7 operations an element of a state that has to come from memory
+// and go back, so the states' bytes bound it.  A row of S needs k, q and its own
+// element of v alone: the unit of work is half a head, 64 rows or 32 KB, for all
+// of a sequence's tokens.  Two blocks an SM take such units in turn; a producer
+// warp brings the coming ones into a ring of three stages by bulk copies (state,
+// and the tokens' k, q and v as they lie), so that some 190 KB an SM are on their
+// way whatever the others do.  Eight warps hold the rows in registers, eight lanes
+// a pair of rows with sixteen columns each, on packed pairs of floats; a row sum is
+// three shuffles for both rows.  The results leave by plain stores in whole lines.
 #include "ls_internal.h"
+#include "ls_tc.cuh"
 
 namespace ls {
 namespace {
 
-constexpr int kD = 128;        // dk = dv
-constexpr int kRows = 32;      // rows of a CTA
-constexpr int kLanes = 8;      // lanes of a row
-constexpr int kTokens = 8;     // tokens staged at a time
-constexpr int kThreads = kRows * kLanes;
+constexpr int kD = 128;                 // dk = dv
+constexpr int kRows = 64;               // rows of a unit
+constexpr int kWarps = 8;               // that compute
+constexpr int kThreads = kWarps * 32 + 32;
+constexpr int kStages = 3;
 
-__device__ __forceinline__ float value(float x) { return x; }
-__device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+struct Stage {
+  static constexpr int kTokens = 16 / (int)sizeof(T);  // a stage's
+  alignas(16) float s[kRows][kD];
+  alignas(16) T k[kTokens][kD], q[kTokens][kD], v[kTokens][kRows];
+  float g[kTokens], b[kTokens];
+  int64_t tok, from;                    // first token; element where the unit's rows begin in `states`, or -1
+  int32_t nt, head, row;                // tokens (-1: no more units)
+  int32_t first, last;                  // the unit begins, ends here
+};
+template <typename T>
+struct Shared {
+  Stage<T> stage[kStages];
+  alignas(8) uint64_t full[kStages], empty[kStages];
+  uint32_t abort;
+};
+
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ float value(float x) { return x; }
+__device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// Eight elements at p (16-byte aligned) to shared memory as float.
-__device__ __forceinline__ void stage8(const float* p, float* to) {
-  *reinterpret_cast<float4*>(to) = *reinterpret_cast<const float4*>(p);
-  *reinterpret_cast<float4*>(to + 4) = *reinterpret_cast<const float4*>(p + 4);
+// Four elements as two pairs of floats.
+__device__ __forceinline__ void pairs4(const float* p, uint64_t (&x)[2]) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(p);
+  x[0] = a.x, x[1] = a.y;
 }
-__device__ __forceinline__ void stage8(const __nv_bfloat16* p, float* to) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-  float x[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<float4*>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void pairs4(const __nv_bfloat16* p, uint64_t (&x)[2]) {
+  const uint2 a = *reinterpret_cast<const uint2*>(p);
+  x[0] = tc::f2(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u));
+  x[1] = tc::f2(__uint_as_float(a.y << 16), __uint_as_float(a.y & 0xffff0000u));
+}
+__device__ __forceinline__ float both(uint64_t x) {
+  float lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+  return lo + hi;
+}
+// Sums of x and y over eight lanes: x's in the lower four of them, y's in the others.
+__device__ __forceinline__ float sum_two(float x, float y, bool upper) {
+  float mine = upper ? y : x;
+  mine += __shfl_xor_sync(0xffffffffu, upper ? x : y, 4);
+  mine += __shfl_xor_sync(0xffffffffu, mine, 2);
+  mine += __shfl_xor_sync(0xffffffffu, mine, 1);
+  return mine;
 }
 
-__device__ __forceinline__ float dot4(const float4& a, const float4& b, float x) {
-  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, x))));
+// A float to shared memory; the barrier hears from the lane when all it asked for has come.
+__device__ __forceinline__ void fetch4(float* to, const float* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(to)), "l"(from) : "memory");
 }
-__device__ __forceinline__ float row_sum(float x) {
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+__device__ __forceinline__ void arrive_fetched(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// A sequence's place in the call, as loaded.
+struct Place {
+  int32_t first, end, use, in, out;
+};
+__device__ __forceinline__ Place place_of(const GdnDecodeParams& p, int b) {
+  Place x;
+  x.first = p.q_start[b], x.end = p.q_start[b + 1];
+  x.use = p.n_use ? p.n_use[b] : INT32_MIN;
+  x.in = p.state_in[b], x.out = p.state_out ? p.state_out[b] : -1;
   return x;
 }
 
+// The producer asks for everything and waits for nothing but room: no load's value is
+// used here but a unit's place, which is loaded one unit ahead.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) gdn_decode_kernel(const GdnDecodeParams p) {
-  __shared__ __align__(16) float ks[kTokens][kD], qs[kTokens][kD];
-  __shared__ float vs[kTokens][kRows], as[kTokens], bs[kTokens];
-  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const int row = blockIdx.x * kRows + tid / kLanes, lane = tid % kLanes;
-  const int64_t first = p.q_start[b];
-  const int64_t n_all = p.q_start[b + 1] - first;
-  const int64_t n = p.n_use ? p.n_use[b] : n_all;
-  const int64_t in = p.state_in[b];
-  int64_t out = p.state_out ? p.state_out[b] : -1;
-  if (first < 0 || n_all < 0 || first + n_all > p.d.total_q || n_all > p.d.max_q || n < 0 || n > n_all ||
-      in < -1 || in >= p.d.n_states) {
-    if (tid == 0 && p.status) atomicOr(p.status, kStatusBadIndex);
+__device__ __forceinline__ void produce(const GdnDecodeParams& p, Shared<T>& sh) {
+  constexpr int K = Stage<T>::kTokens;
+  const int lane = threadIdx.x & 31;
+  const int64_t units = (int64_t)p.d.batch * p.d.heads * 2;
+  int it = 0;
+  // The next stage, once the warps that compute have left it.
+  auto take = [&]() -> Stage<T>* {
+    const int s = it % kStages;
+    if (!__all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&sh.empty[s]), (it / kStages & 1) ^ 1, &sh.abort))) {
+      if (lane == 0) sh.abort = 1;
+      return nullptr;
+    }
+    return &sh.stage[s];
+  };
+  const uint32_t per_seq = 2u * p.d.heads;
+  Place next = place_of(p, (int)(blockIdx.x / per_seq));
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const uint32_t b = (uint32_t)unit / per_seq, in_seq = (uint32_t)unit - b * per_seq;
+    const int half = (int)(in_seq & 1), h = (int)(in_seq >> 1);
+    const Place at = next;
+    if (unit + gridDim.x < units) next = place_of(p, (int)((uint32_t)(unit + gridDim.x) / per_seq));
+    const int64_t first = at.first, n_all = (int64_t)at.end - first, n = p.n_use ? at.use : n_all, in = at.in;
+    int64_t out = at.out;
+    const bool bad = first < 0 || n_all < 0 || first + n_all > p.d.total_q || n_all > p.d.max_q || n < 0 || n > n_all || in < -1 ||
+                     in >= p.d.n_states;
+    if ((bad || out >= p.d.n_states) && in_seq == 0 && lane == 0 && p.status) atomicOr(p.status, kStatusBadIndex);
+    if (out >= p.d.n_states) out = -1;
+    if (bad || ((n == 0 || !p.o) && (out < 0 || (n == 0 && out == in)))) continue;
+    const int64_t rows = ((int64_t)h * kD + half * kRows) * kD, state = (int64_t)p.d.heads * kD * kD;
+    const int kh = h / (p.d.heads / p.d.key_heads);
+    for (int64_t t0 = 0; t0 == 0 || t0 < n; t0 += K, ++it) {
+      Stage<T>* st = take();
+      if (!st) return;
+      const uint32_t full = tc::smem_u32(&sh.full[it % kStages]);
+      const int nt = n - t0 < K ? (int)(n - t0) : K;
+      const bool load = t0 == 0 && in >= 0;
+      if (lane == 0) {
+        st->tok = first + t0, st->from = out >= 0 ? out * state + rows : -1;
+        st->nt = nt, st->head = h, st->row = half * kRows;
+        st->first = t0 == 0 ? (in >= 0 ? 1 : 2) : 0, st->last = t0 + K >= n;
+        tc::mbar_expect_tx(full, (load ? kRows * kD * 4 : 0) + nt * (2 * kD + kRows) * (int)sizeof(T));
+        if (load) tc::bulk_load(tc::smem_u32(st->s), p.states + in * state + rows, kRows * kD * 4, full);
+      }
+      __syncwarp();
+      if (lane < nt) {
+        const int64_t tok = first + t0 + lane;
+        tc::bulk_load(tc::smem_u32(st->k[lane]), static_cast<const T*>(p.k) + tok * p.d.k_stride + kh * kD, kD * sizeof(T), full);
+        tc::bulk_load(tc::smem_u32(st->q[lane]), static_cast<const T*>(p.q) + tok * p.d.q_stride + kh * kD, kD * sizeof(T), full);
+        tc::bulk_load(tc::smem_u32(st->v[lane]), static_cast<const T*>(p.v) + tok * p.d.v_stride + h * kD + half * kRows,
+                      kRows * sizeof(T), full);
+        fetch4(&st->g[lane], p.g + tok * p.d.heads + h);
+        fetch4(&st->b[lane], p.beta + tok * p.d.heads + h);
+      }
+      arrive_fetched(full);
+    }
+  }
+  Stage<T>* st = take();
+  if (!st) return;
+  if (lane == 0) {
+    st->nt = -1;
+    tc::mbar_arrive(tc::smem_u32(&sh.full[it % kStages]));
+  }
+  tc::mbar_arrive(tc::smem_u32(&sh.full[it % kStages]));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) gdn_decode_kernel(const GdnDecodeParams p) {
+  extern __shared__ __align__(16) char raw[];
+  Shared<T>& sh = *reinterpret_cast<Shared<T>*>(raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(tc::smem_u32(&sh.full[s]), 33);  // each lane, and the first's word of what it asked for
+      tc::mbar_init(tc::smem_u32(&sh.empty[s]), kWarps);
+    }
+    sh.abort = 0;
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
+  if (warp == kWarps) {
+    produce<T>(p, sh);
+    if (*(volatile uint32_t*)&sh.abort) {  // a wait gave up: what is on its way lands before the block ends
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (lane < kStages) {
+        const uint32_t bar = tc::smem_u32(&sh.full[lane]);
+        tc::mbar_wait_short(bar, 0), tc::mbar_wait_short(bar, 1);
+      }
+      if (lane == 0 && p.status) {
+        if (!(atomicOr(p.status, kStatusTimeout) & kStatusTimeout)) p.status[1] = (uint32_t)kKGdnDecode << 16 | __LINE__;
+      }
+    }
     return;
   }
-  if (out >= p.d.n_states) {
-    if (tid == 0 && p.status) atomicOr(p.status, kStatusBadIndex);
-    out = -1;
-  }
-  if ((n == 0 || !p.o) && (out < 0 || (n == 0 && out == in))) return;
-  const int64_t at = ((int64_t)h * kD + row) * (kD / 4) + lane;  // of a state's float4s
-  const int64_t state = (int64_t)p.d.heads * kD * (kD / 4);
-  float4 s[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    s[j] = in < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : reinterpret_cast<const float4*>(p.states)[in * state + at + j * kLanes];
-  const int kh = h / (p.d.heads / p.d.key_heads);
-  for (int64_t t0 = 0; t0 < n; t0 += kTokens) {
-    const int nt = n - t0 < kTokens ? (int)(n - t0) : kTokens;
-    if (t0) __syncthreads();
-    {  // a warp a token: sixteen lanes k, sixteen q
-      const int t = tid >> 5, part = (tid & 15) * 8;
-      if (t < nt) {
-        const int64_t tok = first + t0 + t;
-        if (tid & 16)
-          stage8(static_cast<const T*>(p.q) + tok * p.d.q_stride + kh * kD + part, &qs[t][part]);
-        else
-          stage8(static_cast<const T*>(p.k) + tok * p.d.k_stride + kh * kD + part, &ks[t][part]);
-        vs[t][tid & 31] = value(static_cast<const T*>(p.v)[tok * p.d.v_stride + h * kD + blockIdx.x * kRows + (tid & 31)]);
-        if ((tid & 31) == 0) as[t] = expf(p.g[tok * p.d.heads + h]), bs[t] = p.beta[tok * p.d.heads + h];
-      }
+  const int group = tid / 8, l = tid % 8;  // rows `group` and `group` + 32 of the unit, columns 4 (l + 8 j) + 0..3
+  const bool upper = l & 4;
+  uint64_t s[2][8];
+  for (int it = 0;; ++it) {
+    const int at = it % kStages;
+    if (!tc::mbar_wait(tc::smem_u32(&sh.full[at]), it / kStages & 1, &sh.abort)) {
+      sh.abort = 1;
+      return;
     }
-    __syncthreads();
+    const Stage<T>& st = sh.stage[at];
+    const int nt = st.nt;
+    if (nt < 0) return;
+    if (st.first) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint64_t x[2] = {0, 0};
+          if (st.first == 1) pairs4(&st.s[group + 32 * r][4 * (l + 8 * j)], x);
+          s[r][2 * j] = x[0], s[r][2 * j + 1] = x[1];
+        }
+    }
     for (int t = 0; t < nt; ++t) {
-      const float a = as[t];
-      float4 k[4];
-      float u = 0.f;
+      uint64_t k[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        k[j] = *reinterpret_cast<const float4*>(&ks[t][(j * kLanes + lane) * 4]);
-        u = dot4(s[j], k[j], u);
+        uint64_t x[2];
+        pairs4(&st.k[t][4 * (l + 8 * j)], x);
+        k[2 * j] = x[0], k[2 * j + 1] = x[1];
       }
-      u = row_sum(u);
-      const float bw = bs[t] * (vs[t][tid / kLanes] - a * u);
-      float acc = 0.f;
+      uint64_t u0 = 0, u1 = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[j].x = fmaf(a, s[j].x, bw * k[j].x), s[j].y = fmaf(a, s[j].y, bw * k[j].y);
-        s[j].z = fmaf(a, s[j].z, bw * k[j].z), s[j].w = fmaf(a, s[j].w, bw * k[j].w);
-        if (p.o) acc = dot4(s[j], *reinterpret_cast<const float4*>(&qs[t][(j * kLanes + lane) * 4]), acc);
+      for (int j = 0; j < 8; ++j) u0 = tc::f2_fma(s[0][j], k[j], u0), u1 = tc::f2_fma(s[1][j], k[j], u1);
+      const float mine = sum_two(both(u0), both(u1), upper), other = __shfl_xor_sync(0xffffffffu, mine, 4);
+      const float a = expf(st.g[t]), b = st.b[t];
+      const float w0 = b * (value(st.v[t][group]) - a * (upper ? other : mine));
+      const float w1 = b * (value(st.v[t][group + 32]) - a * (upper ? mine : other));
+      const uint64_t a2 = tc::f2(a, a), w02 = tc::f2(w0, w0), w12 = tc::f2(w1, w1);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[0][j] = tc::f2_fma(w02, k[j], tc::f2_mul(a2, s[0][j]));
+        s[1][j] = tc::f2_fma(w12, k[j], tc::f2_mul(a2, s[1][j]));
       }
       if (p.o) {
-        acc = row_sum(acc);
-        if (lane == 0) put(static_cast<T*>(p.o) + ((first + t0 + t) * p.d.heads + h) * kD + row, acc);
+        uint64_t o0 = 0, o1 = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint64_t x[2];
+          pairs4(&st.q[t][4 * (l + 8 * j)], x);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) o0 = tc::f2_fma(s[0][2 * j + i], x[i], o0), o1 = tc::f2_fma(s[1][2 * j + i], x[i], o1);
+        }
+        const float o = sum_two(both(o0), both(o1), upper);
+        if ((l & 3) == 0)
+          put(static_cast<T*>(p.o) + ((st.tok + t) * p.d.heads + st.head) * kD + st.row + group + (upper ? 32 : 0), o);
       }
     }
-  }
-  if (out >= 0) {
+    const int64_t to = st.last ? st.from : -1;
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.empty[at]));
+    if (to >= 0) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) reinterpret_cast<float4*>(p.states)[out * state + at + j * kLanes] = s[j];
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<ulonglong2*>(p.states + to + (group + 32 * r) * kD + 4 * (l + 8 * j)) =
+              make_ulonglong2(s[r][2 * j], s[r][2 * j + 1]);
+    }
   }
+}
+
+template <typename T>
+cudaError_t launch(const GdnDecodeParams& p, cudaStream_t s) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(gdn_decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared<T>));
+  if (e != cudaSuccess) return e;
+  const int64_t units = (int64_t)p.d.batch * p.d.heads * 2, most = 2 * device_sms();
+  if (units > INT32_MAX) return cudaErrorInvalidConfiguration;
+  gdn_decode_kernel<T><<<(unsigned)(units < most ? units : most), kThreads, sizeof(Shared<T>), s>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_gdn_decode(const GdnDecodeParams& p, cudaStream_t s) {
   LaunchScope ls(kKGdnDecode, s);
-  const dim3 grid(kD / kRows, p.d.heads, p.d.batch);
-  if (p.d.dtype == LS_DTYPE_F32)
-    gdn_decode_kernel<float><<<grid, kThreads, 0, s>>>(p);
-  else
-    gdn_decode_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return p.d.dtype == LS_DTYPE_F32 ? launch<float>(p, s) : launch<__nv_bfloat16>(p, s);
 }
 
 }  // namespace ls
