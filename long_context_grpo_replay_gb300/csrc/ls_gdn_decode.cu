@@ -207,6 +207,8 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_decode_kernel(const GdnDecode
           s[r][2 * j] = x[0], s[r][2 * j + 1] = x[1];
         }
     }
+    const float decay = lane < nt ? expf(st.g[lane]) : 0.f;  // a lane a token
+    T* o = p.o ? static_cast<T*>(p.o) + (st.tok * p.d.heads + st.head) * kD + st.row + group + (upper ? 32 : 0) : nullptr;
     for (int t = 0; t < nt; ++t) {
       uint64_t k[8];
 #pragma unroll
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_decode_kernel(const GdnDecode
 #pragma unroll
       for (int j = 0; j < 8; ++j) u0 = tc::f2_fma(s[0][j], k[j], u0), u1 = tc::f2_fma(s[1][j], k[j], u1);
       const float mine = sum_two(both(u0), both(u1), upper), other = __shfl_xor_sync(0xffffffffu, mine, 4);
-      const float a = expf(st.g[t]), b = st.b[t];
+      const float a = __shfl_sync(0xffffffffu, decay, t), b = st.b[t];
       const float w0 = b * (value(st.v[t][group]) - a * (upper ? other : mine));
       const float w1 = b * (value(st.v[t][group + 32]) - a * (upper ? mine : other));
       const uint64_t a2 = tc::f2(a, a), w02 = tc::f2(w0, w0), w12 = tc::f2(w1, w1);
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_decode_kernel(const GdnDecode
         s[0][j] = tc::f2_fma(w02, k[j], tc::f2_mul(a2, s[0][j]));
         s[1][j] = tc::f2_fma(w12, k[j], tc::f2_mul(a2, s[1][j]));
       }
-      if (p.o) {
+      if (o) {
         uint64_t o0 = 0, o1 = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -237,9 +239,9 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_decode_kernel(const GdnDecode
 #pragma unroll
           for (int i = 0; i < 2; ++i) o0 = tc::f2_fma(s[0][2 * j + i], x[i], o0), o1 = tc::f2_fma(s[1][2 * j + i], x[i], o1);
         }
-        const float o = sum_two(both(o0), both(o1), upper);
-        if ((l & 3) == 0)
-          put(static_cast<T*>(p.o) + ((st.tok + t) * p.d.heads + st.head) * kD + st.row + group + (upper ? 32 : 0), o);
+        const float x = sum_two(both(o0), both(o1), upper);
+        if ((l & 3) == 0) put(o, x);
+        o += (int64_t)p.d.heads * kD;
       }
     }
     const int64_t to = st.last ? st.from : -1;
