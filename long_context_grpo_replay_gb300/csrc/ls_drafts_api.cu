@@ -73,8 +73,8 @@ ls_status check_book(const ls_page_book* b) {
     return fail(LS_ERR_INVALID_ARGUMENT, "page_size, n_seqs, pages_per_seq and pool_pages must be >= 1");
   if ((int64_t)b->pages_per_seq * b->page_size > INT32_MAX - 65536)
     return fail(LS_ERR_UNSUPPORTED, "pages_per_seq * page_size too large");
-  if (b->pool_pages > (1 << 29) || b->n_seqs > (1 << 29))
-    return fail(LS_ERR_UNSUPPORTED, "pool_pages and n_seqs must be at most 2^29");
+  if (b->pool_pages > (1 << 29) || b->n_seqs > (1 << 26))
+    return fail(LS_ERR_UNSUPPORTED, "pool_pages must be at most 2^29, n_seqs 2^26");
   if (!b->refs || !b->page_table || !b->kv_len)
     return fail(LS_ERR_INVALID_ARGUMENT, "refs, page_table and kv_len must be non-NULL");
   if (!aligned(b->refs, 4) || !aligned(b->page_table, 4) || !aligned(b->kv_len, 8))
@@ -93,10 +93,8 @@ ls_status pages_params(const ls_page_book* b, int64_t n, void* ws, size_t ws_byt
   p->list = w, w += b->pool_pages;
   p->high = w, w += b->pool_pages;
   p->rank = w, w += b->pool_pages;
-  p->owner = w, w += b->n_seqs;
-  p->begin = w, w += b->n_seqs;
-  p->need = w, w += b->n_seqs;
-  p->kept = w;
+  p->owner = w, w += 8 * (int64_t)b->n_seqs;
+  p->lists = w;
   return LS_OK;
 }
 

@@ -336,10 +336,8 @@ struct PagesParams {
   int32_t* list;         // [pool_pages] free pages in order
   int32_t* high;         // [pool_pages] compact: pages that move, in order
   int32_t* rank;         // [pool_pages] compact: their places in `high`
-  int32_t* owner;        // [n_seqs]
-  int32_t* begin;        // [n_seqs] advance: first of its pages in `list`
-  int32_t* need;         // [n_seqs] advance: pages it takes, and two flags
-  int32_t* kept;         // [n_seqs] advance: tokens it keeps
+  int32_t* owner;        // [8][n_seqs] a block's: who names the sequence
+  int32_t* lists;        // [8][5][n_seqs] a block's, where shared memory does not hold them
   uint32_t* status;
 };
 size_t pages_scratch(const ls_page_book& b);
