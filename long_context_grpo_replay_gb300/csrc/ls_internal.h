@@ -337,7 +337,7 @@ struct PagesParams {
   int32_t* high;         // [pool_pages] compact: pages that move, in order
   int32_t* rank;         // [pool_pages] compact: their places in `high`
   int32_t* owner;        // [8][n_seqs] a block's: who names the sequence
-  int32_t* lists;        // [8][5][n_seqs] a block's, where shared memory does not hold them
+  int32_t* lists;        // [8][6][n_seqs] a block's, where shared memory does not hold them
   uint32_t* status;
 };
 size_t pages_scratch(const ls_page_book& b);

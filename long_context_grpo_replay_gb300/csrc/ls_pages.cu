@@ -23,7 +23,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int32_t kShared = 1 << 30;   // need[]: its last page is others' too
 constexpr int32_t kNoRoom = INT32_MIN; // need[]: the table's row ends, or its last page is no page
 
-constexpr int kListed = 2048;  // sequences of a call that are kept in shared memory
+constexpr int kListed = 1920;  // sequences of a call that are kept in shared memory
+constexpr int kListArrays = 6;
 
 __device__ __forceinline__ int32_t per(int32_t n, int32_t page) { return n > 0 ? (n - 1) / page + 1 : 0; }
 __device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
@@ -45,6 +46,12 @@ struct Team {
     gw = (int)rank * kWarps + (int)warp;
   }
   __device__ void sync() const { Cluster<C>::sync(); }
+  // Threads that share one of n sequences: a power of two, eight or more.
+  __device__ int shares(int n) const {
+    int w = 8;
+    while (w < threads && 2 * w * (int64_t)n <= threads) w *= 2;
+    return w;
+  }
   // Of each warp's count (count[kWarps] in each block): the sum before this warp, and of all.
   __device__ int2 prefix(const int* count) const {
     int before = 0, all = 0;
@@ -87,20 +94,20 @@ struct Stretch {
 
 // What a call says of its sequences, and what is worked out of it.
 struct Lists {
-  int32_t *seq, *keep, *old, *need, *begin;
+  int32_t *seq, *keep, *old, *need, *begin, *last;
 };
 // In shared memory where they fit, else each block in its own part of the workspace.
 __device__ __forceinline__ Lists lists(const PagesParams& p, int32_t* shared, uint32_t rank) {
-  int32_t* w = p.n <= kListed ? shared : p.lists + (int64_t)rank * 5 * p.b.n_seqs;
+  int32_t* w = p.n <= kListed ? shared : p.lists + (int64_t)rank * kListArrays * p.b.n_seqs;
   const int64_t n = p.n <= kListed ? kListed : p.b.n_seqs;
-  return Lists{w, w + n, w + 2 * n, w + 3 * n, w + 4 * n};
+  return Lists{w, w + n, w + 2 * n, w + 3 * n, w + 4 * n, w + 5 * n};
 }
 
 // ---------------------------------------------------------------- advance
 template <int C>
 __global__ void __launch_bounds__(kThreads, 1) pages_advance_kernel(const PagesParams p) {
   __shared__ int count[kWarps], scan[kWarps];
-  __shared__ int32_t listed[5 * kListed];
+  __shared__ int32_t listed[kListArrays * kListed];
   start();
   const Team<C> t;
   const Lists l = lists(p, listed, t.rank);
@@ -139,11 +146,20 @@ __global__ void __launch_bounds__(kThreads, 1) pages_advance_kernel(const PagesP
     if (t.tid == 0) atomicOr(p.status, kStatusBadIndex);
     return;
   }
-  const int ways = t.warps > p.n ? t.warps / p.n : 1, sub = t.gw % ways;
+  // The page that a sequence goes on in, for the first of this thread's sequences: nothing
+  // waits for it before the pages that are dropped are done with.
+  auto last_of = [&](int i) {
+    const int32_t keep = l.keep[i];
+    return keep % S != 0 && grows(i) > 0 && (int64_t)keep + grows(i) <= cap
+               ? p.b.page_table[(int64_t)l.seq[i] * p.b.pages_per_seq + keep / S]
+               : -1;
+  };
+  int32_t last = (int)threadIdx.x < p.n ? last_of(threadIdx.x) : -1;
+  const int width = t.shares(p.n), sub = t.tid % width, groups = t.threads / width;
   // pages that are dropped
-  for (int i = t.gw / ways; i < p.n; i += t.warps / ways) {
+  for (int i = t.tid / width; i < p.n; i += groups) {
     const int32_t* row = p.b.page_table + (int64_t)l.seq[i] * p.b.pages_per_seq;
-    for (int32_t j = per(l.keep[i], S) + sub * 32 + t.lane; j < per(l.old[i], S); j += ways * 32) {
+    for (int32_t j = per(l.keep[i], S) + sub; j < per(l.old[i], S); j += width) {
       const int32_t page = row[j];
       bool ok = page >= 0 && page < p.b.pool_pages;
       if (ok && atomicSub(p.b.refs + page, 1) <= 0) atomicAdd(p.b.refs + page, 1), ok = false;
@@ -151,7 +167,9 @@ __global__ void __launch_bounds__(kThreads, 1) pages_advance_kernel(const PagesP
     }
   }
   t.sync();
-  // free pages, and what each sequence takes: the pages' loads are under way during the sequences'
+  // free pages, and what each sequence takes
+  auto others = [&](int32_t page) { return page >= 0 && page < p.b.pool_pages ? __ldcg(p.b.refs + page) : 0; };
+  int32_t names = others(last);
   const Stretch<C> stretch(t, p.b.refs, p.b.pool_pages);
   int carry = 0;
   for (int i0 = 0; i0 < p.n; i0 += kThreads) {
@@ -159,17 +177,17 @@ __global__ void __launch_bounds__(kThreads, 1) pages_advance_kernel(const PagesP
     int need = 0;
     bool shared = false, full = false;
     if (i < p.n) {
+      if (i0) last = last_of(i), names = others(last);
       const int32_t keep = l.keep[i];
       const int64_t want = (int64_t)keep + grows(i);
       full = want > cap;
       if (!full && want > keep) {
         need = per((int32_t)want, S) - per(keep, S);
         if (keep % S != 0) {
-          const int32_t page = p.b.page_table[(int64_t)l.seq[i] * p.b.pages_per_seq + keep / S];
-          if (page < 0 || page >= p.b.pool_pages)
+          if (last < 0 || last >= p.b.pool_pages)
             full = true, need = 0, atomicOr(p.status, kStatusBadPage);
           else
-            shared = __ldcg(p.b.refs + page) > 1, need += shared;
+            shared = names > 1, need += shared;
         }
       }
     }
@@ -187,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_advance_kernel(const PagesP
     if (i < p.n) {
       l.begin[i] = upto - need;
       l.need[i] = full ? kNoRoom : need | (shared ? kShared : 0);
+      l.last[i] = last;
     }
     __syncthreads();
   }
@@ -209,38 +228,36 @@ __global__ void __launch_bounds__(kThreads, 1) pages_advance_kernel(const PagesP
   }
   t.sync();  // the list is there, and no block reads another's counts any more
   // the new lengths, entries and slots
-  for (int i = t.gw / ways; i < p.n; i += t.warps / ways) {
+  for (int i = t.tid / width; i < p.n; i += groups) {
     const int s = l.seq[i];
-    const int32_t word = l.need[i], begin = l.begin[i], keep = l.keep[i];
+    const int32_t word = l.need[i], begin = l.begin[i], keep = l.keep[i], page0 = l.last[i];
     const bool shared = word != kNoRoom && (word & kShared);
     const int32_t need = word == kNoRoom ? 0 : word & ~kShared;
     const bool served = word != kNoRoom && (need == 0 || (int64_t)begin + need <= rank.y);
-    const int32_t grow = grows(i), have = per(keep, S), first = have - (shared ? 1 : 0);
+    const int32_t grow = grows(i), first = per(keep, S) - (shared ? 1 : 0);
     int32_t* row = p.b.page_table + (int64_t)s * p.b.pages_per_seq;
-    const int32_t last = keep % S != 0 ? row[have - 1] : -1;
-    __syncwarp();  // `last` is read before this warp writes the entry
-    if (sub == 0 && t.lane == 0) {
+    if (sub == 0) {
       p.b.kv_len[s] = served ? keep + grow : keep;
       const bool copy = served && shared;
-      if (copy) atomicSub(p.b.refs + last, 1);
+      if (copy) atomicSub(p.b.refs + page0, 1);
       if (p.copies) {
-        p.copies[3 * (int64_t)i] = copy ? last : -1;
+        p.copies[3 * (int64_t)i] = copy ? page0 : -1;
         p.copies[3 * (int64_t)i + 1] = copy ? __ldcg(p.list + begin) : -1;
         p.copies[3 * (int64_t)i + 2] = copy ? keep % S : -1;
       }
       if (!served) atomicOr(p.status, kStatusNoPages);
     }
     if (served)
-      for (int32_t j = sub * 32 + t.lane; j < need; j += ways * 32) {
+      for (int32_t j = sub; j < need; j += width) {
         const int32_t page = __ldcg(p.list + begin + j);
         row[first + j] = page;
         p.b.refs[page] = 1;
       }
     if (p.q_start) {
       const int32_t t0 = p.q_start[i];
-      for (int32_t x = sub * 32 + t.lane; x < grow; x += ways * 32) {
+      for (int32_t x = sub; x < grow; x += width) {
         const int32_t pos = keep + x, j = pos / S;
-        const int32_t page = !served ? 0 : j >= first && j - first < need ? __ldcg(p.list + begin + j - first) : last;
+        const int32_t page = !served ? 0 : j >= first ? __ldcg(p.list + begin + j - first) : page0;
         p.slots[t0 + x] = served ? (int64_t)page * S + pos % S : -1;
       }
     }
@@ -250,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_advance_kernel(const PagesP
 // ---------------------------------------------------------------- fork
 template <int C>
 __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const PagesParams p) {
-  __shared__ int32_t listed[5 * kListed];
+  __shared__ int32_t listed[kListArrays * kListed];
   start();
   const Team<C> t;
   const Lists l = lists(p, listed, t.rank);  // seq: destinations, begin: sources, keep: new lengths
@@ -280,13 +297,13 @@ __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const PagesPara
     if (t.tid == 0) atomicOr(p.status, kStatusBadIndex);
     return;
   }
-  const int ways = t.warps > p.n ? t.warps / p.n : 1, sub = t.gw % ways;
-  for (int i = t.gw / ways; i < p.n; i += t.warps / ways) {
+  const int width = t.shares(p.n), sub = t.tid % width;
+  for (int i = t.tid / width; i < p.n; i += t.threads / width) {
     const int32_t had = per(l.old[i], S), want = per(l.keep[i], S);
     const int32_t* from = p.b.page_table + (int64_t)l.begin[i] * p.b.pages_per_seq;
     int32_t* to = p.b.page_table + (int64_t)l.seq[i] * p.b.pages_per_seq;
 #pragma unroll 4
-    for (int32_t j = sub * 32 + t.lane; j < max(had, want); j += ways * 32) {
+    for (int32_t j = sub; j < max(had, want); j += width) {
       bool ok = true;
       if (j < want) {
         const int32_t page = from[j], mine = j < had ? to[j] : -1;
@@ -452,7 +469,7 @@ cudaError_t launch_team(void (*one)(PagesParams), void (*eight)(PagesParams), bo
 }  // namespace
 
 size_t pages_scratch(const ls_page_book& b) {
-  return 4 * (3 * (size_t)b.pool_pages + 8 * (size_t)b.n_seqs * (b.n_seqs > kListed ? 6 : 1));
+  return 4 * (3 * (size_t)b.pool_pages + 8 * (size_t)b.n_seqs * (b.n_seqs > kListed ? 1 + kListArrays : 1));
 }
 
 cudaError_t launch_pages_advance(const PagesParams& p, cudaStream_t s) {
