@@ -27,6 +27,13 @@ struct Cluster {
     else
       asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
+  // The same in two halves: arrive, and wait for all the others' arrival.
+  static __device__ __forceinline__ void arrive() {
+    if constexpr (C != 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
+  static __device__ __forceinline__ void wait() {
+    if constexpr (C != 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
   // The word that block `r` holds in the place of `p` in this block's shared memory.
   template <typename T>
   static __device__ __forceinline__ T at(const T* p, uint32_t r) {

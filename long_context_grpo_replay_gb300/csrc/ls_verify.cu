@@ -5,7 +5,7 @@
 //   next token: least v with sum_{j<=v} w_j > u sum_j w_j,  w = max(p - q, 0) or p.
 //
 // Two kernels.  verify_rows_kernel reads every logit once: a (maximum, sum) pair
-// for each row and 16 KB of it, in base 2.  verify_draw_kernel, a cluster of up to eight
+// for each row and 2 KB of it, in base 2.  verify_draw_kernel, a cluster of up to eight
 // blocks for each sequence, joins them, tests the drafts and draws from the one
 // row where they end.
 //
@@ -31,12 +31,13 @@
 
 #include "ls_cluster.cuh"
 #include "ls_internal.h"
+#include "ls_tc.cuh"
 
 namespace ls {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kChunkBytes = 16384, kVectors = kChunkBytes / 16, kEach = kVectors / kThreads;
+constexpr int kEach = 4, kVectors = 32 * kEach, kChunkBytes = 16 * kVectors;  // a warp's in the pass over the rows
 constexpr int kMaxCluster = 8;
 constexpr int kTile = 256;  // elements a warp takes at a time in the draw, eight a lane
 
@@ -90,24 +91,50 @@ __device__ __forceinline__ float2 join_warp(float2 a, float c) {
   return a;
 }
 
-__device__ __forceinline__ void unpack(const uint4& w, float (&x)[4]) {
-  x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
 }
-__device__ __forceinline__ void unpack(const uint4& w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(u[i] << 16), x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-}
+// The elements of a 16-byte piece in pairs of floats, and their largest (a NaN aside).
+template <typename T>
+struct Piece;
+template <>
+struct Piece<float> {
+  static constexpr int E = 4;
+  static __device__ __forceinline__ float largest(const uint4& w) {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  }
+  static __device__ __forceinline__ uint64_t pair(const uint4& w, int i) {
+    return i ? tc::f2(__uint_as_float(w.z), __uint_as_float(w.w)) : tc::f2(__uint_as_float(w.x), __uint_as_float(w.y));
+  }
+};
+template <>
+struct Piece<__nv_bfloat16> {
+  static constexpr int E = 8;
+  static __device__ __forceinline__ __nv_bfloat162 two(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+  static __device__ __forceinline__ float largest(const uint4& w) {
+    const __nv_bfloat162 m = __hmax2(__hmax2(two(w.x), two(w.y)), __hmax2(two(w.z), two(w.w)));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+  static __device__ __forceinline__ uint64_t pair(const uint4& w, int i) {
+    const uint32_t u = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+    return tc::f2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+};
 
-// Block (row, chunk).  A row starts anywhere: its 16-byte pieces are dealt out to
-// the chunks, the elements before the first and after the last go to chunk 0.
+// A warp takes 2 KB of a row by itself: all of it loaded at once, the maximum of the
+// lanes first, the exponentials relative to it, on packed pairs.  A row starts
+// anywhere: its 16-byte pieces are dealt out, the elements before the first and after
+// the last go to its first warp.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) verify_rows_kernel(const VerifyParams p) {
-  constexpr int E = 16 / sizeof(T);
-  __shared__ float2 warps[kWarps];
+  constexpr int E = Piece<T>::E;
   asm volatile("griddepcontrol.launch_dependents;");  // the draw's blocks set up while the last rows are read
-  const int chunk = blockIdx.x % p.chunks, tid = threadIdx.x;
-  const int64_t r = blockIdx.x / p.chunks;
+  const int64_t part = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (part >= p.d.total_q * p.chunks) return;
+  const int64_t r = part / p.chunks;
+  const int chunk = (int)(part - r * p.chunks), lane = threadIdx.x & 31;
   const T* row = static_cast<const T*>(p.logits) + r * p.d.logits_stride;
   const int before = (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T);
   const int head = before < p.d.vocab ? before : p.d.vocab;
@@ -116,50 +143,45 @@ __global__ void __launch_bounds__(kThreads) verify_rows_kernel(const VerifyParam
   uint4 w[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const int at = chunk * kVectors + i * kThreads + tid;
-    if (at < vectors) w[i] = __ldcs(body + at);
+    const int at = chunk * kVectors + i * 32 + lane;
+    constexpr uint32_t low = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -infinity
+    w[i] = at < vectors ? __ldcs(body + at) : make_uint4(low, low, low, low);
   }
-  float2 a = make_float2(-INFINITY, 0.f);
+  float z = -INFINITY;
   if (chunk == 0) {
-    float z = -INFINITY;
-    if (tid < head) z = value(row[tid]);
-    if (tid >= 32 && tid < 32 + tail) z = value(row[head + vectors * E + tid - 32]);
-    a = make_float2(z, z == -INFINITY ? 0.f : z - z + 1.f);  // NaN for NaN and +infinity
+    if (lane < head) z = value(row[lane]);
+    if (lane >= 16 && lane < 16 + tail) z = value(row[head + vectors * E + lane - 16]);
   }
-  float m = a.x;
+  float m = z;
 #pragma unroll
-  for (int i = 0; i < kEach; ++i)
-    if (chunk * kVectors + i * kThreads + tid < vectors) {
-      float x[E];
-      unpack(w[i], x);
-#pragma unroll
-      for (int e = 0; e < E; ++e) m = fmaxf(m, x[e]);
-    }
+  for (int i = 0; i < kEach; ++i) m = fmaxf(m, Piece<T>::largest(w[i]));
+  m = warp_max(m);
   const float base = m == -INFINITY ? 0.f : m;
-  float sum = a.y * ex2((a.x - base) * p.c);
+  const uint64_t base2 = tc::f2(-base, -base), c2 = tc::f2(p.c, p.c);
+  float sum = ex2((z - base) * p.c);
+  uint64_t more = 0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i)
-    if (chunk * kVectors + i * kThreads + tid < vectors) {
-      float x[E];
-      unpack(w[i], x);
 #pragma unroll
-      for (int e = 0; e < E; ++e) sum += ex2((x[e] - base) * p.c);
+    for (int j = 0; j < E / 2; ++j) {
+      float lo, hi;
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(tc::f2_mul(tc::f2_add(Piece<T>::pair(w[i], j), base2), c2)));
+      more = tc::f2_add(more, tc::f2(ex2(lo), ex2(hi)));
     }
-  a = join_warp(make_float2(m, sum), p.c);
-  if ((tid & 31) == 0) warps[tid >> 5] = a;
-  __syncthreads();
-  if (tid < 32) {
-    a = join_warp(tid < kWarps ? warps[tid] : make_float2(-INFINITY, 0.f), p.c);
-    if (tid == 0) p.parts[blockIdx.x] = a;
-  }
+  float lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(more));
+  sum += lo + hi;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) p.parts[part] = make_float2(m, sum);
 }
 
 // ---------------------------------------------------------------- the draw
 struct Row {
-  float base;      // taken off every logit first: 0, or the maximum where the products would leave the grid
+  float base;      // taken off every logit first where it is not 0: the maximum, where the products would leave the grid
   float bias;      // 1.5 * 2^15 less the maximum's product on the grid of 2^-8
   float rest;      // the rest of that product
-  float least;     // below it a weight is 0 (2^-62 of the largest)
+  float least;     // logits below it count as it: 2^-90 of the largest weight, nothing in units of 2^-61
   float c, c_low;
   uint32_t scale;  // exponent bits of 2^-k, with 2^-k Z in [0.5, 1)
   float z0;        // 2^-k Z0
@@ -174,7 +196,7 @@ __device__ __forceinline__ Row make_row(float top, float sum, float c, float c_l
   const float grid = rintf(hi * 256.f) * 0x1p-8f;
   r.rest = (hi - grid) + fmaf(m, c_low, fmaf(m, c, -hi));
   r.bias = __uint_as_float(kGrid) - grid;
-  r.least = fmaxf(m - 62.f / c, -3.402823466e38f);
+  r.least = fmaxf(m - 90.f / c, -3.402823466e38f);
   const uint32_t bits = __float_as_uint(sum);
   r.scale = (253u - (bits >> 23)) << 23;                         // 127 - (exponent + 1)
   r.z0 = __uint_as_float((bits & 0x7fffffu) | 0x3f000000u);
@@ -184,13 +206,14 @@ __device__ __forceinline__ Row make_row(float top, float sum, float c, float c_l
 // e = 2^(c (z - top)) in the row's units, as a sum of two floats: the lower one is
 // up to 2^-8.5 of the upper.
 __device__ __forceinline__ void weight(float z, const Row& r, const float2* table, float& upper, float& lower) {
-  const float v = z - r.base, s = fmaxf(v, r.least);
+  if (r.base != 0.f) z -= r.base;
+  const float s = fmaxf(z, r.least);
   const float t = fmaf(s, r.c, r.bias);
   const float f = fmaf(s, r.c, r.bias - t) + fmaf(s, r.c_low, -r.rest);
   const uint32_t k = __float_as_uint(t);
   const float2 w = table[k & 255u];
   const float d = f * fmaf(f, fmaf(f, 0.0555041087f, 0.240226507f), 0.693147181f);  // powers of ln 2 over factorials
-  const float scale = v >= r.least ? __uint_as_float(((k & 0xffffff00u) << 15) + r.scale) : 0.f;
+  const float scale = __uint_as_float(((k & 0xffffff00u) << 15) + r.scale);
   upper = w.x * scale;
   lower = fmaf(w.x, d, w.y) * scale;
 }
@@ -358,6 +381,24 @@ __global__ void __launch_bounds__(kThreads, 4) verify_draw_kernel(const VerifyPa
   }
   const int n = (int)n64, V = p.d.vocab;
   const T* logits = static_cast<const T*>(p.logits);
+  // A warp a row: what its draft is, and what is said of it.
+  struct Draft {
+    int64_t x;
+    float z, q, u;
+  };
+  auto draft_of = [&](int i) {
+    Draft d{-1, 0.f, 1.f, 0.f};
+    if (i + 1 < n) {
+      const int64_t r = first + i;
+      d.x = p.tokens[r + 1], d.u = p.u[r];
+      if (d.x >= 0 && d.x < V) {
+        d.z = value(logits[r * p.d.logits_stride + d.x]);
+        if (p.probs) d.q = p.probs[r * p.d.draft_stride + d.x];
+      }
+    }
+    return d;
+  };
+  Draft draft0 = draft_of(warp);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' pairs are there
   // the drafts, a warp a row, up to the first that does not pass
   int stop = -1;
@@ -370,15 +411,13 @@ __global__ void __launch_bounds__(kThreads, 4) verify_draw_kernel(const VerifyPa
       for (int x = lane; x < p.chunks; x += 32) a = join(a, p.parts[r * p.chunks + x], p.c);
       a = join_warp(a, p.c);
       bool pass = false;
+      const Draft t = i0 ? draft_of(i) : draft0;
       if (i + 1 < n) {
-        const int64_t x = p.tokens[r + 1];
-        if (x >= 0 && x < V) {
-          const float d = value(logits[r * p.d.logits_stride + x]) - a.x;
-          const double e = exp2f(fmaf(d, p.c, d * p.c_low));
-          const double q = p.probs ? p.probs[r * p.d.draft_stride + x] : 1.f;
-          pass = (double)p.u[r] * q * a.y < e;
+        if (t.x >= 0 && t.x < V) {
+          const float d = t.z - a.x;
+          pass = t.u * t.q * a.y < exp2f(fmaf(d, p.c, d * p.c_low));
           if (pass && rank == 0 && lane == 0) {
-            p.emitted[r] = x;
+            p.emitted[r] = t.x;
             if (p.logp) p.logp[r] = d * p.d.logit_scale - logf(a.y);
           }
         } else if (rank == 0 && lane == 0) {
@@ -465,6 +504,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_draw_kernel(const VerifyPa
       z_all = all;
     }
   }
+  __syncwarp();
+  Team::arrive();  // this block has read the others' sums
   __syncthreads();
   // the block that holds the segment looks into it
   if (picked / kWarps == (int)rank) {
@@ -536,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_draw_kernel(const VerifyPa
       if (p.logp) p.logp[r] = (value(z[found]) - row.x) * p.d.logit_scale - logf(row.y);
     }
   }
-  Team::sync();  // the sums are read by other blocks
+  Team::wait();  // the others have read this block's
 }
 
 }  // namespace
@@ -549,7 +590,7 @@ int verify_chunks(const ls_verify_desc& d) {
 cudaError_t launch_draft_verify(const VerifyParams& p, cudaStream_t s) {
   if (p.d.total_q > 0) {
     LaunchScope ls(kKVerifyRows, s);
-    const unsigned grid = (unsigned)(p.d.total_q * p.chunks);
+    const unsigned grid = (unsigned)((p.d.total_q * p.chunks + kWarps - 1) / kWarps);
     if (p.d.dtype == LS_DTYPE_F32)
       verify_rows_kernel<float><<<grid, kThreads, 0, s>>>(p);
     else
