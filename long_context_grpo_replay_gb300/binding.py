@@ -708,6 +708,8 @@ def ls_pages_advance(book, q_start, slots, copies, ws, seqs=None, keep=None, str
     torch = _torch or _lazy_torch()
     i32 = torch.int32
     if q_start is not None:
+        if slots is None or copies is None:
+            raise ValueError("slots and copies go with q_start")
         n, total = q_start.shape[0] - 1, slots.shape[0]
         if not (q_start.dtype is i32 and copies.dtype is i32 and slots.dtype is torch.int64 and q_start.is_contiguous() and
                 slots.is_contiguous() and copies.is_contiguous() and copies.shape == (n, 3) and q_start.dim() == slots.dim() == 1):

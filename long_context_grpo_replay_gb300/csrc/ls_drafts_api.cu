@@ -106,8 +106,8 @@ ls_status check_verify(const ls_verify_desc* d) {
   if (d->vocab > (1 << 30)) return fail(LS_ERR_UNSUPPORTED, "vocab %d > 2^30", d->vocab);
   LS_CHECK(check_tokens(d->batch, d->total_q, d->max_q));
   if (d->logits_stride < d->vocab) return fail(LS_ERR_INVALID_ARGUMENT, "logits_stride must be at least vocab");
-  if (!(d->logit_scale > 0.f) || !std::isfinite(d->logit_scale))
-    return fail(LS_ERR_INVALID_ARGUMENT, "logit_scale must be finite and > 0");
+  if (!(d->logit_scale > 0.f) || !std::isfinite(d->logit_scale * 1.45f))
+    return fail(LS_ERR_INVALID_ARGUMENT, "logit_scale must be > 0 and below 2^127");
   if (d->total_q * verify_chunks(*d) > INT32_MAX) return fail(LS_ERR_UNSUPPORTED, "total_q * vocab too large");
   return LS_OK;
 }

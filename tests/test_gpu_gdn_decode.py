@@ -110,6 +110,35 @@ def test_fork_from_one_state_and_from_zeros(cuda_device):
     assert torch.equal(states[2], m["states"][8])      # no token: a copy
 
 
+def test_no_tokens_at_all(cuda_device):
+    """Sequences without a token move their states only; nothing else is read."""
+    states = torch.randn(6, 3, 128, 128, device="cuda")
+    want = states.clone()
+    e = torch.empty((0, 3, 128), device="cuda")
+    z = torch.empty((0, 3), device="cuda")
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    desc = ls.gdn_decode_desc(e, e, e, states, 3, 0)
+    ls.ls_gdn_decode(desc, states, e, e, e, z, z, ints(0, 0, 0, 0), ints(0, 1, -1), ints(4, -1, 5), e)
+    want[4], want[5] = want[0], 0
+    assert torch.equal(states, want)
+
+
+def test_states_far_into_a_pool(cuda_device):
+    """Element offsets past 2^31: slots of 64 heads, 1 M elements each."""
+    n = 2100
+    m = make([1, 2], 64, 32, torch.bfloat16, seed=12, n_states=2)
+    d = on_gpu(m)
+    states = torch.empty((n, 64, 128, 128), device="cuda")
+    states[n - 1], states[0] = d["states"][0], d["states"][1]
+    desc = ls.gdn_decode_desc(d["q"], d["k"], d["v"], states, 2, 2)
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    o = torch.empty(m["v"].shape, dtype=torch.bfloat16, device="cuda")
+    ls.ls_gdn_decode(desc, states, d["q"], d["k"], d["v"], d["g"], d["beta"], d["q_start"], ints(n - 1, 0), ints(n - 2, n - 1 - 1024), o)
+    want_o, want = run(dict(m, states=torch.cat([m["states"], torch.zeros_like(m["states"])])), [0, 1], [2, 3])
+    assert torch.equal(o.cpu(), want_o)
+    assert torch.equal(states[n - 2].cpu(), want[2]) and torch.equal(states[n - 1 - 1024].cpu(), want[3])
+
+
 def test_step_by_step_is_one_call(cuda_device):
     """Tokens one call at a time give what one call gives, bit for bit."""
     m = make([5, 5], 2, 1, torch.float32, seed=7)

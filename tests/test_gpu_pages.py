@@ -59,12 +59,15 @@ class Device:
             assert row[:len(want)] == want
 
 
-@pytest.mark.parametrize("pool,page,n_seqs,per_seq", [(40, 4, 5, 12), (5000, 16, 70, 100), (9001, 1, 33, 300), (300, 256, 3, 100)])
-def test_a_rollout_at_random(cuda_device, pool, page, n_seqs, per_seq):
+@pytest.mark.parametrize("pool,page,n_seqs,per_seq,steps", [
+    (40, 4, 5, 12, 60), (5000, 16, 70, 100, 60), (9001, 1, 33, 300, 60), (300, 256, 3, 100, 60),
+    (20011, 2, 2500, 6, 25),      # more sequences than a block keeps to itself
+    (270007, 3, 40, 5000, 25)])   # more pages than the warps keep a bit for
+def test_a_rollout_at_random(cuda_device, pool, page, n_seqs, per_seq, steps):
     """Growth, truncation, forks, release and compaction in a random order, on both sizes of the kernels."""
     rng = random.Random(pool)
     d = Device(pool, page, n_seqs, per_seq)
-    for step in range(60):
+    for step in range(steps):
         kind = rng.choice(["advance", "advance", "advance", "fork", "release", "compact"])
         seqs = rng.sample(range(n_seqs), rng.randint(1, n_seqs))
         if kind == "advance":
@@ -231,6 +234,46 @@ def test_more_entries_than_one_row_of_blocks(cuda_device):
     ls.ls_cache_copy_pages(cache, copies)
     for t in raw + exps:
         assert torch.equal(t[3], t[2]) and torch.equal(t[1], t[0])
+
+
+def test_graph_of_a_fork_with_its_copies(cuda_device):
+    """Fork, advance and copy captured together on a side stream, each starting under the one before it; replays begin
+    by taking back what the replay before gave."""
+    d = Device(60, 8, 5, 6)
+    d.advance([0], None, [21])
+    cache, raw, exps = pools(60, 2, 8, 64, torch.float8_e4m3fn)
+    src, dst, q_start = d.t([0] * 4), d.t([1, 2, 3, 4]), d.t([0, 1, 3, 4, 9])
+    slots, copies = torch.zeros(9, dtype=I64, device="cuda"), torch.zeros((4, 3), dtype=I32, device="cuda")
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=s):
+        ls.ls_pages_fork(d.book, src, dst, d.ws)
+        ls.ls_pages_advance(d.book, q_start, slots, copies, d.ws, seqs=dst)
+        ls.ls_cache_copy_pages(cache, copies, d.ws)
+    for _ in range(4):
+        graph.replay()
+        d.ref.fork([0] * 4, [1, 2, 3, 4], [21] * 4)
+        want = d.ref.advance([1, 2, 3, 4], [21] * 4, [1, 2, 1, 5])
+        torch.cuda.synchronize()
+        assert slots.tolist() == want[0] and [tuple(r) for r in copies.tolist()] == want[1]
+        d.same()
+        for a, b, n in want[1]:
+            assert all(torch.equal(t[a, :, :n], t[b, :, :n]) for t in raw + exps)
+
+
+def test_pages_far_into_a_pool(cuda_device):
+    """Byte offsets past 2^32."""
+    pages = 40000
+    shape = (pages, 2, 256, 256)                        # 5.2 GB a pool
+    k = torch.empty(shape, dtype=torch.uint8, device="cuda")
+    v = torch.empty(shape, dtype=torch.uint8, device="cuda")
+    exps = [torch.zeros(shape[:3], dtype=torch.int8, device="cuda") for _ in range(2)]
+    for i, t in enumerate((k, v)):
+        t[5] = torch.randint(0, 256, shape[1:], dtype=torch.uint8, device="cuda")
+        t[pages - 1] = 17 + i
+    cache = ls.kv_cache_from(k.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn), *exps)
+    ls.ls_cache_copy_pages(cache, torch.tensor([[5, pages - 2, 256], [pages - 1, 6, 100]], dtype=I32, device="cuda"))
+    for i, t in enumerate((k, v)):
+        assert torch.equal(t[pages - 2], t[5]) and (t[6, :, :100] == 17 + i).all() and (t[pages - 1] == 17 + i).all()
 
 
 def test_graph_of_a_step(cuda_device):

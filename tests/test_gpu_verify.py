@@ -219,6 +219,41 @@ def test_sequences_that_are_left_out(cuda_device):
     assert run(m)[0].tolist() == [0, 0]
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_far_apart_and_oddly_placed(cuda_device, dtype):
+    """Element offsets past 2^31, and a first element at every place within 16 bytes."""
+    v, stride = 3001, 1_200_000_001
+    m = make([2, 1], v, dtype, False, seed=19)
+    big = torch.empty(2 * stride + v + 16, dtype=dtype, device="cuda")
+    want = run(m)
+    check(m, want)
+    for off in range(16 // dtype.itemsize):
+        logits = big[off:].as_strided((3, v), (stride, 1))
+        logits.copy_(m["wide"])
+        desc = ls.verify_desc(logits, 2, 2)
+        ws = torch.zeros(ls.ls_draft_verify_workspace_size(desc), dtype=torch.uint8, device="cuda")
+        count, out = torch.empty(2, dtype=torch.int32, device="cuda"), torch.empty(3, dtype=torch.int64, device="cuda")
+        ls.ls_draft_verify(desc, logits, m["tokens"].cuda(), torch.tensor([0, 2, 3], dtype=torch.int32, device="cuda"), m["u"].cuda(),
+                           m["u_next"].cuda(), count, out, None, ws)
+        ls.ls_read_device_status(ws)
+        assert torch.equal(count.cpu(), want[0]) and torch.equal(out.cpu(), want[1])
+
+
+def test_scales_at_their_ends(cuda_device):
+    """A very small scale makes all tokens alike, a very large one leaves the largest; logits far from zero."""
+    m = make([1] * 6, 5003, torch.float32, False, seed=20)
+    for scale in (1e-38, 1e30):
+        got = run(dict(m, scale=scale))
+        if scale > 1:
+            assert got[1].tolist() == m["wide"].argmax(1).tolist()
+        else:
+            assert all(abs(t - float(u) * 5003) <= 1 for t, u in zip(got[1].tolist(), m["u_next"]))
+    far = dict(m, wide=(m["wide"] * 4).round() / 4 + 2.0 ** 20)   # the maximum's product leaves the grid of the draw
+    check(far, run(far))
+    near = dict(m, wide=(m["wide"] * 4).round() / 4)              # the same distribution near zero
+    assert torch.equal(run(far)[1], run(near)[1])
+
+
 def test_tokens_come_out_as_from_the_target(cuda_device):
     """The first token's distribution over 60,000 sequences: each count within 6 standard deviations."""
     n, g = 60000, torch.Generator().manual_seed(16)
