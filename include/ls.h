@@ -619,7 +619,8 @@ LS_API ls_status ls_cache_copy_pages(const ls_kv_cache* cache, const int32_t* co
  *   The weights of the draw are good to 2^-31 each and their sums exact,
  *     so that the token is the definition's also in a vocabulary of 10^5; an
  *     acceptance within about 2^-20 of its border may fall either way.
- *   dtype: of logits; draft_probs is float32.  Strides in elements, any. */
+ *   dtype: of logits; draft_probs is float32.  Strides in elements, any.
+ *   logit_scale: 2^-100 to 2^100. */
 typedef struct {
   int32_t dtype;
   int32_t vocab;

@@ -106,14 +106,17 @@ ls_status check_verify(const ls_verify_desc* d) {
   if (d->vocab > (1 << 30)) return fail(LS_ERR_UNSUPPORTED, "vocab %d > 2^30", d->vocab);
   LS_CHECK(check_tokens(d->batch, d->total_q, d->max_q));
   if (d->logits_stride < d->vocab) return fail(LS_ERR_INVALID_ARGUMENT, "logits_stride must be at least vocab");
-  if (!(d->logit_scale > 0.f) || !std::isfinite(d->logit_scale * 1.45f))
-    return fail(LS_ERR_INVALID_ARGUMENT, "logit_scale must be > 0 and below 2^127");
+  if (!(d->logit_scale > 0.f) || !std::isfinite(d->logit_scale))
+    return fail(LS_ERR_INVALID_ARGUMENT, "logit_scale must be finite and > 0");
+  // beyond these a masked token's product is not far enough below the others', or overflows
+  if (d->logit_scale < 0x1p-100f || d->logit_scale > 0x1p100f)
+    return fail(LS_ERR_UNSUPPORTED, "logit_scale %g is not within 2^-100 .. 2^100", (double)d->logit_scale);
   if (d->total_q * verify_chunks(*d) > INT32_MAX) return fail(LS_ERR_UNSUPPORTED, "total_q * vocab too large");
   return LS_OK;
 }
 
 size_t verify_need(const ls_verify_desc& d) {
-  return kWsHeader + (size_t)d.total_q * verify_chunks(d) * sizeof(float2);
+  return kWsHeader + verify_scratch(d);
 }
 
 }  // namespace

@@ -312,11 +312,12 @@ struct VerifyParams {
   int64_t* emitted;
   float* logp;
   int64_t* keep;
-  float2* parts;  // [total_q][chunks] (maximum, sum of the others' exponentials relative to it)
+  float2* parts;  // [total_q][chunks] (maximum, sum of the others' exponentials relative to it), or what replaces them
   int32_t chunks;
   uint32_t* status;
 };
 int verify_chunks(const ls_verify_desc& d);
+size_t verify_scratch(const ls_verify_desc& d);
 cudaError_t launch_draft_verify(const VerifyParams& p, cudaStream_t s);
 
 // Pages of a cache (ls_pages.cu).  The work arrays lie after the status header.

@@ -88,7 +88,7 @@ def test_pages_calls(ls):
     (dict(dtype=2), 1), (dict(vocab=0), 1), (dict(vocab=(1 << 30) + 1, logits_stride=1 << 31), 2), (dict(batch=-1), 1),
     (dict(batch=70000, max_q=1), 2), (dict(total_q=-1), 1), (dict(total_q=7), 1), (dict(max_q=6), 1), (dict(max_q=1), 1),
     (dict(logits_stride=99), 1), (dict(logit_scale=0.0), 1), (dict(logit_scale=float("nan")), 1), (dict(logit_scale=-1.0), 1),
-    (dict(logit_scale=float("inf")), 1), (dict(logit_scale=3e38), 1), (dict(total_q=1 << 30, max_q=1 << 30, vocab=1 << 20, logits_stride=1 << 20), 2)])
+    (dict(logit_scale=float("inf")), 1), (dict(logit_scale=3e38), 2), (dict(logit_scale=1e-31), 2), (dict(total_q=1 << 30, max_q=1 << 30, vocab=1 << 20, logits_stride=1 << 20), 2)])
 def test_bad_verify_descs(ls, bad, status):
     n = ctypes.c_size_t(0)
     assert ls.lib().ls_draft_verify_workspace_size(ctypes.byref(verify(ls, **bad)), ctypes.byref(n)) == status

@@ -242,12 +242,15 @@ def test_rows_far_apart_and_oddly_placed(cuda_device, dtype):
 def test_scales_at_their_ends(cuda_device):
     """A very small scale makes all tokens alike, a very large one leaves the largest; logits far from zero."""
     m = make([1] * 6, 5003, torch.float32, False, seed=20)
-    for scale in (1e-38, 1e30):
+    for scale in (2.0 ** -100, 2.0 ** 100):
         got = run(dict(m, scale=scale))
         if scale > 1:
             assert got[1].tolist() == m["wide"].argmax(1).tolist()
         else:
             assert all(abs(t - float(u) * 5003) <= 1 for t, u in zip(got[1].tolist(), m["u_next"]))
+    masked = dict(m, scale=2.0 ** -100, wide=m["wide"].clone())
+    masked["wide"][:, 10:] = -math.inf
+    assert all(abs(t - float(u) * 10) <= 1 for t, u in zip(run(masked)[1].tolist(), m["u_next"]))
     far = dict(m, wide=(m["wide"] * 4).round() / 4 + 2.0 ** 20)   # the maximum's product leaves the grid of the draw
     check(far, run(far))
     near = dict(m, wide=(m["wide"] * 4).round() / 4)              # the same distribution near zero
