@@ -12,6 +12,11 @@
 // the warps' counts gives each free page its rank, and the rank its taker, so the
 // result does not depend on which thread came first.  The kernels let the one after
 // them start early, which waits for their end before it reads anything.
+//   Measured, one call after another: a step of 8 sequences 5.4 us in a graph (6.3 as
+// calls), of 384 over 131,000 pages 13.3 us; 16 members forked from 100,003 tokens, their
+// first slots and the copies of their last page 14.5 us in a graph; 3001 pages compacted
+// in 11 us before the copies.  One block alone takes 8 us where eight take 10 for the
+// first of these, but 97 for the second.
 #include "ls_cluster.cuh"
 #include "ls_internal.h"
 
@@ -405,7 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const PagesP
 // ---------------------------------------------------------------- copies
 constexpr int kCopyThreads = 256, kPiece = 16384;  // bytes of a block
 
-// Pieces of 16 KB, dealt out in turn: piece x % pieces of side x / pieces (K's heads,
+// Bytes only: 588 MB read and written in 98 us (6.0 TB/s, 88 % of a copy's rate), 560
+// pages of 1500 entries.  Pieces of 16 KB, dealt out in turn: piece x % pieces of side x / pieces (K's heads,
 // then V's) of an entry's page.  All of a block's piece is loaded before its first
 // store, eight blocks an SM.
 __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const ls_kv_cache c, const int32_t* __restrict__ copies, int row_bytes,
