@@ -126,6 +126,12 @@ class VerifyDesc(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("vocab", ctypes.c_int32), ("batch", ctypes.c_int32),
                 ("max_q", ctypes.c_int32), ("total_q", ctypes.c_int64), ("logits_stride", ctypes.c_int64),
                 ("draft_stride", ctypes.c_int64), ("logit_scale", ctypes.c_float)]
+    layout = None  # verify_desc sets what the call's tensors have to be
+
+    def __setattr__(self, name, value):  # a field that is changed by hand: what the tensors have to be is looked up again
+        super().__setattr__(name, value)
+        if name != "layout":
+            super().__setattr__("layout", None)
 
 
 class GdnDecodeDesc(ctypes.Structure):
@@ -134,7 +140,12 @@ class GdnDecodeDesc(ctypes.Structure):
                 ("max_q", ctypes.c_int32), ("reserved", ctypes.c_int32), ("total_q", ctypes.c_int64),
                 ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
                 ("n_states", ctypes.c_int64)]
-    layout = None  # gdn_decode_desc sets q's, k's and v's shapes and strides
+    layout = None  # gdn_decode_desc sets what the call's tensors have to be
+
+    def __setattr__(self, name, value):  # a field that is changed by hand: what the tensors have to be is looked up again
+        super().__setattr__(name, value)
+        if name != "layout":
+            super().__setattr__("layout", None)
 
 
 def library_path() -> Path:
@@ -671,6 +682,11 @@ def _stream_of(stream, dev):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _done(status):
+    if status:
+        _check(status)
+
+
 def page_book(refs, page_table, kv_len, page_size) -> PageBook:
     """The book of a pool's pages: refs int32 [pool_pages], page_table int32 [n_seqs, pages_per_seq], kv_len
     int64 [n_seqs].  The book holds addresses: keep the tensors alive."""
@@ -731,7 +747,7 @@ def ls_pages_advance(book, q_start, slots, copies, ws, seqs=None, keep=None, str
             (q_start is not None and not q_start.get_device() == slots.get_device() == copies.get_device() == dev) or \
             (seqs is not None and seqs.get_device() != dev) or (keep is not None and keep.get_device() != dev):
         _on_book(book, ws, q_start, slots, copies, seqs, keep)
-    _check(lib().ls_pages_advance(book, n, None if seqs is None else seqs.data_ptr(), None if keep is None else keep.data_ptr(),
+    _done((_lib or lib()).ls_pages_advance(book, n, None if seqs is None else seqs.data_ptr(), None if keep is None else keep.data_ptr(),
                                   *at, ws.data_ptr(), _nbytes(ws), _stream_of(stream, dev)))
 
 
@@ -760,7 +776,7 @@ def ls_pages_fork(book, src, dst, ws, lens=None, stream=None):
     if dev < 0 or not dev == book.device == src.get_device() == dst.get_device() == torch._C._cuda_getDevice() or \
             (lens is not None and lens.get_device() != dev):
         _on_book(book, ws, src, dst, lens)
-    _check(lib().ls_pages_fork(book, n, src.data_ptr(), dst.data_ptr(), _ptr(lens), ws.data_ptr(), _nbytes(ws),
+    _done((_lib or lib()).ls_pages_fork(book, n, src.data_ptr(), dst.data_ptr(), _ptr(lens), ws.data_ptr(), _nbytes(ws),
                                _stream_of(stream, dev)))
 
 
@@ -785,7 +801,7 @@ def ls_cache_copy_pages(cache, copies, ws=None, stream=None):
         if not cache.on_gpu:
             _refuse_host()
         _one_gpu(copies, ws)
-    _check(lib().ls_cache_copy_pages(cache, copies.data_ptr(), copies.shape[0], _ptr(ws),
+    _done((_lib or lib()).ls_cache_copy_pages(cache, copies.data_ptr(), copies.shape[0], _ptr(ws),
                                      0 if ws is None else _nbytes(ws), _stream_of(stream, dev)))
 
 
@@ -797,8 +813,11 @@ def verify_desc(logits, batch, max_q, draft_probs=None, logit_scale=1.0) -> Veri
         if draft_probs.shape != logits.shape:
             raise ValueError("draft_probs must have the logits' shape")
         stride = _rows(draft_probs, "draft_probs")
-    return VerifyDesc(_dtype_code(logits.dtype), logits.shape[1], batch, max_q, logits.shape[0], _rows(logits, "logits"),
+    desc = VerifyDesc(_dtype_code(logits.dtype), logits.shape[1], batch, max_q, logits.shape[0], _rows(logits, "logits"),
                       stride, logit_scale)
+    desc.layout = (logits.dtype, logits.shape, logits.stride(), None if draft_probs is None else draft_probs.stride(),
+                   (logits.shape[0],), (batch + 1,), (batch,))
+    return desc
 
 
 def ls_draft_verify_workspace_size(desc) -> int:
@@ -807,12 +826,9 @@ def ls_draft_verify_workspace_size(desc) -> int:
     return out.value
 
 
-def ls_draft_verify(desc, logits, tokens, q_start, u, u_next, n_emitted, emitted, logp, ws, draft_probs=None, kv_len=None,
-                    keep=None, stream=None):
-    """Drafts against the target's logits and the token after them (see ls.h); logp and keep may be None."""
-    torch = _torch or _lazy_torch()
+def _verify_check(desc, logits, tokens, q_start, u, u_next, n_emitted, emitted, logp, draft_probs, kv_len, keep):
+    import torch
     n, b = desc.total_q, desc.batch
-    f32, i32, i64 = torch.float32, torch.int32, torch.int64
     if logits.shape != (n, desc.vocab) or _dtype_code(logits.dtype) != desc.dtype or _rows(logits, "logits") != desc.logits_stride:
         raise ValueError("logits is not the tensor of the desc")
     if draft_probs is not None:
@@ -821,30 +837,45 @@ def ls_draft_verify(desc, logits, tokens, q_start, u, u_next, n_emitted, emitted
         _want_f32(draft_probs)
     elif desc.draft_stride:
         raise ValueError("the desc has draft_probs")
-    if not ((tokens.dtype, emitted.dtype, q_start.dtype, n_emitted.dtype, u.dtype, u_next.dtype) == (i64, i64, i32, i32, f32, f32) and
-            tokens.shape == emitted.shape == u.shape == (n,) and q_start.shape == (b + 1,) and u_next.shape == n_emitted.shape == (b,) and
-            tokens.is_contiguous() and emitted.is_contiguous() and q_start.is_contiguous() and n_emitted.is_contiguous() and
-            u.is_contiguous() and u_next.is_contiguous()):
-        _want(tokens, i64, (n,), "tokens")
-        _want(q_start, i32, (b + 1,), "q_start")
-        _want(u, f32, (n,), "u")
-        _want(u_next, f32, (b,), "u_next")
-        _want(n_emitted, i32, (b,), "n_emitted")
-        _want(emitted, i64, (n,), "emitted")
+    _want(tokens, torch.int64, (n,), "tokens")
+    _want(q_start, torch.int32, (b + 1,), "q_start")
+    _want(u, torch.float32, (n,), "u")
+    _want(u_next, torch.float32, (b,), "u_next")
+    _want(n_emitted, torch.int32, (b,), "n_emitted")
+    _want(emitted, torch.int64, (n,), "emitted")
     if logp is not None:
-        _want(logp, f32, (n,), "logp")
+        _want(logp, torch.float32, (n,), "logp")
     if keep is not None:
         if kv_len is None:
             raise ValueError("keep needs kv_len")
-        _want(keep, i64, (b,), "keep")
-        _want(kv_len, i64, (b,), "kv_len")
+        _want(keep, torch.int64, (b,), "keep")
+        _want(kv_len, torch.int64, (b,), "kv_len")
+
+
+def ls_draft_verify(desc, logits, tokens, q_start, u, u_next, n_emitted, emitted, logp, ws, draft_probs=None, kv_len=None,
+                    keep=None, stream=None):
+    """Drafts against the target's logits and the token after them (see ls.h); logp and keep may be None."""
+    torch = _torch or _lazy_torch()
+    f32, i32, i64 = torch.float32, torch.int32, torch.int64
+    dt, shape, stride, q_stride, rows, starts, each = desc.layout or _NO_LAYOUT[:7]
+    if not (logits.dtype is dt and logits.shape == shape and logits.stride() == stride and
+            (draft_probs is None) == (q_stride is None) and
+            (draft_probs is None or (draft_probs.dtype is f32 and draft_probs.shape == shape and draft_probs.stride() == q_stride)) and
+            tokens.dtype is i64 and emitted.dtype is i64 and q_start.dtype is i32 and n_emitted.dtype is i32 and u.dtype is f32 and
+            u_next.dtype is f32 and tokens.shape == rows and emitted.shape == rows and u.shape == rows and q_start.shape == starts and
+            u_next.shape == each and n_emitted.shape == each and tokens.is_contiguous() and emitted.is_contiguous() and
+            q_start.is_contiguous() and n_emitted.is_contiguous() and u.is_contiguous() and u_next.is_contiguous() and
+            (logp is None or (logp.dtype is f32 and logp.shape == rows and logp.is_contiguous())) and
+            (keep is None or (kv_len is not None and keep.dtype is i64 and keep.shape == each and keep.is_contiguous() and
+                              kv_len.dtype is i64 and kv_len.shape == each and kv_len.is_contiguous()))):
+        _verify_check(desc, logits, tokens, q_start, u, u_next, n_emitted, emitted, logp, draft_probs, kv_len, keep)
     dev = ws.get_device()
     if dev < 0 or not (dev == logits.get_device() == tokens.get_device() == q_start.get_device() == u.get_device() ==
                        u_next.get_device() == n_emitted.get_device() == emitted.get_device() == torch._C._cuda_getDevice()) or \
             (logp is not None and logp.get_device() != dev) or (draft_probs is not None and draft_probs.get_device() != dev) or \
             (keep is not None and not keep.get_device() == kv_len.get_device() == dev):
         _one_gpu(logits, tokens, q_start, u, u_next, n_emitted, emitted, logp, ws, draft_probs, kv_len, keep)
-    _check(lib().ls_draft_verify(desc, logits.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(), tokens.data_ptr(),
+    _done((_lib or lib()).ls_draft_verify(desc, logits.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(), tokens.data_ptr(),
                                  q_start.data_ptr(), u.data_ptr(), u_next.data_ptr(), None if keep is None else kv_len.data_ptr(),
                                  n_emitted.data_ptr(), emitted.data_ptr(), None if logp is None else logp.data_ptr(),
                                  None if keep is None else keep.data_ptr(), ws.data_ptr(), _nbytes(ws), _stream_of(stream, dev)))
@@ -863,8 +894,12 @@ def gdn_decode_desc(q, k, v, states, batch, max_q) -> GdnDecodeDesc:
     desc = GdnDecodeDesc(_dtype_code(q.dtype), v.shape[1], q.shape[1], q.shape[2], v.shape[2], batch, max_q, 0,
                          q.shape[0], _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"),
                          states.shape[0])
-    desc.layout = q.shape, k.shape, v.shape, q.stride(), k.stride(), v.stride()
+    n, h = v.shape[0], v.shape[1]
+    desc.layout = (q.dtype, q.shape, v.shape, q.stride(), k.stride(), v.stride(), states.shape, (n, h), (batch + 1,), (batch,))
     return desc
+
+
+_NO_LAYOUT = (None,) * 10  # of a desc that was not made from tensors: all checks by name
 
 
 def _gdn_decode_check(desc, states, q, k, v, g, beta, q_start, state_in, state_out, o, n_use):
@@ -893,16 +928,17 @@ def ls_gdn_decode(desc, states, q, k, v, g, beta, q_start, state_in, state_out, 
     """New tokens of each sequence through its recurrent state, from slot state_in[b] to slot state_out[b]
     (None: not kept); see ls.h."""
     torch = _torch or _lazy_torch()
-    n, b, h = desc.total_q, desc.batch, desc.heads
-    f32, i32, dt = torch.float32, torch.int32, q.dtype
-    if not ((q.shape, k.shape, v.shape, q.stride(), k.stride(), v.stride()) == desc.layout and _CODES.get(dt) == desc.dtype and
-            (k.dtype, v.dtype, states.dtype, g.dtype, beta.dtype, q_start.dtype, state_in.dtype) == (dt, dt, f32, f32, f32, i32, i32) and
-            states.shape == (desc.n_states, h, desc.dv, desc.dk) and g.shape == beta.shape == (n, h) and q_start.shape == (b + 1,) and
-            state_in.shape == (b,) and states.is_contiguous() and g.is_contiguous() and beta.is_contiguous() and
-            q_start.is_contiguous() and state_in.is_contiguous() and
-            (state_out is None or (state_out.dtype is i32 and state_out.shape == (b,) and state_out.is_contiguous())) and
-            (n_use is None or (n_use.dtype is i32 and n_use.shape == (b,) and n_use.is_contiguous())) and
-            (o is None or (o.dtype is dt and o.shape == v.shape and o.is_contiguous()))):
+    f32, i32 = torch.float32, torch.int32
+    dt, qk, vs, q_str, k_str, v_str, pool, gates, starts, each = desc.layout or _NO_LAYOUT
+    if not (q.dtype is dt and k.dtype is dt and v.dtype is dt and q.shape == qk and k.shape == qk and v.shape == vs and
+            q.stride() == q_str and k.stride() == k_str and v.stride() == v_str and
+            states.dtype is f32 and g.dtype is f32 and beta.dtype is f32 and q_start.dtype is i32 and state_in.dtype is i32 and
+            states.shape == pool and g.shape == gates and beta.shape == gates and q_start.shape == starts and state_in.shape == each and
+            states.is_contiguous() and g.is_contiguous() and beta.is_contiguous() and q_start.is_contiguous() and
+            state_in.is_contiguous() and
+            (state_out is None or (state_out.dtype is i32 and state_out.shape == each and state_out.is_contiguous())) and
+            (n_use is None or (n_use.dtype is i32 and n_use.shape == each and n_use.is_contiguous())) and
+            (o is None or (o.dtype is dt and o.shape == vs and o.is_contiguous()))):
         _gdn_decode_check(desc, states, q, k, v, g, beta, q_start, state_in, state_out, o, n_use)
     dev = states.get_device()
     if dev < 0 or not (dev == q.get_device() == k.get_device() == v.get_device() == g.get_device() == beta.get_device() ==
@@ -910,7 +946,7 @@ def ls_gdn_decode(desc, states, q, k, v, g, beta, q_start, state_in, state_out, 
             (state_out is not None and state_out.get_device() != dev) or (n_use is not None and n_use.get_device() != dev) or \
             (o is not None and o.get_device() != dev) or (ws is not None and ws.get_device() != dev):
         _one_gpu(states, q, k, v, g, beta, q_start, state_in, state_out, o, ws, n_use)
-    _check(lib().ls_gdn_decode(desc, states.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+    _done((_lib or lib()).ls_gdn_decode(desc, states.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
                                beta.data_ptr(), q_start.data_ptr(), None if n_use is None else n_use.data_ptr(), state_in.data_ptr(),
                                None if state_out is None else state_out.data_ptr(), None if o is None else o.data_ptr(),
                                None if ws is None else ws.data_ptr(), 0 if ws is None else _nbytes(ws), _stream_of(stream, dev)))

@@ -73,10 +73,13 @@ const char* kKernelNames[kNumKernelIds] = {
 
 // ------------------------------------------------------------------ devices
 int device_sms() {
+  static std::atomic<int> known[64];  // by device; asking the runtime takes longer than a small call's checks
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
     return 152;
+  if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 

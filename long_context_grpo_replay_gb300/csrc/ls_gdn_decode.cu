@@ -18,6 +18,8 @@
 // sequences 43 us, where the states' bytes would take 22.  Three blocks an SM, sixteen
 // lanes to four rows, and a token's operands loaded under the one before it were no
 // faster (45, 50 and 47 us).
+#include <atomic>
+
 #include "ls_internal.h"
 #include "ls_tc.cuh"
 
@@ -267,9 +269,16 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_decode_kernel(const GdnDecode
 
 template <typename T>
 cudaError_t launch(const GdnDecodeParams& p, cudaStream_t s) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(gdn_decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared<T>));
+  static std::atomic<uint64_t> allowed;  // devices on which the kernel may use its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(gdn_decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared<T>));
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
   const int64_t units = (int64_t)p.d.batch * p.d.heads * 2, most = 2 * device_sms();
   if (units > INT32_MAX) return cudaErrorInvalidConfiguration;
   gdn_decode_kernel<T><<<(unsigned)(units < most ? units : most), kThreads, sizeof(Shared<T>), s>>>(p);

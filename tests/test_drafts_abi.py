@@ -169,6 +169,10 @@ def test_binding_checks_tensors(ls):
         assert "GPU" not in str(e.value)
     with pytest.raises(ValueError, match="keep"):
         ls.ls_draft_verify(*args, keep=z(3, dt=I64))
+    changed = ls.verify_desc(logits, 3, 2)
+    changed.total_q = 4                                     # by hand: the tensors are no longer the desc's
+    with pytest.raises(ValueError, match="desc"):
+        ls.ls_draft_verify(changed, *args[1:])
     with pytest.raises(ValueError, match="draft_probs"):
         ls.ls_draft_verify(*args, draft_probs=logits[:, :99])
     q, v, s = z(5, 2, 128, dt=F32), z(5, 4, 128, dt=F32), z(6, 4, 128, 128, dt=F32)
@@ -180,6 +184,10 @@ def test_binding_checks_tensors(ls):
         ls.gdn_decode_desc(q, q, v, s.bfloat16(), 3, 2)
     d = ls.gdn_decode_desc(q, q, v, s, 3, 2)
     args = [d, s, q, q, v, z(5, 4, dt=F32), z(5, 4, dt=F32), z(4), z(3), z(3), v.clone()]
+    changed = ls.gdn_decode_desc(q, q, v, s, 3, 2)
+    changed.heads = 2
+    with pytest.raises(ValueError, match="desc"):
+        ls.ls_gdn_decode(changed, *args[1:])
     for at, bad in ((1, s[:5]), (2, q[:4]), (2, q.bfloat16()), (3, z(5, 4, 128, dt=F32)[:, ::2]), (4, v[:, :3]), (5, z(5, 3, dt=F32)),
                     (6, z(5, 4)), (7, z(3)), (8, z(3, dt=I64)), (9, z(4)), (10, v.bfloat16())):
         with pytest.raises((TypeError, ValueError)) as e:
