@@ -78,9 +78,9 @@ struct Stretch {
   const int32_t* refs;
   int64_t lo, hi;
   int steps;
-  uint32_t used;
+  uint32_t used, unused;
   bool kept;
-  __device__ Stretch(const Team<C>& t, const int32_t* r, int32_t pages) : refs(r), used(0) {
+  __device__ Stretch(const Team<C>& t, const int32_t* r, int32_t pages) : refs(r), used(0), unused(0) {
     const int64_t each = ((int64_t)per(pages, t.warps) + 31) / 32 * 32;
     lo = t.gw * each + t.lane, hi = t.gw * each + each < pages ? t.gw * each + each : pages;
     steps = (int)(each / 32), kept = steps <= 32;
@@ -88,13 +88,29 @@ struct Stretch {
       for (int x0 = 0; x0 < steps; x0 += 8) {
 #pragma unroll
         for (int x = 0; x < 8; ++x)
-          if (x0 + x < steps && in(x0 + x)) used |= (__ldcg(refs + page(x0 + x)) > 0 ? 1u : 0u) << (x0 + x);
+          if (x0 + x < steps && in(x0 + x)) {
+            const bool is = __ldcg(refs + page(x0 + x)) > 0;
+            used |= (is ? 1u : 0u) << (x0 + x), unused |= (is ? 0u : 1u) << (x0 + x);
+          }
       }
   }
   __device__ int64_t page(int x) const { return lo + 32 * x; }
   __device__ bool in(int x) const { return page(x) < hi; }
-  __device__ bool taken(int x) const { return kept ? used >> x & 1 : __ldcg(refs + page(x)) > 0; }
-  __device__ bool free(int x) const { return in(x) && !taken(x); }
+  __device__ bool taken(int x) const { return kept ? used >> x & 1 : in(x) && __ldcg(refs + page(x)) > 0; }
+  __device__ bool free(int x) const { return kept ? unused >> x & 1 : in(x) && __ldcg(refs + page(x)) <= 0; }
+  // This lane's pages that are free, that are taken.
+  __device__ int count_free() const {
+    int n = __popc(unused);
+    if (!kept)
+      for (int x = 0; x < steps; ++x) n += free(x);
+    return n;
+  }
+  __device__ int count_taken() const {
+    int n = __popc(used);
+    if (!kept)
+      for (int x = 0; x < steps; ++x) n += taken(x);
+    return n;
+  }
 };
 
 // What a call says of its sequences, and what is worked out of it.
@@ -215,9 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_advance_kernel(const PagesP
     __syncthreads();
   }
   const int wanted = carry;
-  int free = 0;
-  for (int x = 0; x < stretch.steps; ++x) free += stretch.free(x);
-  free = warp_sum(free);
+  const int free = warp_sum(stretch.count_free());
   if (t.lane == 0) count[t.warp] = free;
   t.sync();
   const int2 rank = t.prefix(count);
@@ -343,13 +357,11 @@ __global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const PagesP
   const int32_t S = p.b.page_size, pool = p.b.pool_pages;
   const bool same = p.refs_out == p.b.refs;
   const Stretch<C> stretch(t, p.b.refs, pool);
-  int live = 0;
-  for (int x = 0; x < stretch.steps; ++x) live += stretch.in(x) && stretch.taken(x);
-  live = warp_sum(live);
+  const int live = warp_sum(stretch.count_taken());
   if (t.lane == 0) live_of[t.warp] = live;
   t.sync();
   const int32_t A = t.prefix(live_of).y;  // pages in use: they end in [0, A)
-  auto goes = [&](int x) { return stretch.in(x) && stretch.taken(x) && stretch.page(x) >= A; };
+  auto goes = [&](int x) { return stretch.taken(x) && stretch.page(x) >= A; };
   auto gap = [&](int x) { return stretch.free(x) && stretch.page(x) < A; };
   int low = 0, high = 0;
   for (int x = 0; x < stretch.steps; ++x) low += gap(x), high += goes(x);
