@@ -88,6 +88,7 @@ ls_status pages_params(const ls_page_book* b, int64_t n, void* ws, size_t ws_byt
   LS_CHECK(check_ws(ws, ws_bytes, kWsHeader + pages_scratch(*b)));
   p->b = *b;
   p->n = (int32_t)n;
+  page_divisor(b->page_size, &p->page_mul, &p->page_shift);
   p->status = static_cast<uint32_t*>(ws);
   int32_t* w = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kWsHeader);
   p->list = w, w += b->pool_pages;

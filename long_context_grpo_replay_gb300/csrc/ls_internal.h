@@ -164,6 +164,8 @@ void set_last_error(const char* msg);
 ls_status fail(ls_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 ls_status check_ws(const void* ws, size_t ws_bytes, size_t need);
 ls_status check_cache(const ls_kv_cache* c);
+// j / d = umulhi(j, mul) >> shift for 0 <= j < 2^31 (mul 0: d is 1).
+void page_divisor(uint32_t d, uint32_t* mul, uint32_t* shift);
 int device_sms();
 bool device_is_sm100_family();
 bool force_simt();  // LS_FORCE_SIMT is set
@@ -334,11 +336,13 @@ struct PagesParams {
   int32_t* table_out;
   int32_t* refs_out;
   bool drop_all;         // advance: keep nothing
+  uint32_t page_mul, page_shift;  // of a division by page_size (page_divisor)
+  int32_t share_shift;   // 2^this threads share a sequence
   int32_t* list;         // [pool_pages] free pages in order
   int32_t* high;         // [pool_pages] compact: pages that move, in order
   int32_t* rank;         // [pool_pages] compact: their places in `high`
   int32_t* owner;        // [8][n_seqs] a block's: who names the sequence
-  int32_t* lists;        // [8][6][n_seqs] a block's, where shared memory does not hold them
+  int32_t* lists;        // [8][7][n_seqs] a block's, where shared memory does not hold them
   uint32_t* status;
 };
 size_t pages_scratch(const ls_page_book& b);

@@ -28,10 +28,19 @@ constexpr int kWarps = kThreads / 32;
 constexpr int32_t kShared = 1 << 30;   // need[]: its last page is others' too
 constexpr int32_t kNoRoom = INT32_MIN; // need[]: the table's row ends, or its last page is no page
 
-constexpr int kListed = 1920;  // sequences of a call that are kept in shared memory
-constexpr int kListArrays = 6;
+constexpr int kListed = 1664;  // sequences of a call that are kept in shared memory
+constexpr int kListArrays = 7;
 
-__device__ __forceinline__ int32_t per(int32_t n, int32_t page) { return n > 0 ? (n - 1) / page + 1 : 0; }
+__device__ __forceinline__ int32_t per(int32_t n, int32_t each) { return n > 0 ? (n - 1) / each + 1 : 0; }
+// A book's page size, to divide by.
+struct Pages {
+  int32_t S;
+  uint32_t mul, shift;
+  __device__ explicit Pages(const PagesParams& p) : S(p.b.page_size), mul(p.page_mul), shift(p.page_shift) {}
+  __device__ int32_t page(int32_t pos) const { return mul ? (int32_t)(__umulhi((uint32_t)pos, mul) >> shift) : pos; }
+  __device__ int32_t row(int32_t pos) const { return pos - page(pos) * S; }
+  __device__ int32_t of(int32_t n) const { return n > 0 ? page(n - 1) + 1 : 0; }  // that n tokens take
+};
 __device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
 __device__ __forceinline__ void start() {
   asm volatile("griddepcontrol.launch_dependents;");
@@ -51,12 +60,6 @@ struct Team {
     gw = (int)rank * kWarps + (int)warp;
   }
   __device__ void sync() const { Cluster<C>::sync(); }
-  // Threads that share one of n sequences: a power of two, eight or more.
-  __device__ int shares(int n) const {
-    int w = 8;
-    while (w < threads && 2 * w * (int64_t)n <= threads) w *= 2;
-    return w;
-  }
   // Of each warp's count (count[kWarps] in each block): the sum before this warp, and of all.
   __device__ int2 prefix(const int* count) const {
     int before = 0, all = 0;
@@ -115,13 +118,13 @@ struct Stretch {
 
 // What a call says of its sequences, and what is worked out of it.
 struct Lists {
-  int32_t *seq, *keep, *old, *need, *begin, *last;
+  int32_t *seq, *keep, *old, *need, *begin, *last, *grow;
 };
 // In shared memory where they fit, else each block in its own part of the workspace.
 __device__ __forceinline__ Lists lists(const PagesParams& p, int32_t* shared, uint32_t rank) {
   int32_t* w = p.n <= kListed ? shared : p.lists + (int64_t)rank * kListArrays * p.b.n_seqs;
   const int64_t n = p.n <= kListed ? kListed : p.b.n_seqs;
-  return Lists{w, w + n, w + 2 * n, w + 3 * n, w + 4 * n, w + 5 * n};
+  return Lists{w, w + n, w + 2 * n, w + 3 * n, w + 4 * n, w + 5 * n, w + 6 * n};
 }
 
 // ---------------------------------------------------------------- advance
@@ -132,17 +135,19 @@ __global__ void __launch_bounds__(kThreads, 1) pages_advance_kernel(const PagesP
   start();
   const Team<C> t;
   const Lists l = lists(p, listed, t.rank);
-  const int32_t S = p.b.page_size, cap = p.b.pages_per_seq * S;
+  const Pages pages(p);
+  const int32_t S = pages.S, cap = p.b.pages_per_seq * S;
   int32_t* owner = p.owner + (int64_t)t.rank * p.b.n_seqs;
-  auto grows = [&](int i) { return p.q_start ? p.q_start[i + 1] - p.q_start[i] : 0; };
   // the lists, before anything is changed
   bool bad = false;
   for (int i = threadIdx.x; i < p.n; i += kThreads) {
     const int s = p.seqs ? p.seqs[i] : i;
     bool ok = s >= 0 && s < p.b.n_seqs;
     int64_t old = 0, keep = 0;
+    int32_t grow = 0;
     if (p.q_start) {
       const int a = p.q_start[i], e = p.q_start[i + 1];
+      grow = e - a;
       ok = ok && a >= 0 && a <= e && e <= p.total_q && (i != 0 || a == 0) && (i != p.n - 1 || e == p.total_q);
     }
     if (s >= 0 && s < p.b.n_seqs) {
@@ -150,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_advance_kernel(const PagesP
       ok = ok && old >= 0 && old <= cap && keep >= 0 && keep <= old;
       if (p.seqs) owner[s] = i;
     }
-    l.seq[i] = s, l.old[i] = (int32_t)old, l.keep[i] = (int32_t)keep;
+    l.seq[i] = s, l.old[i] = (int32_t)old, l.keep[i] = (int32_t)keep, l.grow[i] = grow;
     bad |= !ok;
   }
   if (p.seqs) {
@@ -170,17 +175,17 @@ __global__ void __launch_bounds__(kThreads, 1) pages_advance_kernel(const PagesP
   // The page that a sequence goes on in, for the first of this thread's sequences: nothing
   // waits for it before the pages that are dropped are done with.
   auto last_of = [&](int i) {
-    const int32_t keep = l.keep[i];
-    return keep % S != 0 && grows(i) > 0 && (int64_t)keep + grows(i) <= cap
-               ? p.b.page_table[(int64_t)l.seq[i] * p.b.pages_per_seq + keep / S]
+    const int32_t keep = l.keep[i], grow = l.grow[i];
+    return grow > 0 && pages.row(keep) != 0 && (int64_t)keep + grow <= cap
+               ? p.b.page_table[(int64_t)l.seq[i] * p.b.pages_per_seq + pages.page(keep)]
                : -1;
   };
   int32_t last = (int)threadIdx.x < p.n ? last_of(threadIdx.x) : -1;
-  const int width = t.shares(p.n), sub = t.tid % width, groups = t.threads / width;
+  const int width = 1 << p.share_shift, sub = t.tid & (width - 1), groups = t.threads >> p.share_shift;
   // pages that are dropped
-  for (int i = t.tid / width; i < p.n; i += groups) {
+  for (int i = t.tid >> p.share_shift; i < p.n; i += groups) {
     const int32_t* row = p.b.page_table + (int64_t)l.seq[i] * p.b.pages_per_seq;
-    for (int32_t j = per(l.keep[i], S) + sub; j < per(l.old[i], S); j += width) {
+    for (int32_t j = pages.of(l.keep[i]) + sub, end = pages.of(l.old[i]); j < end; j += width) {
       const int32_t page = row[j];
       bool ok = page >= 0 && page < p.b.pool_pages;
       if (ok && atomicSub(p.b.refs + page, 1) <= 0) atomicAdd(p.b.refs + page, 1), ok = false;
@@ -200,11 +205,11 @@ __global__ void __launch_bounds__(kThreads, 1) pages_advance_kernel(const PagesP
     if (i < p.n) {
       if (i0) last = last_of(i), names = others(last);
       const int32_t keep = l.keep[i];
-      const int64_t want = (int64_t)keep + grows(i);
+      const int64_t want = (int64_t)keep + l.grow[i];
       full = want > cap;
       if (!full && want > keep) {
-        need = per((int32_t)want, S) - per(keep, S);
-        if (keep % S != 0) {
+        need = pages.of((int32_t)want) - pages.of(keep);
+        if (pages.row(keep) != 0) {
           if (last < 0 || last >= p.b.pool_pages)
             full = true, need = 0, atomicOr(p.status, kStatusBadPage);
           else
@@ -247,13 +252,13 @@ __global__ void __launch_bounds__(kThreads, 1) pages_advance_kernel(const PagesP
   }
   t.sync();  // the list is there, and no block reads another's counts any more
   // the new lengths, entries and slots
-  for (int i = t.tid / width; i < p.n; i += groups) {
+  for (int i = t.tid >> p.share_shift; i < p.n; i += groups) {
     const int s = l.seq[i];
     const int32_t word = l.need[i], begin = l.begin[i], keep = l.keep[i], page0 = l.last[i];
     const bool shared = word != kNoRoom && (word & kShared);
     const int32_t need = word == kNoRoom ? 0 : word & ~kShared;
     const bool served = word != kNoRoom && (need == 0 || (int64_t)begin + need <= rank.y);
-    const int32_t grow = grows(i), first = per(keep, S) - (shared ? 1 : 0);
+    const int32_t grow = l.grow[i], first = pages.of(keep) - (shared ? 1 : 0);
     int32_t* row = p.b.page_table + (int64_t)s * p.b.pages_per_seq;
     if (sub == 0) {
       p.b.kv_len[s] = served ? keep + grow : keep;
@@ -262,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_advance_kernel(const PagesP
       if (p.copies) {
         p.copies[3 * (int64_t)i] = copy ? page0 : -1;
         p.copies[3 * (int64_t)i + 1] = copy ? __ldcg(p.list + begin) : -1;
-        p.copies[3 * (int64_t)i + 2] = copy ? keep % S : -1;
+        p.copies[3 * (int64_t)i + 2] = copy ? pages.row(keep) : -1;
       }
       if (!served) atomicOr(p.status, kStatusNoPages);
     }
@@ -275,9 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1) pages_advance_kernel(const PagesP
     if (p.q_start) {
       const int32_t t0 = p.q_start[i];
       for (int32_t x = sub; x < grow; x += width) {
-        const int32_t pos = keep + x, j = pos / S;
+        const int32_t pos = keep + x, j = pages.page(pos);
         const int32_t page = !served ? 0 : j >= first ? __ldcg(p.list + begin + j - first) : page0;
-        p.slots[t0 + x] = served ? (int64_t)page * S + pos % S : -1;
+        p.slots[t0 + x] = served ? (int64_t)page * S + (pos - j * S) : -1;
       }
     }
   }
@@ -290,7 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const PagesPara
   start();
   const Team<C> t;
   const Lists l = lists(p, listed, t.rank);  // seq: destinations, begin: sources, keep: new lengths
-  const int32_t S = p.b.page_size, cap = p.b.pages_per_seq * S;
+  const Pages pages(p);
+  const int32_t cap = p.b.pages_per_seq * pages.S;
   int32_t* owner = p.owner + (int64_t)t.rank * p.b.n_seqs;
   auto in = [&](int s) { return s >= 0 && s < p.b.n_seqs; };
   bool bad = false;
@@ -316,9 +322,9 @@ __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const PagesPara
     if (t.tid == 0) atomicOr(p.status, kStatusBadIndex);
     return;
   }
-  const int width = t.shares(p.n), sub = t.tid % width;
-  for (int i = t.tid / width; i < p.n; i += t.threads / width) {
-    const int32_t had = per(l.old[i], S), want = per(l.keep[i], S);
+  const int width = 1 << p.share_shift, sub = t.tid & (width - 1);
+  for (int i = t.tid >> p.share_shift; i < p.n; i += t.threads >> p.share_shift) {
+    const int32_t had = pages.of(l.old[i]), want = pages.of(l.keep[i]);
     const int32_t* from = p.b.page_table + (int64_t)l.begin[i] * p.b.pages_per_seq;
     int32_t* to = p.b.page_table + (int64_t)l.seq[i] * p.b.pages_per_seq;
 #pragma unroll 4
@@ -479,7 +485,11 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, int block
   cfg.attrs = at, cfg.numAttrs = blocks ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
-cudaError_t launch_team(void (*one)(PagesParams), void (*eight)(PagesParams), bool wide, const PagesParams& p, cudaStream_t s) {
+cudaError_t launch_team(void (*one)(PagesParams), void (*eight)(PagesParams), bool wide, PagesParams p, cudaStream_t s) {
+  // Threads that share one of n sequences: a power of two, eight or more.
+  const int threads = (wide ? 8 : 1) * kThreads;
+  p.share_shift = 3;
+  while ((2 << p.share_shift) <= threads && ((int64_t)p.n << (p.share_shift + 1)) <= threads) ++p.share_shift;
   LaunchScope ls(kKPages, s);
   return wide ? launch_early(eight, dim3(8), kThreads, 8, s, p) : launch_early(one, dim3(1), kThreads, 0, s, p);
 }

@@ -71,21 +71,6 @@ ls_status check_cached(const ls_cached_attn_desc* d, const ls_kv_cache* c) {
   return LS_OK;
 }
 
-// Multiplier and shift of j / d for 0 <= j < 2^31 (d >= 1): with 2^(s-1) < d <=
-// 2^s, m = ceil(2^(31+s) / d) is below 2^32 and off by e < d <= 2^s, so j m /
-// 2^(31+s) exceeds j / d by j e / (d 2^(31+s)) < 1 / d.  umulhi takes 2^32 of
-// the divisor; d = 1 has no such pair, and a multiplier of 0 stands for it.
-void page_divisor(uint32_t d, uint32_t* mul, uint32_t* shift) {
-  uint32_t s = 0;
-  while ((1ull << s) < d) ++s;
-  if (s == 0) {
-    *mul = 0, *shift = 0;
-    return;
-  }
-  *mul = (uint32_t)(((1ull << (31 + s)) + d - 1) / d);
-  *shift = s - 1;
-}
-
 CachedPlan plan_cached(const ls_cached_attn_desc& d, const ls_kv_cache& c) {
   CachedPlan pl{};
   const int gq = d.hq / c.hkv, sms = device_sms();
@@ -174,6 +159,21 @@ size_t vocab_need(const ls_vocab_desc& d, bool with_grad) {
 }
 
 }  // namespace
+
+// Multiplier and shift of j / d for 0 <= j < 2^31 (d >= 1): with 2^(s-1) < d <=
+// 2^s, m = ceil(2^(31+s) / d) is below 2^32 and off by e < d <= 2^s, so j m /
+// 2^(31+s) exceeds j / d by j e / (d 2^(31+s)) < 1 / d.  umulhi takes 2^32 of
+// the divisor; d = 1 has no such pair, and a multiplier of 0 stands for it.
+void page_divisor(uint32_t d, uint32_t* mul, uint32_t* shift) {
+  uint32_t s = 0;
+  while ((1ull << s) < d) ++s;
+  if (s == 0) {
+    *mul = 0, *shift = 0;
+    return;
+  }
+  *mul = (uint32_t)(((1ull << (31 + s)) + d - 1) / d);
+  *shift = s - 1;
+}
 
 ls_status check_cache(const ls_kv_cache* c) {
   if (!c) return fail(LS_ERR_INVALID_ARGUMENT, "cache is NULL");
