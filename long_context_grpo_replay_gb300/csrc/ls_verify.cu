@@ -365,10 +365,11 @@ __device__ __forceinline__ Sums segment(const Source<T>& src, int lo, int stop, 
 
 // The token of elements from .. stop-1 in which the running sum of the weights passes t
 // (all of a block): its index in the thread that has it, below 0 in the others.  over_q:
-// weights are max(e - q Z, 0), Z = z_hi + z_lo; but: an element that weighs nothing.
+// weights are max(e - q Z, 0), Z = z_hi + z_lo; but: an element that weighs nothing.  its:
+// the token's logit, in the same thread.
 template <typename T>
 __device__ __forceinline__ int look(const Source<T>& src, const Row& w, const float2* table, int64_t from, int stop, uint64_t t,
-                                    bool over_q, float z_hi, float z_lo, int but, uint64_t* scan, int* most_of) {
+                                    bool over_q, float z_hi, float z_lo, int but, uint64_t* scan, int* most_of, float& its) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int found = -1, last = -1;  // the last token so far that weighs anything
   for (int64_t lo = from; lo < stop && found == -1; lo += kThreads * 8) {
@@ -376,8 +377,9 @@ __device__ __forceinline__ int look(const Source<T>& src, const Row& w, const fl
     uint64_t x[8], sum = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = 0;
+    Raw8<T> raw{};
     if (v < stop) {
-      const Raw8<T> raw = src.logits(v);
+      raw = src.logits(v);
       Raw8<float> share{};
       if (over_q) share = src.shares(v);
 #pragma unroll
@@ -418,7 +420,7 @@ __device__ __forceinline__ int look(const Source<T>& src, const Row& w, const fl
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           run += x[i];
-          if (found < 0 && run > t) found = v + i;
+          if (found < 0 && run > t) found = v + i, its = element(raw, i);
         }
     } else {
       t -= total;
@@ -426,7 +428,7 @@ __device__ __forceinline__ int look(const Source<T>& src, const Row& w, const fl
     __syncthreads();
   }
   // The sum that t was taken from may be past the tiles' own by rounding: their last token then.
-  if (found == -1 && tid == 0) found = last >= 0 ? last : max((int)from, 0);
+  if (found == -1 && tid == 0) found = last >= 0 ? last : max((int)from, 0), its = value(src.z[found]);
   return found;
 }
 
@@ -559,11 +561,11 @@ __global__ void __launch_bounds__(kThreads, 4) verify_draw_kernel(const VerifyPa
       sq[i] = in ? Team::at(seg_q + s % kWarps, s / kWarps) : 0.f;
     }
     const uint64_t all = warp_sum(e[0] + e[1]);
-    const float off = (float)((int64_t)all - fixed(w.z0));
+    const float off = (float)((int64_t)all - fixed(w.z0)) * 0x1p-61f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t fixed = q ? (int64_t)x[i] - __float2ll_rn(off * sq[i]) : (int64_t)x[i];
-      x[i] = fixed > 0 ? (uint64_t)fixed : 0;
+      const int64_t right = q ? (int64_t)x[i] - fixed(off * sq[i]) : (int64_t)x[i];
+      x[i] = right > 0 ? (uint64_t)right : 0;
     }
     const bool none = warp_sum(x[0] + x[1]) < (1ull << 31);  // of 2^61: rounding alone
     if (none) x[0] = e[0], x[1] = e[1];
@@ -586,10 +588,11 @@ __global__ void __launch_bounds__(kThreads, 4) verify_draw_kernel(const VerifyPa
     const int64_t from = (int64_t)picked * each - shift;
     const int stop = (int)(from + each < V ? from + each : V);
     const float z_hi = (float)z_all * 0x1p-61f, z_lo = (float)((int64_t)z_all - fixed(z_hi)) * 0x1p-61f;
-    const int found = look(src, w, table, from, stop, target, q && !use_p, z_hi, z_lo, use_p ? -1 : (int)draft, scan, passes);
+    float its = 0.f;
+    const int found = look(src, w, table, from, stop, target, q && !use_p, z_hi, z_lo, use_p ? -1 : (int)draft, scan, passes, its);
     if (found >= 0) {
       p.emitted[r] = found;
-      if (p.logp) p.logp[r] = (value(z[found]) - row.x) * p.d.logit_scale - logf(row.y);
+      if (p.logp) p.logp[r] = (its - row.x) * p.d.logit_scale - logf(row.y);
     }
   }
   Team::wait();  // the others have read this block's
@@ -736,11 +739,12 @@ __global__ void __launch_bounds__(kThreads) one_draw_kernel(const VerifyParams p
   const int shift = (int)(reinterpret_cast<uintptr_t>(z) & 15) / (int)sizeof(T);
   const Source<T> src{z, nullptr, V, false};
   const int64_t from = (int64_t)picked * kOne - shift;
-  const int found = look(src, w, table, from, (int)(from + kOne < V ? from + kOne : V), target, false, 0.f, 0.f, -1, scan, most);
+  float its = 0.f;
+  const int found = look(src, w, table, from, (int)(from + kOne < V ? from + kOne : V), target, false, 0.f, 0.f, -1, scan, most, its);
   if (found >= 0) {
     p.emitted[first] = found;
     if (p.logp)
-      p.logp[first] = (value(z[found]) - top) * p.d.logit_scale - logf((float)total * 0x1p-61f / __uint_as_float(w.scale));
+      p.logp[first] = (its - top) * p.d.logit_scale - logf((float)total * 0x1p-61f / __uint_as_float(w.scale));
   }
 }
 
