@@ -558,7 +558,8 @@ LS_API ls_status ls_pages_workspace_size(const ls_page_book* book, size_t* bytes
  * row ends, the sequence does not grow (slots -1, which ls_cache_write leaves
  * out), and the status word says so (LS_ERR_OUT_OF_PAGES); later ones still do
  * if they need no page.
- *   keep int64 [n]; q_start int32 [n+1]; slots int64 [total_q]; copies int32 [n][3]. */
+ *   keep int64 [n]; q_start int32 [n+1]; slots int64 [total_q] (total_q at most 2^29);
+ *   copies int32 [n][3]. */
 LS_API ls_status ls_pages_advance(const ls_page_book* book, int32_t n, const int32_t* seqs,
                                   const int64_t* keep, const int32_t* q_start, int64_t total_q,
                                   int64_t* slots, int32_t* copies, void* ws, size_t ws_bytes,

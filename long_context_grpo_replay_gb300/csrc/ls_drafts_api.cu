@@ -140,7 +140,7 @@ ls_status ls_pages_advance(const ls_page_book* book, int32_t n, const int32_t* s
                            void* stream) {
   LS_CHECK(check_book(book));
   if (total_q < 0) return fail(LS_ERR_INVALID_ARGUMENT, "total_q < 0");
-  if (total_q > INT32_MAX) return fail(LS_ERR_UNSUPPORTED, "total_q > 2^31-1");
+  if (total_q > (1 << 29)) return fail(LS_ERR_UNSUPPORTED, "total_q > 2^29");  // so that counts of pages fit 30 bits
   if (total_q > 0 && (!q_start || !slots || n == 0))
     return fail(LS_ERR_INVALID_ARGUMENT, "new tokens need q_start, slots and sequences");
   if (q_start && !copies && n > 0) return fail(LS_ERR_INVALID_ARGUMENT, "growing sequences need copies");

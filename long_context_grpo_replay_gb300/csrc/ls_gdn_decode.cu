@@ -5,19 +5,20 @@
 // A token does 7 operations an element of a state that has to come from memory
 // and go back, so for a token or two the states' bytes bound it.  A row of S needs k,
 // q and its own element of v alone: the unit of work is half a head, 64 rows or 32 KB,
-// for all of a sequence's tokens.  Two blocks an SM take such units in turn; a
-// producer warp brings the coming ones into a ring of three stages by bulk copies
+// for all of a sequence's tokens.  Three blocks an SM take such units in turn; a
+// producer warp brings the coming ones into a ring of two stages by bulk copies
 // (state, and the tokens' k, q and v as they lie; the gates by 4-byte copies), so that
-// some 190 KB an SM are on their way whatever the others do.  Eight warps hold the
-// rows in registers, eight lanes a pair of rows with sixteen columns each, on packed
-// pairs of floats; a row sum is three shuffles for both rows.  The results leave by
-// plain stores in whole lines.
+// some 190 KB an SM are on their way whatever the others do.  Four warps hold the rows
+// in registers, eight lanes four rows with sixteen columns each, on packed pairs of
+// floats; the four row sums are four shuffles.  The results leave by plain stores in
+// whole lines.
 //   Measured: 96 sequences x 32 heads, one token, 405 MB in 69.5 us (5.8 TB/s, 86 % of
-// a copy's rate; 64 KB a block without the ring 92 us).  From three tokens on the
-// arithmetic counts, 8 us a token for 64 x 32 heads: 1 to 6 drafted tokens of 64
-// sequences 43 us, where the states' bytes would take 22.  Three blocks an SM, sixteen
-// lanes to four rows, and a token's operands loaded under the one before it were no
-// faster (45, 50 and 47 us).
+// a copy's rate; 64 KB a block without the ring 92 us).  From four tokens on the
+// arithmetic counts, 7 us a token for 64 x 32 heads: 1 to 6 drafted tokens of 64
+// sequences 43 us, where the states' bytes would take 22; 16 tokens 130 us.  Two rows
+// to eight lanes in twice the warps take 144 us for those, four rows to sixteen lanes
+// 180; a token's operands loaded, and its sums taken, beside the one before it are no
+// faster.
 #include <atomic>
 
 #include "ls_internal.h"
@@ -28,9 +29,11 @@ namespace {
 
 constexpr int kD = 128;                 // dk = dv
 constexpr int kRows = 64;               // rows of a unit
-constexpr int kWarps = 8;               // that compute
+constexpr int kWarps = 4;               // that compute
+constexpr int kGroupRows = 4;           // rows of eight lanes: group, group + 16, + 32, + 48
 constexpr int kThreads = kWarps * 32 + 32;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
+constexpr int kBlocks = 3;               // an SM's
 
 template <typename T>
 struct Stage {
@@ -69,13 +72,40 @@ __device__ __forceinline__ float both(uint64_t x) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
   return lo + hi;
 }
-// Sums of x and y over eight lanes: x's in the lower four of them, y's in the others.
-__device__ __forceinline__ float sum_two(float x, float y, bool upper) {
-  float mine = upper ? y : x;
-  mine += __shfl_xor_sync(0xffffffffu, upper ? x : y, 4);
-  mine += __shfl_xor_sync(0xffffffffu, mine, 2);
-  mine += __shfl_xor_sync(0xffffffffu, mine, 1);
-  return mine;
+// This lane's sixteen columns of a token's k or q, or of a row of the state: 4 (l + 8 j) + 0..3.
+template <typename T>
+__device__ __forceinline__ void columns(const T* p, int l, uint64_t (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint64_t y[2];
+    pairs4(p + 4 * (l + 8 * j), y);
+    x[2 * j] = y[0], x[2 * j + 1] = y[1];
+  }
+}
+// The four rows' products with x, summed over eight lanes in four shuffles: lane l gets row l / 2's.
+__device__ __forceinline__ float row_sums(const uint64_t (&s)[kGroupRows][8], const uint64_t (&x)[8], int l) {
+  uint64_t y[kGroupRows] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int r = 0; r < kGroupRows; ++r) y[r] = tc::f2_fma(s[r][j], x[j], y[r]);
+  const float z[kGroupRows] = {both(y[0]), both(y[1]), both(y[2]), both(y[3])};
+  const bool four = l & 4, two = l & 2;
+  float a = four ? z[2] : z[0], b = four ? z[3] : z[1];
+  a += __shfl_xor_sync(0xffffffffu, four ? z[0] : z[2], 4);
+  b += __shfl_xor_sync(0xffffffffu, four ? z[1] : z[3], 4);
+  float c = two ? b : a;
+  c += __shfl_xor_sync(0xffffffffu, two ? a : b, 2);
+  c += __shfl_xor_sync(0xffffffffu, c, 1);
+  return c;
+}
+// All four in every lane, from what row_sums gave.
+__device__ __forceinline__ void share(float y, int l, float (&x)[kGroupRows]) {
+  const bool four = l & 4, two = l & 2;
+  const float z = __shfl_xor_sync(0xffffffffu, y, 2);
+  const float a = two ? z : y, b = two ? y : z;
+  const float c = __shfl_xor_sync(0xffffffffu, a, 4), d = __shfl_xor_sync(0xffffffffu, b, 4);
+  x[0] = four ? c : a, x[1] = four ? d : b, x[2] = four ? a : c, x[3] = four ? b : d;
 }
 
 // A float to shared memory; the barrier hears from the lane when all it asked for has come.
@@ -167,7 +197,7 @@ __device__ __forceinline__ void produce(const GdnDecodeParams& p, Shared<T>& sh)
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) gdn_decode_kernel(const GdnDecodeParams p) {
+__global__ void __launch_bounds__(kThreads, kBlocks) gdn_decode_kernel(const GdnDecodeParams p) {
   extern __shared__ __align__(16) char raw[];
   Shared<T>& sh = *reinterpret_cast<Shared<T>*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -194,9 +224,8 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_decode_kernel(const GdnDecode
     }
     return;
   }
-  const int group = tid / 8, l = tid % 8;  // rows `group` and `group` + 32 of the unit, columns 4 (l + 8 j) + 0..3
-  const bool upper = l & 4;
-  uint64_t s[2][8];
+  const int group = tid / 8, l = tid % 8;
+  uint64_t s[kGroupRows][8];
   for (int it = 0;; ++it) {
     const int at = it % kStages;
     if (!tc::mbar_wait(tc::smem_u32(&sh.full[at]), it / kStages & 1, &sh.abort)) {
@@ -206,50 +235,35 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_decode_kernel(const GdnDecode
     const Stage<T>& st = sh.stage[at];
     const int nt = st.nt;
     if (nt < 0) return;
-    if (st.first) {
+    if (st.first == 1) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int r = 0; r < kGroupRows; ++r) columns(st.s[group + 16 * r], l, s[r]);
+    } else if (st.first == 2) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint64_t x[2] = {0, 0};
-          if (st.first == 1) pairs4(&st.s[group + 32 * r][4 * (l + 8 * j)], x);
-          s[r][2 * j] = x[0], s[r][2 * j + 1] = x[1];
-        }
+      for (int r = 0; r < kGroupRows; ++r)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[r][j] = 0;
     }
     const float decay = lane < nt ? expf(st.g[lane]) : 0.f;  // a lane a token
-    T* o = p.o ? static_cast<T*>(p.o) + (st.tok * p.d.heads + st.head) * kD + st.row + group + (upper ? 32 : 0) : nullptr;
+    T* o = p.o ? static_cast<T*>(p.o) + (st.tok * p.d.heads + st.head) * kD + st.row + group + 16 * (l / 2) : nullptr;
     for (int t = 0; t < nt; ++t) {
       uint64_t k[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint64_t x[2];
-        pairs4(&st.k[t][4 * (l + 8 * j)], x);
-        k[2 * j] = x[0], k[2 * j + 1] = x[1];
-      }
-      uint64_t u0 = 0, u1 = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u0 = tc::f2_fma(s[0][j], k[j], u0), u1 = tc::f2_fma(s[1][j], k[j], u1);
-      const float mine = sum_two(both(u0), both(u1), upper), other = __shfl_xor_sync(0xffffffffu, mine, 4);
+      columns(st.k[t], l, k);
       const float a = __shfl_sync(0xffffffffu, decay, t), b = st.b[t];
-      const float w0 = b * (value(st.v[t][group]) - a * (upper ? other : mine));
-      const float w1 = b * (value(st.v[t][group + 32]) - a * (upper ? mine : other));
-      const uint64_t a2 = tc::f2(a, a), w02 = tc::f2(w0, w0), w12 = tc::f2(w1, w1);
+      float u[kGroupRows];
+      share(row_sums(s, k, l), l, u);
+      const uint64_t a2 = tc::f2(a, a);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        s[0][j] = tc::f2_fma(w02, k[j], tc::f2_mul(a2, s[0][j]));
-        s[1][j] = tc::f2_fma(w12, k[j], tc::f2_mul(a2, s[1][j]));
+      for (int r = 0; r < kGroupRows; ++r) {
+        const float w = b * (value(st.v[t][group + 16 * r]) - a * u[r]);
+        const uint64_t w2 = tc::f2(w, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[r][j] = tc::f2_fma(w2, k[j], tc::f2_mul(a2, s[r][j]));
       }
       if (o) {
-        uint64_t o0 = 0, o1 = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint64_t x[2];
-          pairs4(&st.q[t][4 * (l + 8 * j)], x);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) o0 = tc::f2_fma(s[0][2 * j + i], x[i], o0), o1 = tc::f2_fma(s[1][2 * j + i], x[i], o1);
-        }
-        const float x = sum_two(both(o0), both(o1), upper);
-        if ((l & 3) == 0) put(o, x);
+        columns(st.q[t], l, k);
+        const float x = row_sums(s, k, l);
+        if ((l & 1) == 0) put(o, x);
         o += (int64_t)p.d.heads * kD;
       }
     }
@@ -258,10 +272,10 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_decode_kernel(const GdnDecode
     if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.empty[at]));
     if (to >= 0) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int r = 0; r < kGroupRows; ++r)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<ulonglong2*>(p.states + to + (group + 32 * r) * kD + 4 * (l + 8 * j)) =
+          *reinterpret_cast<ulonglong2*>(p.states + to + (group + 16 * r) * kD + 4 * (l + 8 * j)) =
               make_ulonglong2(s[r][2 * j], s[r][2 * j + 1]);
     }
   }
@@ -279,7 +293,7 @@ cudaError_t launch(const GdnDecodeParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     allowed.fetch_or(bit, std::memory_order_relaxed);
   }
-  const int64_t units = (int64_t)p.d.batch * p.d.heads * 2, most = 2 * device_sms();
+  const int64_t units = (int64_t)p.d.batch * p.d.heads * 2, most = kBlocks * device_sms();
   if (units > INT32_MAX) return cudaErrorInvalidConfiguration;
   gdn_decode_kernel<T><<<(unsigned)(units < most ? units : most), kThreads, sizeof(Shared<T>), s>>>(p);
   return cudaGetLastError();

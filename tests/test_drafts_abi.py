@@ -65,7 +65,7 @@ def test_pages_calls(ls):
         ctypes.byref(b), n, seqs, keep, qs, total, slots, copies, ws, nb, None)
     assert adv(n=0, total=0) == 0 and adv(n=0, seqs=None, keep=None, qs=None, total=0, slots=None, copies=None) == 0
     assert adv(n=-1) == 1 and adv(n=5) == 1                  # a call names each sequence at most once
-    assert adv(total=-1) == 1 and adv(total=1 << 31) == 2
+    assert adv(total=-1) == 1 and adv(total=1 << 31) == 2 and adv(total=(1 << 29) + 1) == 2
     assert adv(qs=None) == 1 and adv(slots=None) == 1 and adv(copies=None) == 1 and adv(n=0) == 1
     assert adv(seqs=A + 2) == 1 and adv(keep=A + 4) == 1 and adv(qs=A + 1) == 1 and adv(slots=A + 4) == 1 and adv(copies=A + 2) == 1
     assert adv(ws=None) == 1 and adv(ws=A + 64) == 1 and adv(nb=need - 1) == 3
