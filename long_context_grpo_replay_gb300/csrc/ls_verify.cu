@@ -453,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_draw_kernel(const VerifyPa
       p.n_emitted[b] = 0;
       if (p.keep) p.keep[b] = p.kv_len[b];
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // who comes after this kernel comes after the rows' too
     return;
   }
   const int n = (int)n64, V = p.d.vocab;
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_draw_kernel(const VerifyPa
       d.x = p.tokens[r + 1], d.u = p.u[r];
       if (d.x >= 0 && d.x < V) {
         d.z = value(logits[r * p.d.logits_stride + d.x]);
-        if (p.probs) d.q = p.probs[r * p.d.draft_stride + d.x];
+        if (p.probs) d.q = fmaxf(p.probs[r * p.d.draft_stride + d.x], 0.f);
       }
     }
     return d;
@@ -683,8 +684,8 @@ __global__ void __launch_bounds__(kThreads) one_draw_kernel(const VerifyParams p
     if (bad || n == 0) p.n_emitted[b] = 0;
     if (p.keep) p.keep[b] = p.kv_len[b];  // a row that is drawn from drops nothing
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are there, and who comes after this kernel comes after them
   if (bad || n == 0) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are there
   const Part* parts = reinterpret_cast<const Part*>(p.parts) + first * p.chunks;
   const int each = (p.chunks + kThreads - 1) / kThreads, c0 = min(tid * each, p.chunks), c1 = min(c0 + each, p.chunks);
   float top = -INFINITY;

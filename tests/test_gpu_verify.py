@@ -164,6 +164,48 @@ def test_probabilities_that_are_none(cuda_device):
     assert torch.equal(out, run(dict(m, probs=probs))[1])
 
 
+@pytest.mark.parametrize("q", [0.0, -1.0, -math.inf, math.nan])
+def test_a_draft_whose_probability_is_none(cuda_device, q):
+    """It counts as 0: the draft is taken where the target gives it anything, and not where it is masked."""
+    m = make([2] * 4, 900, torch.float32, seed=11)
+    m["u"][:] = 0.5
+    for b in range(4):
+        r = m["q_start"][b]
+        m["probs"][r, int(m["tokens"][r + 1])] = q
+        if b == 1:
+            m["wide"][r, int(m["tokens"][r + 1])] = -math.inf
+    got = run(m)
+    assert got[0].tolist() == [2, 1, 2, 2]
+    check(dict(m, probs=torch.where(m["probs"] > 0, m["probs"], 0.0)), got)
+
+
+@pytest.mark.parametrize("max_q", [1, 4096])
+def test_a_call_behind_one_whose_sequences_are_all_left_out(cuda_device, max_q):
+    """The second call's pairs are its own, though the first draws from none of the many rows it reads."""
+    big = torch.zeros(4096, 50000, dtype=torch.bfloat16, device="cuda")
+    n, b = big.shape[0], 2 if max_q > 1 else 4096
+    z = lambda k, dt: torch.zeros(k, dtype=dt, device="cuda")  # noqa: E731
+    i32, i64, f32 = torch.int32, torch.int64, torch.float32
+    starts = z(b + 1, i32)
+    starts[0], starts[1:] = -1, n                      # below 0 for the first, none for the others
+    desc = ls.verify_desc(big, b, max_q)
+    m = make([2] * 8 if max_q > 1 else [1] * 8, 8191, torch.float32, probs=False, seed=12)
+    small = m["wide"].cuda()
+    sdesc = ls.verify_desc(small, 8, max(m["counts"]))
+    ws = z(max(ls.ls_draft_verify_workspace_size(desc), ls.ls_draft_verify_workspace_size(sdesc)), torch.uint8)
+    k = small.shape[0]
+    count, out, lp = z(8, i32), z(k, i64), z(k, f32)
+    args = m["tokens"].cuda(), torch.tensor(m["q_start"], dtype=i32, device="cuda"), m["u"].cuda(), m["u_next"].cuda()
+    first = z(n, i64), starts, z(n, f32), z(b, f32), z(b, i32), z(n, i64), z(n, f32)
+    for _ in range(3):
+        ls.ls_draft_verify(desc, big, *first, ws)
+        ls.ls_draft_verify(sdesc, small, *args, count, out, lp, ws)
+        got = count.cpu(), out.cpu(), lp.cpu(), m["kv_len"] - torch.tensor(m["counts"]) + count.cpu()
+        check(m, got)
+    with pytest.raises(ls.LsError):
+        ls.ls_read_device_status(ws)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_masked_tokens(cuda_device, dtype):
     m = make([3, 3, 2, 1], 777, dtype, seed=11)
