@@ -432,7 +432,7 @@ constexpr int kCopyThreads = 256, kPiece = 16384;  // bytes of a block
 // pages of 1500 entries.  Pieces of 16 KB, dealt out in turn: piece x % pieces of side x / pieces (K's heads,
 // then V's) of an entry's page.  All of a block's piece is loaded before its first
 // store, eight blocks an SM.
-__global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const ls_kv_cache c, const int32_t* __restrict__ copies, int row_bytes,
+__global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const ls_kv_cache c, const int32_t* copies, int row_bytes,
                                                                  int pieces, int64_t n, uint32_t* status) {
   start();
   const int each = pieces * 2 * c.hkv;
