@@ -641,7 +641,8 @@ LS_API ls_status ls_draft_verify_workspace_size(const ls_verify_desc* desc, size
  * float32 [total_q] or NULL; kv_len and keep int64 [batch], or keep NULL.  max_q is an
  * upper bound of a sequence's rows (max_q <= total_q <= batch * max_q); a sequence with
  * more, or with rows outside [0, total_q), is left out (n_emitted 0, its rows of emitted
- * and logp as they were, keep its kv_len) and reported. */
+ * and logp as they were, keep its kv_len) and reported.  emitted must not overlap tokens,
+ * nor logp u; keep may be kv_len. */
 LS_API ls_status ls_draft_verify(const ls_verify_desc* desc, const void* logits,
                                  const float* draft_probs, const int64_t* tokens,
                                  const int32_t* q_start, const float* u, const float* u_next,
@@ -665,7 +666,8 @@ LS_API ls_status ls_draft_verify(const ls_verify_desc* desc, const void* logits,
  *   key_heads divides heads: value head h takes q and k of head
  *     h / (heads / key_heads).  q, k [total_q][key_heads][dk], v [total_q][heads][dv],
  *     token strides in elements, multiples of 8 (rows of one projection as they
- *     lie); g, beta [total_q][heads] and o [total_q][heads][dv] contiguous.
+ *     lie); g, beta [total_q][heads] and o [total_q][heads][dv] contiguous, o apart
+ *     from q, k and v.
  *   states [n_states][heads][dv][dk].  dk = dv = 128.
  *   max_q: upper bound of a sequence's tokens (max_q <= total_q <= batch * max_q). */
 typedef struct {

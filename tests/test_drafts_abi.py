@@ -100,7 +100,7 @@ def test_verify_calls(ls):
     names = ("logits", "probs", "tokens", "q_start", "u", "u_next", "kv_len", "count", "out", "logp", "keep")
 
     def call(desc=None, ws=A, nb=need, **kw):
-        d = dict.fromkeys(names, A) | kw
+        d = {n: A + (i << 40) for i, n in enumerate(names)} | kw  # apart
         return L.ls_draft_verify(ctypes.byref(desc or verify(ls)), *(d[n] for n in names), ws, nb, None)
 
     assert call(verify(ls, batch=0, total_q=0, max_q=0), ws=None, **dict.fromkeys(names)) == 0
@@ -108,6 +108,11 @@ def test_verify_calls(ls):
         assert call(**{name: None}) == 1, name
     for name, off in (("logits", 1), ("probs", 2), ("tokens", 4), ("q_start", 2), ("u", 1), ("keep", 4), ("out", 4)):
         assert call(**{name: A + off}) == 1, name
+    for name, other in (("out", "tokens"), ("logp", "u")):   # n tokens of 8 and of 4 bytes from either side
+        each = 8 if name == "out" else 4
+        for off in (0, 4 * each, -4 * each):
+            assert call(**{name: 2 * A + off, other: 2 * A}) == 1, name
+            assert b"overlap" in L.ls_last_error()
     assert call(verify(ls, draft_stride=99)) == 1 and call(nb=need - 1) == 3 and call(ws=None) == 1 and call(ws=A + 16) == 1
 
 
@@ -125,7 +130,7 @@ def test_decode_calls(ls):
     names = ("states", "q", "k", "v", "g", "beta", "q_start", "n_use", "state_in", "state_out", "o")
 
     def call(desc=None, ws=None, nb=0, **kw):
-        d = dict.fromkeys(names, A) | kw
+        d = {n: A + (i << 40) for i, n in enumerate(names)} | kw  # apart
         return L.ls_gdn_decode(ctypes.byref(desc or decode(ls)), *(d[n] for n in names), ws, nb, None)
 
     assert call(decode(ls, batch=0, total_q=0, max_q=0), **dict.fromkeys(names)) == 0
@@ -134,6 +139,10 @@ def test_decode_calls(ls):
         assert call(**{name: None}) == 1, name
     for name, off in (("states", 8), ("q", 8), ("o", 2), ("g", 2), ("state_out", 2), ("n_use", 1)):
         assert call(**{name: A + off}) == 1, name
+    for name in ("q", "k", "v"):
+        for off in (0, 1024, -1024):
+            assert call(o=2 * A + off, **{name: 2 * A}) == 1, name
+            assert b"overlap" in L.ls_last_error()
     assert call(ws=A, nb=255) == 3 and call(ws=A + 8, nb=256) == 1
 
 
