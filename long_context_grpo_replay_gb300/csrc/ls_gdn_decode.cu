@@ -5,20 +5,22 @@
 // A token does 7 operations an element of a state that has to come from memory
 // and go back, so for a token or two the states' bytes bound it.  A row of S needs k,
 // q and its own element of v alone: the unit of work is half a head, 64 rows or 32 KB,
-// for all of a sequence's tokens.  Three blocks an SM take such units in turn; a
-// producer warp brings the coming ones into a ring of two stages by bulk copies
+// for all of a sequence's tokens, and a block of the launch.  Three blocks an SM begin;
+// a block that is through with its unit takes that of one that has not begun (they
+// differ by their tokens; dealt out in turn the last SMs end a fifth later).  A
+// producer warp brings the coming units into a ring of two stages by bulk copies
 // (state, and the tokens' k, q and v as they lie; the gates by 4-byte copies), so that
 // some 190 KB an SM are on their way whatever the others do.  Four warps hold the rows
 // in registers, eight lanes four rows with sixteen columns each, on packed pairs of
 // floats; the four row sums are four shuffles.  The results leave by plain stores in
 // whole lines.
-//   Measured: 96 sequences x 32 heads, one token, 405 MB in 69.5 us (5.8 TB/s, 86 % of
-// a copy's rate; 64 KB a block without the ring 92 us).  From four tokens on the
-// arithmetic counts, 7 us a token for 64 x 32 heads: 1 to 6 drafted tokens of 64
-// sequences 43 us, where the states' bytes would take 22; 16 tokens 130 us.  Two rows
-// to eight lanes in twice the warps take 144 us for those, four rows to sixteen lanes
-// 180; a token's operands loaded, and its sums taken, beside the one before it are no
-// faster.
+//   Measured: 96 sequences x 32 heads, one token, 405 MB in 63.7 us (6.4 TB/s, 94 % of
+// a copy's rate; with units dealt out 69.5, without the ring 92).  From four tokens on the
+// arithmetic counts, 6 to 7 us a token for 64 x 32 heads: 1 to 6 drafted tokens of 64
+// sequences 39.0 us (dealt out 43), where the states' bytes would take 22; 16 tokens 128
+// us.  Units dealt out, two rows to eight lanes in twice the warps took 144 us for
+// those, four rows to sixteen lanes 180; a token's operands loaded, and its sums taken,
+// beside the one before it were no faster.
 #include <atomic>
 
 #include "ls_internal.h"
@@ -48,7 +50,8 @@ struct Stage {
 template <typename T>
 struct Shared {
   Stage<T> stage[kStages];
-  alignas(8) uint64_t full[kStages], empty[kStages];
+  alignas(16) uint4 answer;              // which unit comes next
+  alignas(8) uint64_t full[kStages], empty[kStages], answered;
   uint32_t abort;
 };
 
@@ -116,6 +119,29 @@ __device__ __forceinline__ void arrive_fetched(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// A block that has units left to start takes the place of one that has not begun, by
+// asking the launch for it: the answer is that block's number, or that there is none.
+__device__ __forceinline__ void ask(void* answer, uint32_t bar) {
+  tc::mbar_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   tc::smem_u32(answer)),
+               "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ int asked(const uint4* answer) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(answer);
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t"
+      "mov.b128 a, {%1, %2};\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, a;\n\t}"
+      : "=r"(x)
+      : "l"(a.x), "l"(a.y));
+  return x;
+}
+
 // A sequence's place in the call, as loaded.
 struct Place {
   int32_t first, end, use, in, out;
@@ -129,13 +155,12 @@ __device__ __forceinline__ Place place_of(const GdnDecodeParams& p, int b) {
 }
 
 // The producer asks for everything and waits for nothing but room: no load's value is
-// used here but a unit's place, which is loaded one unit ahead.
+// used here but a unit's number and place, two units before the one that is worked on.
 template <typename T>
 __device__ __forceinline__ void produce(const GdnDecodeParams& p, Shared<T>& sh) {
   constexpr int K = Stage<T>::kTokens;
   const int lane = threadIdx.x & 31;
-  const int64_t units = (int64_t)p.d.batch * p.d.heads * 2;
-  int it = 0;
+  int it = 0, turn = 0;
   // The next stage, once the warps that compute have left it.
   auto take = [&]() -> Stage<T>* {
     const int s = it % kStages;
@@ -146,22 +171,22 @@ __device__ __forceinline__ void produce(const GdnDecodeParams& p, Shared<T>& sh)
     return &sh.stage[s];
   };
   const uint32_t per_seq = 2u * p.d.heads;
-  Place next = place_of(p, (int)(blockIdx.x / per_seq));
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+  const uint32_t answered = tc::smem_u32(&sh.answered);
+  if (lane == 0) ask(&sh.answer, answered);
+  for (int unit = (int)blockIdx.x; unit >= 0; ++turn) {
     const uint32_t b = (uint32_t)unit / per_seq, in_seq = (uint32_t)unit - b * per_seq;
     const int half = (int)(in_seq & 1), h = (int)(in_seq >> 1);
-    const Place at = next;
-    if (unit + gridDim.x < units) next = place_of(p, (int)((uint32_t)(unit + gridDim.x) / per_seq));
+    const Place at = place_of(p, (int)b);
     const int64_t first = at.first, n_all = (int64_t)at.end - first, n = p.n_use ? at.use : n_all, in = at.in;
     int64_t out = at.out;
     const bool bad = first < 0 || n_all < 0 || first + n_all > p.d.total_q || n_all > p.d.max_q || n < 0 || n > n_all || in < -1 ||
                      in >= p.d.n_states;
     if ((bad || out >= p.d.n_states) && in_seq == 0 && lane == 0 && p.status) atomicOr(p.status, kStatusBadIndex);
     if (out >= p.d.n_states) out = -1;
-    if (bad || ((n == 0 || !p.o) && (out < 0 || (n == 0 && out == in)))) continue;
+    const bool idle = bad || ((n == 0 || !p.o) && (out < 0 || (n == 0 && out == in)));
     const int64_t rows = ((int64_t)h * kD + half * kRows) * kD, state = (int64_t)p.d.heads * kD * kD;
     const int kh = h / (p.d.heads / p.d.key_heads);
-    for (int64_t t0 = 0; t0 == 0 || t0 < n; t0 += K, ++it) {
+    for (int64_t t0 = 0; !idle && (t0 == 0 || t0 < n); t0 += K, ++it) {
       Stage<T>* st = take();
       if (!st) return;
       const uint32_t full = tc::smem_u32(&sh.full[it % kStages]);
@@ -186,6 +211,16 @@ __device__ __forceinline__ void produce(const GdnDecodeParams& p, Shared<T>& sh)
       }
       arrive_fetched(full);
     }
+    if (!__all_sync(0xffffffffu, tc::mbar_wait(answered, turn & 1, &sh.abort))) {
+      if (lane == 0) sh.abort = 1;
+      return;
+    }
+    unit = asked(&sh.answer);
+    __syncwarp();
+    if (lane == 0 && unit >= 0) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read before it is written again
+      ask(&sh.answer, answered);
+    }
   }
   Stage<T>* st = take();
   if (!st) return;
@@ -206,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) gdn_decode_kernel(const Gdn
       tc::mbar_init(tc::smem_u32(&sh.full[s]), 33);  // each lane, and the first's word of what it asked for
       tc::mbar_init(tc::smem_u32(&sh.empty[s]), kWarps);
     }
+    tc::mbar_init(tc::smem_u32(&sh.answered), 1);
     sh.abort = 0;
     tc::fence_mbar_init();
   }
@@ -214,8 +250,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) gdn_decode_kernel(const Gdn
     produce<T>(p, sh);
     if (*(volatile uint32_t*)&sh.abort) {  // a wait gave up: what is on its way lands before the block ends
       asm volatile("cp.async.wait_all;" ::: "memory");
-      if (lane < kStages) {
-        const uint32_t bar = tc::smem_u32(&sh.full[lane]);
+      if (lane <= kStages) {
+        const uint32_t bar = tc::smem_u32(lane < kStages ? &sh.full[lane] : &sh.answered);
         tc::mbar_wait_short(bar, 0), tc::mbar_wait_short(bar, 1);
       }
       if (lane == 0 && p.status) {
@@ -293,9 +329,9 @@ cudaError_t launch(const GdnDecodeParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     allowed.fetch_or(bit, std::memory_order_relaxed);
   }
-  const int64_t units = (int64_t)p.d.batch * p.d.heads * 2, most = kBlocks * device_sms();
+  const int64_t units = (int64_t)p.d.batch * p.d.heads * 2;
   if (units > INT32_MAX) return cudaErrorInvalidConfiguration;
-  gdn_decode_kernel<T><<<(unsigned)(units < most ? units : most), kThreads, sizeof(Shared<T>), s>>>(p);
+  gdn_decode_kernel<T><<<(unsigned)units, kThreads, sizeof(Shared<T>), s>>>(p);
   return cudaGetLastError();
 }
 
