@@ -12,11 +12,11 @@
 // the warps' counts gives each free page its rank, and the rank its taker, so the
 // result does not depend on which thread came first.  The kernels let the one after
 // them start early, which waits for their end before it reads anything.
-//   Measured, one call after another: a step of 8 sequences 5.4 us in a graph (6.3 as
-// calls), of 384 over 131,000 pages 13.3 us; 16 members forked from 100,003 tokens, their
-// first slots and the copies of their last page 14.5 us in a graph; 3001 pages compacted
-// in 11 us before the copies.  One block alone takes 8 us where eight take 10 for the
-// first of these, but 97 for the second.
+//   Measured, one call after another in a graph: a step of 8 sequences 4.3 us (6.2 as
+// calls), of 384 over 131,000 pages 9.8; 16 members forked from 100,003 tokens, their
+// first slots and the copies of their last page 13.0 us; 3001 pages compacted in 11 us
+// before the copies.  One block alone is faster for few (8 of 10 us for the first of
+// these when it was tried) and takes 97 us for the second.
 #include "ls_cluster.cuh"
 #include "ls_internal.h"
 

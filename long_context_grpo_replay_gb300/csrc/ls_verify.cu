@@ -27,7 +27,7 @@
 // within 2^-20 of it, each partial sum is put right afterwards by (Z - Z0) times the
 // sum of its q where e > q Z0 (tokens within 2^-20 of that border weigh 2^-20 of
 // theirs, so that their side does not matter).
-//   Measured: 64 sequences of up to 5 rows x 128,000 (54 MB) 28.9 us: the rows' pass 8
+//   Measured: 64 sequences of up to 5 rows x 128,000 (54 MB) 29.5 us: the rows' pass 8
 // (4.3 TB/s with cold caches), the draw 20, of which half is the weights' arithmetic
 // (34 instructions an element, three issued a cycle on the SMs that hold four blocks)
 // and half the chain of a block's loads, barriers and scans.  Packed pairs with a copy
