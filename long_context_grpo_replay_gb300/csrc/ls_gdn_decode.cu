@@ -7,7 +7,7 @@
 // q and its own element of v alone: the unit of work is half a head, 64 rows or 32 KB,
 // for all of a sequence's tokens, and a block of the launch.  Three blocks an SM begin;
 // a block that is through with its unit takes that of one that has not begun (they
-// differ by their tokens; dealt out in turn the last SMs end a fifth later).  A
+// differ by their tokens; dealt out in turn the last SMs end a tenth later).  A
 // producer warp brings the coming units into a ring of two stages by bulk copies
 // (state, and the tokens' k, q and v as they lie; the gates by 4-byte copies), so that
 // some 190 KB an SM are on their way whatever the others do.  Four warps hold the rows

@@ -153,6 +153,41 @@ def test_step_by_step_is_one_call(cuda_device):
     assert torch.equal(cur[:2], states[:2])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_sequences_are_those_of_a_few(cuda_device, dtype):
+    """Far more units of work than the device holds at once, of all lengths, some of them none, two such calls
+    side by side: each sequence's bits are those it has in a call of ten."""
+    b, heads = 90, 16
+    g = torch.Generator().manual_seed(21)
+    counts = torch.randint(0, 8, (b,), generator=g).tolist()
+    m = make(counts, heads, 8, dtype, n_states=2 * b, seed=22)
+    d = on_gpu(m)
+    n = sum(counts)
+    ins, outs = torch.arange(b, dtype=torch.int32), torch.arange(b, 2 * b, dtype=torch.int32)
+    ins[5], outs[7:9], ins[11] = -1, -1, 10000        # from zeros, not kept, left out
+    args, ins, outs = (d["q"], d["k"], d["v"], d["g"], d["beta"]), ins.cuda(), outs.cuda()
+
+    def call(first, end, states, o, stream=None):
+        at = d["q_start"][first:end + 1]
+        desc = ls.gdn_decode_desc(d["q"], d["k"], d["v"], states, end - first, 7 if end - first == b else n)
+        ls.ls_gdn_decode(desc, states, *args, at, ins[first:end], outs[first:end], o, stream=stream)
+
+    def fresh():
+        return d["states"].clone(), torch.full(m["v"].shape, 7.0, dtype=dtype, device="cuda")
+
+    few, many, other = fresh(), fresh(), fresh()
+    for first in range(0, b, 10):
+        call(first, first + 10, *few)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for s, (states, o) in zip(streams, (many, other)):
+        for _ in range(3):
+            call(0, b, states, o, stream=s)
+    torch.cuda.synchronize()
+    for states, o in (many, other):
+        assert torch.equal(o, few[1]) and torch.equal(states, few[0])
+
+
 def test_agrees_with_the_replay(cuda_device):
     """A response replayed from the captured state is the same tokens stepped from it."""
     m = make([20], 3, 3, torch.float32, seed=8)
