@@ -612,7 +612,8 @@ LS_API ls_status ls_cache_copy_pages(const ls_kv_cache* cache, const int32_t* co
  * n_use, n_emitted makes ls_gdn_decode keep).  A sequence without rows has none:
  * n_emitted 0, keep its kv_len.  Rows that judge no draft may hold anything in
  * draft_probs and u; elsewhere what is not above 0 in draft_probs counts as 0.
- *   logits may be -infinity or the type's lowest value (a masked token).  A row
+ *   logits may be -infinity or the type's lowest value (a masked token); a draft's
+ *     probability below 2^-149 of the row's largest is 0.  A row
  *     that has no distribution (all -infinity, or a NaN or +infinity in it) accepts
  *     nothing; where it had to give the next token, emitted is -1 there, n_emitted
  *     counts the drafts before it, keep their keys and the last token's, and the

@@ -491,8 +491,9 @@ __global__ void __launch_bounds__(kThreads, 4) verify_draw_kernel(const VerifyPa
       const Draft t = i0 ? draft_of(i) : draft0;
       if (i + 1 < n) {
         if (t.x >= 0 && t.x < V) {
-          const float d = t.z - a.x;
-          pass = t.u * t.q * a.y < exp2f(fmaf(d, p.c, d * p.c_low));
+          const float d = t.z - a.x, x = d * p.c;
+          // below 2^-149 it is 0, whatever d * c_low is: that may overflow where c_low is negative
+          pass = t.u * t.q * a.y < (x < -160.f ? 0.f : exp2f(fmaf(d, p.c, d * p.c_low)));
           if (pass && rank == 0 && lane == 0) {
             p.emitted[r] = t.x;
             if (p.logp) p.logp[r] = d * p.d.logit_scale - logf(a.y);
