@@ -530,7 +530,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_draw_kernel(const VerifyPa
   const Row w = make_row(row.x, row.y, p.c, p.c_low);
   const T* z = logits + r * p.d.logits_stride;
   const float* q = p.probs && rejected ? p.probs + r * p.d.draft_stride : nullptr;
-  const int64_t draft = rejected && !p.probs ? p.tokens[r + 1] : -1;
+  const int64_t next = rejected && !p.probs ? p.tokens[r + 1] : -1;
+  const int draft = next >= 0 && next < V ? (int)next : -1;  // an id outside takes nothing out of the row
   // each warp its segment of the row; segments begin where 16-byte pieces do, `shift` elements before the row
   const int shift = (int)(reinterpret_cast<uintptr_t>(z) & 15) / (int)sizeof(T);
   const Source<T> src{z, q, V, (reinterpret_cast<uintptr_t>(q - shift) & 15) == 0};
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_draw_kernel(const VerifyPa
     Sums s{};
     if (lo < V) s = q ? segment<true>(src, (int)lo, stop, w, table) : segment<false>(src, (int)lo, stop, w, table);
     s.e = warp_sum(s.e), s.w = warp_sum(s.w), s.q = warp_sum(s.q);
-    if (draft >= 0 && draft >= lo && draft < lo + each && draft < V) {
+    if (draft >= 0 && draft >= lo && draft < lo + each) {
       float a, b;
       weight(value(z[draft]), w, table, a, b);
       const uint64_t x = (uint64_t)fixed(a, b);
@@ -591,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_draw_kernel(const VerifyPa
     const int stop = (int)(from + each < V ? from + each : V);
     const float z_hi = (float)z_all * 0x1p-61f, z_lo = (float)((int64_t)z_all - fixed(z_hi)) * 0x1p-61f;
     float its = 0.f;
-    const int found = look(src, w, table, from, stop, target, q && !use_p, z_hi, z_lo, use_p ? -1 : (int)draft, scan, passes, its);
+    const int found = look(src, w, table, from, stop, target, q && !use_p, z_hi, z_lo, use_p ? -1 : draft, scan, passes, its);
     if (found >= 0) {
       p.emitted[r] = found;
       if (p.logp) p.logp[r] = (its - row.x) * p.d.logit_scale - logf(row.y);

@@ -38,3 +38,24 @@ def test_masked_drafts_at_any_scale(cuda_device, dtype, probs, scale):
             edge = float(m["u_next"][b]) * float(upto[-1])
             if float((upto - edge).abs().min() / upto[-1]) > 2.0 ** -20:   # the excess is 2^-9.6 of the row, good to 2^-30 of it
                 assert int(got[1][2 * b]) == int((upto <= edge).sum())
+
+
+@pytest.mark.parametrize("probs", [True, False])
+@pytest.mark.parametrize("by", [2 ** 32, -2 ** 32, 2 ** 40, -2 ** 40, 2 ** 63 - 512, -2 ** 63])
+def test_drafts_whose_lower_half_is_a_token(cuda_device, probs, by):
+    """An id outside the vocabulary is rejected as it is, and the next token comes from p: the token that its lower 32
+    bits name is drawn like any other."""
+    m = make([2] * 4, 512, torch.float32, probs, seed=33)
+    m["u"][:] = 0.0
+    for b, t in enumerate((0, 3, 300, 511)):
+        r = m["q_start"][b]
+        m["wide"][r, t] = m["wide"][r].max() + 3       # most of the row
+        if probs:
+            m["probs"][r, t] = 0.0
+        m["u_next"][b] = float(torch.softmax(m["wide"][r].double(), 0)[:t].sum()) + 0.1
+        m["tokens"][r + 1] = t + by
+    got = run(m, status=5)
+    check(m, got)
+    assert got[0].tolist() == [1] * 4
+    if not probs:
+        assert got[1][::2].tolist() == [0, 3, 300, 511]
