@@ -372,8 +372,18 @@ __device__ __forceinline__ int look(const Source<T>& src, const Row& w, const fl
                                     bool over_q, float z_hi, float z_lo, int but, uint64_t* scan, int* most_of, float& its) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int found = -1, last = -1;  // the last token so far that weighs anything
-  for (int64_t lo = from; lo < stop && found == -1; lo += kThreads * 8) {
-    const int v = (int)lo + tid * 8;
+  for (int lo = (int)from, turn = 0; found == -1; lo += kThreads * 8) {
+    if (lo >= stop) {
+      // The sum that t was taken from may be past the tiles' own by rounding: their last token then.  And rounding may
+      // have left a sum where no token is to be drawn (the rejected draft's part, tokens that weigh less than a unit):
+      // the next one behind comes out, or else the row's last, by p alone (a remainder's last segments hold nothing else).
+      if (last >= 0 || turn == 2) break;
+      if (turn == 0 && stop < src.end)
+        turn = 1, lo = stop, stop = src.end, t = 0;
+      else
+        turn = 2, lo = (int)-(-from & 7), stop = src.end, t = ~0ull, over_q = false;  // from where a piece begins
+    }
+    const int v = lo + tid * 8;
     uint64_t x[8], sum = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = 0;
@@ -427,8 +437,7 @@ __device__ __forceinline__ int look(const Source<T>& src, const Row& w, const fl
     }
     __syncthreads();
   }
-  // The sum that t was taken from may be past the tiles' own by rounding: their last token then.
-  if (found == -1 && tid == 0) found = last >= 0 ? last : max((int)from, 0), its = value(src.z[found]);
+  if (found == -1 && last >= 0 && tid == 0) found = last, its = value(src.z[last]);
   return found;
 }
 

@@ -59,3 +59,48 @@ def test_drafts_whose_lower_half_is_a_token(cuda_device, probs, by):
     assert got[0].tolist() == [1] * 4
     if not probs:
         assert got[1][::2].tolist() == [0, 3, 300, 511]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("masked", ["inf", "low"])
+def test_a_segment_that_holds_the_rejected_draft_alone(cuda_device, dtype, masked):
+    """Around the rejected draft all tokens are masked: nothing can be drawn there, whatever its weight leaves of the sums
+    it was in.  The first or the last token that is left comes out."""
+    n = 64
+    m = make([2] * n, 8191, dtype, False, seed=35)
+    low = -math.inf if masked == "inf" else LOW[dtype]
+    m["u"][:] = 1.0 - 2.0 ** -24
+    for b in range(n):
+        r = m["q_start"][b]
+        first = b % 4 < 2
+        d = 7 + b if first else 8180 - b               # before all others, or behind them
+        m["wide"][r] = low
+        m["wide"][r, d] = -7.0 - 0.13 * b               # 2^-12 to 2^-23 of the others: its lower part is rounded with the rest of the sum
+        m["wide"][r, 4000:4011] = torch.linspace(0, 1, 11).to(dtype)
+        m["tokens"][r + 1] = d
+        m["u_next"][b] = 0.0 if first else 1.0 - 2.0 ** -24
+    got = run(m)
+    assert got[0].tolist() == [1] * n
+    assert got[1][::2].tolist() == [4000 if b % 4 < 2 else 4010 for b in range(n)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("drafts", [0, 1])
+def test_tokens_too_small_to_be_drawn(cuda_device, dtype, drafts):
+    """Tokens below 2^-61 of the row (2^-60 where its sum is a power of two) count as none one by one, whatever they are together: the first token that is drawn
+    is the first of the others, never a masked one."""
+    n = 6
+    m = make([1 + drafts] * n, 5000, dtype, False, seed=37)
+    m["u"][:] = 0.0                                    # the draft passes
+    m["u_next"][:] = 0.0
+    for b in range(n):
+        r = m["q_start"][b] + drafts
+        m["wide"][r] = -math.inf
+        m["wide"][r, 10 + b:1024] = -42.5              # 2^-61.3 each, 2^-51.3 together
+        m["wide"][r, 3000 + b] = 0.0
+        m["wide"][r, 4000] = -42.5
+    count, out, _, _ = run(m)
+    assert count.tolist() == [1 + drafts] * n
+    assert out[drafts::1 + drafts].tolist() == [3000 + b for b in range(n)]
+    m["u_next"][:] = 1.0 - 2.0 ** -24
+    assert run(m)[1][drafts::1 + drafts].tolist() == [3000 + b for b in range(n)]
