@@ -604,7 +604,7 @@ LS_API ls_status ls_cache_copy_pages(const ls_kv_cache* cache, const int32_t* co
  * at the draft), the drafts are accepted while u[r] * q_r(x) < p_r(x).  At the row
  * where that ends the next token is the least v with
  *   sum_{j <= v} w_j > u_next[b] * sum_j w_j,
- * w = max(p - q, 0) after a rejection (p where that is 0 everywhere) and p after the
+ * w = max(p - q, 0) after a rejection (p where its sum is at most 2^-30) and p after the
  * last draft.  So a sequence of n rows has 1 to n tokens come out: emitted[r] =
  * accepted drafts, then the new token, then -1s; logp[r] = log p_r(emitted[r]), 0
  * where there is none; n_emitted[b] their number; keep[b] = kv_len[b] - n +

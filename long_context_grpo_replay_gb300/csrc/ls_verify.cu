@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_draw_kernel(const VerifyPa
       const int64_t right = q ? (int64_t)x[i] - fixed(off * sq[i]) : (int64_t)x[i];
       x[i] = right > 0 ? (uint64_t)right : 0;
     }
-    const bool none = warp_sum(x[0] + x[1]) < (1ull << 31);  // of 2^61: rounding alone
+    const bool none = warp_sum(x[0] + x[1]) <= all >> 30;  // 2^-30 of the row: it may be rounding alone
     if (none) x[0] = e[0], x[1] = e[1];
     const uint64_t upto = warp_prefix(x[0] + x[1]), total = __shfl_sync(0xffffffffu, upto, 31);
     const uint64_t t = part_of(p.u_next[b], total), before = upto - x[0] - x[1];

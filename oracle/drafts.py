@@ -98,7 +98,8 @@ class Book:
 def verify(logits, probs, tokens, q_start, u, u_next, scale):
     """Per sequence (emitted tokens, their log-probabilities, how near the nearest decision was to its border:
     of an acceptance relative to p, of the draw relative to all weights).  logits, probs in any type on any
-    device; a sequence whose row has no distribution ends with the token None."""
+    device; a sequence whose row has no distribution ends with the token None.  What a rejection leaves is taken for
+    nothing, and the draw is from p, where it sums to 2^-30 or less."""
     out = []
     for b in range(len(q_start) - 1):
         toks, logp, near = [], [], float("inf")

@@ -104,3 +104,30 @@ def test_tokens_too_small_to_be_drawn(cuda_device, dtype, drafts):
     assert out[drafts::1 + drafts].tolist() == [3000 + b for b in range(n)]
     m["u_next"][:] = 1.0 - 2.0 ** -24
     assert run(m)[1][drafts::1 + drafts].tolist() == [3000 + b for b in range(n)]
+
+
+def test_what_a_rejection_leaves_at_its_threshold(cuda_device):
+    """max(p - q, 0) is taken for 0 everywhere where its sum is at most 2^-30 of p's, whatever p's sum is: just above the
+    next token is the one that it has, just below it comes from p.  (The excess is good to float32's q of 2^-28, 2^-53.)"""
+    n, v, j = 24, 1000, 417
+    m = make([2] * n, v, torch.float32, True, seed=41)
+    m["u"][:] = 0.9
+    m["u_next"][:] = 0.5
+    sums = []
+    for b in range(n):
+        r = m["q_start"][b]
+        m["wide"][r, j] = -math.inf
+        z = m["wide"][r].double()
+        m["wide"][r, j] = float(torch.logsumexp(z, 0)) - 28 * math.log(2.0)
+        z = m["wide"][r].double()
+        sums.append(float(torch.exp(z - z.max()).sum()))
+        p = torch.softmax(z, 0)
+        m["probs"][r] = (1.5 * p).float()
+        m["probs"][r, j] = (p[j] - (1.25 if b % 2 else 0.75) * 2.0 ** -30).float()
+        m["tokens"][r + 1] = int(p.argmax())
+    assert min(math.frexp(s)[0] for s in sums) < 0.6 and max(math.frexp(s)[0] for s in sums) > 0.9
+    got = run(m)
+    assert got[0].tolist() == [1] * n
+    assert got[1][2::4].tolist() == [j] * (n // 2)
+    assert j not in got[1][::4].tolist()
+    check(m, got)
