@@ -618,9 +618,13 @@ LS_API ls_status ls_cache_copy_pages(const ls_kv_cache* cache, const int32_t* co
  *     nothing; where it had to give the next token, emitted is -1 there, n_emitted
  *     counts the drafts before it, keep their keys and the last token's, and the
  *     status word says so.  A draft outside [0, vocab) is rejected and reported.
- *   The weights of the draw are good to 2^-31 each and their sums exact,
- *     so that the token is the definition's also in a vocabulary of 10^5; an
- *     acceptance within about 2^-20 of its border may fall either way.
+ *   An acceptance within 2^-16 of its border (relative; twice that for each
+ *     doubling of vocab beyond 2^17; about 2^-20 in practice) may fall either way.
+ *     The weights of the draw are good to 2^-30 each (those below 2^-23 of the row to
+ *     2^-47 of it) and their sums to about 2^-31 of the row, so that in a vocabulary
+ *     of 10^5 one draw in some thousands gives a neighbour of the definition's token.
+ *     A token below 2^-60 of the row is never drawn.
+ *   vocab: at most 2^24.
  *   dtype: of logits; draft_probs is float32.  Strides in elements, any.
  *   logit_scale: 2^-100 to 2^100. */
 typedef struct {

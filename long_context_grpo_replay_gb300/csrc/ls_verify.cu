@@ -12,21 +12,25 @@
 // The draw compares u with a running sum that has a step for every token, 10^5
 // of them in [0, 1): with sums good to 2^-24 one draw in a hundred would give a
 // neighbour of the definition's token.  So the draw's weights are formed anew, to
-// 2^-31 of each or better, and summed without loss:
+// 2^-30 of each (2^-33 rms), and summed as exactly:
 //   e = 2^(s log2(e) (z - max)) = 2^(k/256) (1 + d),  d = 2^f - 1,  |f| <= 2^-8,
 // k/256 being z's product rounded to that grid less the maximum's (both exact),
 // f what is left of both, formed by fused multiply-adds; 2^(j/256) comes from a
 // table of pairs (Tang's method: P. T. P. Tang, Table-driven implementation of the
 // exponential function, ACM TOMS 15, 1989) and d from three terms (the fourth is
 // below 2^-38).  A weight, scaled so that all of them sum to less than 1, is split
-// at 2^-22: sums of the upper parts are exact in float32, those of the lower ones,
-// 2^-8.5 of the weights at most, good to 2^-32 of theirs.  Beyond a thread they are
-// integers in units of 2^-61, whose sums do not depend on their order.
+// at 2^-22: sums of the upper parts are exact in float32.  A lower part is 2^-8.5 of
+// its weight at most, and 2^-23: below that a weight is all lower part, good to
+// 2^-24 of itself, 2^-47 of the row.  A thread adds up to 256 of them in float32, in
+// longer segments 64 at a time; beyond that they are integers in units of 2^-61, whose
+// sums do not depend on their order.  Roundings that fall as they may leave about
+// 2^-31 of the row; at worst, where all of a thread's parts are alike, 2^-17.6 of what
+// the lower parts sum to (2^-20.6 in longer segments).
 //   After a rejection w = max(e - q Z, 0) needs Z, the sum of all e, before the
 // first of them is known: the pass takes the row's float32 sum Z0, and as Z is
-// within 2^-20 of it, each partial sum is put right afterwards by (Z - Z0) times the
-// sum of its q where e > q Z0 (tokens within 2^-20 of that border weigh 2^-20 of
-// theirs, so that their side does not matter).
+// within about 2^-20 of it (2^-17 at most up to 2^17 tokens), each partial sum is put
+// right afterwards by (Z - Z0) times the sum of its q where e > q Z0 (tokens as near
+// that border weigh 2^-20 of theirs, so that their side does not matter).
 //   Measured: 64 sequences of up to 5 rows x 128,000 (54 MB) 29.5 us: the rows' pass 8
 // (4.3 TB/s with cold caches), the draw 20, of which half is the weights' arithmetic
 // (34 instructions an element, three issued a cycle on the SMs that hold four blocks)
@@ -47,6 +51,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kEach = 4, kVectors = 32 * kEach, kChunkBytes = 16 * kVectors;  // a warp's in the pass over the rows
 constexpr int kMaxCluster = 8;
 constexpr int kTile = 256;  // elements a warp takes at a time in the draw, eight a lane
+constexpr int kShort = 32, kChain = 8;  // tiles whose lower parts a lane sums in float32: of a whole segment, of a longer one at a time
 
 // ---------------------------------------------------------------- 2^(j/256)
 struct Table {
@@ -326,40 +331,53 @@ struct Sums {
   float q;
 };
 // This lane's part of the elements lo .. stop-1 (lo where a 16-byte piece begins, perhaps before the row).
-template <bool Q, typename T>
+// Long: of more than kShort tiles; the lower parts' sums are put aside after every kChain.
+template <bool Q, bool Long, typename T>
 __device__ __forceinline__ Sums segment(const Source<T>& src, int lo, int stop, const Row& r, const float2* table) {
-  float e0 = 0.f, e1 = 0.f, w0 = 0.f, w1 = 0.f, sum_q = 0.f;
+  float e0 = 0.f, e1 = 0.f, w0 = 0.f, w1 = 0.f, sum_q = 0.f, all_q = 0.f;
+  int64_t e = 0, w = 0;
   int v = lo + (threadIdx.x & 31) * 8;
   Raw8<T> x = src.logits(v);
   Raw8<float> y{};
   if constexpr (Q) y = src.shares(v);
-  for (; v < stop; v += kTile) {
-    const Raw8<T> x1 = src.logits(v + kTile);  // under this tile's arithmetic
-    Raw8<float> y1{};
-    if constexpr (Q) y1 = src.shares(v + kTile);
+  auto add = [&](int till) {
+    for (; v < till; v += kTile) {
+      const Raw8<T> x1 = src.logits(v + kTile);  // under this tile's arithmetic
+      Raw8<float> y1{};
+      if constexpr (Q) y1 = src.shares(v + kTile);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float a, b;
-      weight(element(x, i), r, table, a, b);
-      const float a0 = on_grid(a), a1 = (a - a0) + b;
-      e0 += a0, e1 += a1;
-      if constexpr (Q) {
-        const float q = fmaxf(element(y, i), 0.f), s = q * r.z0, s0 = on_grid(s);
-        const float d0 = a0 - s0, d1 = a1 - ((s - s0) + fmaf(q, r.z0, -s));
-        if (d0 + d1 > 0.f) w0 += d0, w1 += d1, sum_q += q;
+      for (int i = 0; i < 8; ++i) {
+        float a, b;
+        weight(element(x, i), r, table, a, b);
+        const float a0 = on_grid(a), a1 = (a - a0) + b;
+        e0 += a0, e1 += a1;
+        if constexpr (Q) {
+          const float q = fmaxf(element(y, i), 0.f), s = q * r.z0, s0 = on_grid(s);
+          const float d0 = a0 - s0, d1 = a1 - ((s - s0) + fmaf(q, r.z0, -s));
+          if (d0 + d1 > 0.f) w0 += d0, w1 += d1, sum_q += q;
+        }
       }
+      x = x1, y = y1;
     }
-    x = x1, y = y1;
+  };
+  if constexpr (Long) {
+    while (v < stop) {
+      add(min(stop, v + kChain * kTile));
+      e += fixed(e1), e1 = 0.f;
+      if constexpr (Q) w += fixed(w1), w1 = 0.f, all_q += sum_q, sum_q = 0.f;
+    }
+  } else {
+    add(stop);
   }
   Sums s;
-  s.e = (uint64_t)fixed(e0, e1);
+  s.e = (uint64_t)(e + fixed(e0, e1));
   if constexpr (Q) {
-    const int64_t w = fixed(w0, w1);
+    w += fixed(w0, w1);
     s.w = w > 0 ? (uint64_t)w : 0;
   } else {
     s.w = s.e;
   }
-  s.q = sum_q;
+  s.q = all_q + sum_q;
   return s;
 }
 
@@ -441,7 +459,7 @@ __device__ __forceinline__ int look(const Source<T>& src, const Row& w, const fl
   return found;
 }
 
-template <typename T>
+template <typename T, bool Long>
 __global__ void __launch_bounds__(kThreads, 4) verify_draw_kernel(const VerifyParams p) {
   using Team = Cluster<0>;
   __shared__ float2 table[256];
@@ -550,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_draw_kernel(const VerifyPa
     const int64_t lo = (int64_t)((int)rank * kWarps + warp) * each - shift;
     const int stop = (int)(lo + each < V ? lo + each : V);
     Sums s{};
-    if (lo < V) s = q ? segment<true>(src, (int)lo, stop, w, table) : segment<false>(src, (int)lo, stop, w, table);
+    if (lo < V) s = q ? segment<true, Long>(src, (int)lo, stop, w, table) : segment<false, Long>(src, (int)lo, stop, w, table);
     s.e = warp_sum(s.e), s.w = warp_sum(s.w), s.q = warp_sum(s.q);
     if (draft >= 0 && draft >= lo && draft < lo + each) {
       float a, b;
@@ -801,8 +819,12 @@ cudaError_t launch_draft_verify(const VerifyParams& p, cudaStream_t s) {
     ++n;
   }
   cfg.attrs = at, cfg.numAttrs = n;
+  // A row's segments of more than kShort tiles (524,000 tokens over eight blocks, 65,000 over one) take the form that keeps
+  // its float32 sums short; in it 64 x 5 rows of 128,000 take 29.2 us instead of 28.6, 310 x 2 of 152,064 160 instead of 157.
+  const bool many = (int64_t)p.d.vocab + 7 > (int64_t)kShort * kTile * kWarps * blocks;
   auto kernel = one ? (wide ? one_draw_kernel<float> : one_draw_kernel<__nv_bfloat16>)
-                    : (wide ? verify_draw_kernel<float> : verify_draw_kernel<__nv_bfloat16>);
+                : many ? (wide ? verify_draw_kernel<float, true> : verify_draw_kernel<__nv_bfloat16, true>)
+                       : (wide ? verify_draw_kernel<float, false> : verify_draw_kernel<__nv_bfloat16, false>);
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 

@@ -94,6 +94,13 @@ def test_bad_verify_descs(ls, bad, status):
     assert ls.lib().ls_draft_verify_workspace_size(ctypes.byref(verify(ls, **bad)), ctypes.byref(n)) == status
 
 
+def test_vocabularies(ls):
+    n = ctypes.c_size_t(0)
+    for vocab, status in ((1 << 24, 0), ((1 << 24) + 1, 2), (1 << 30, 2)):
+        d = verify(ls, vocab=vocab, logits_stride=vocab, draft_stride=vocab)
+        assert ls.lib().ls_draft_verify_workspace_size(ctypes.byref(d), ctypes.byref(n)) == status
+
+
 def test_verify_calls(ls):
     L = ls.lib()
     need = ls.ls_draft_verify_workspace_size(verify(ls))

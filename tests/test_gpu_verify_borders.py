@@ -1,9 +1,17 @@
-"""Verification of drafts where a decision can go wrong."""
+"""Verification of drafts where a decision can go wrong.
+
+Bounds.  An acceptance: a 2 KB piece's exponentials are 4 roundings of 2^-24 each (ex2's 2^-22), at most 23 additions
+on their way, then up to 8 joins in a lane and 5 between lanes at 2^17 float32 logits, 6 roundings each (an addition,
+two of the argument, ex2); the arguments' own roundings are 2.5 2^-24 of the mean of -log2 p over the row, at most 13
+there, times ln 2: in all 4 + 23 + 78 + 22 = 127 roundings of 2^-24, and with the products and exp2f of the test
+itself and 1.4 roundings for each bit that the draft is below the largest, under 256 for p down to 2^-80: 2^-16.  The
+joins in a lane double with the vocabulary.  A draw's bounds stand at its tests."""
 import math
 
 import pytest
 import torch
 
+import long_context_grpo_replay_gb300.binding as ls
 from test_gpu_verify import LOW, check, make, run
 
 pytestmark = pytest.mark.gpu
@@ -131,3 +139,61 @@ def test_what_a_rejection_leaves_at_its_threshold(cuda_device):
     assert got[1][2::4].tolist() == [j] * (n // 2)
     assert j not in got[1][::4].tolist()
     check(m, got)
+
+
+def test_draws_from_millions_of_tokens(cuda_device):
+    """A row of one large and V - 1 equal logits: the steps of the draw are known.  All lower parts of a thread's weights
+    are alike, so that the roundings of their float32 sum add up: over 64 of them at most 2^-20 (1 + 1/4 + ...) / 2 of
+    the sum, 2^-20.6, and as a block's warp holds a sixteenth of the row here (160 sequences, two blocks each), a border
+    moves by 2^-24.6 of the whole.  The random numbers are float32 and lie in the middle of a token, 2^-23 from its
+    borders but for their rounding of 2^-25."""
+    v, b, x = 4_000_003, 160, 1.296875
+    g = torch.Generator().manual_seed(39)
+    row = torch.zeros(v, dtype=torch.bfloat16, device="cuda")
+    row[0] = x
+    logits = row.expand(2 * b, v).contiguous()
+    top = math.exp(x)
+    total = top + v - 1
+    want = torch.randint(1, v, (b,), generator=g)
+    ends = (torch.arange(1, 17) * (v // 16)).clamp(max=v - 1)   # about the last tokens of the segments
+    want[:16] = ends - 1
+    u_next = ((top + want.double() - 0.5) / total).float()
+    i32, i64 = torch.int32, torch.int64
+    desc = ls.verify_desc(logits, b, 2)
+    ws = torch.zeros(ls.ls_draft_verify_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    count, out = torch.empty(b, dtype=i32, device="cuda"), torch.empty(2 * b, dtype=i64, device="cuda")
+    ls.ls_draft_verify(desc, logits, torch.ones(2 * b, dtype=i64, device="cuda"), torch.arange(0, 2 * b + 1, 2, dtype=i32, device="cuda"),
+                       torch.zeros(2 * b, device="cuda"), u_next.cuda(), count, out, None, ws)
+    ls.ls_read_device_status(ws)
+    assert (count == 2).all()
+    got = out.cpu()[1::2]
+    assert torch.equal(got, want), (got - want)[got != want]
+
+
+@pytest.mark.parametrize("dtype,probs", [(torch.float32, True), (torch.bfloat16, True), (torch.bfloat16, False)])
+def test_draws_from_a_million_tokens(cuda_device, dtype, probs):
+    """Rejected and accepted drafts over a long row with a tail.  Some 10^6 lower parts are added in float32, each rounding
+    within 2^-42 of the row (half a step of a sum of 64 below 2^-17): where they fall as they may 2^-32 in all, and the
+    weights' own 2^-30 of each add 2^-40.  Draws within 2^-28 of the row of a border are left out."""
+    v, b = 1_000_003, 48
+    m = make([2] * b, v, dtype, probs, spread=1.5, seed=45, device="cuda")
+    m["u"][::4] = 0.0
+    count, out, _, _ = run(m)
+    left_out = 0
+    for i in range(b):
+        r = 2 * i + int(count[i]) - 1
+        z = m["wide"][2 * i:2 * i + 2].double()
+        p = torch.softmax(z, 1)
+        d = int(m["tokens"][2 * i + 1])
+        q = m["probs"][2 * i].double() if probs else torch.nn.functional.one_hot(m["tokens"][2 * i + 1], v).double()
+        side = float(m["u"][2 * i]) * float(q[d]), float(p[0, d])
+        if abs(side[0] - side[1]) > 2.0 ** -13 * max(side):   # 2^-16, doubled three times
+            assert int(count[i]) == 1 + (side[0] < side[1])
+        w = p[1] if r % 2 else (p[0] - q).clamp(min=0)
+        upto = torch.cumsum(w, 0)
+        edge = float(m["u_next"][i]) * float(upto[-1])
+        if float((upto - edge).abs().min()) < 2.0 ** -28:
+            left_out += 1
+            continue
+        assert int(out[r]) == int((upto <= edge).sum())
+    assert left_out <= 3
