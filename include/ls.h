@@ -609,7 +609,8 @@ LS_API ls_status ls_cache_copy_pages(const ls_kv_cache* cache, const int32_t* co
  * accepted drafts, then the new token, then -1s; logp[r] = log p_r(emitted[r]), 0
  * where there is none; n_emitted[b] their number; keep[b] = kv_len[b] - n +
  * n_emitted[b], the tokens whose keys stay valid (what ls_pages_advance keeps and, as
- * n_use, n_emitted makes ls_gdn_decode keep).  A sequence without rows has none:
+ * n_use, n_emitted makes ls_gdn_decode keep; but see the row without a distribution).
+ * A sequence without rows has none:
  * n_emitted 0, keep its kv_len.  Rows that judge no draft may hold anything in
  * draft_probs and u; elsewhere what is not above 0 in draft_probs counts as 0.
  *   logits may be -infinity or the type's lowest value (a masked token); a draft's
@@ -617,7 +618,9 @@ LS_API ls_status ls_cache_copy_pages(const ls_kv_cache* cache, const int32_t* co
  *     that has no distribution (all -infinity, or a NaN or +infinity in it) accepts
  *     nothing; where it had to give the next token, emitted is -1 there, n_emitted
  *     counts the drafts before it, keep their keys and the last token's, and the
- *     status word says so.  A draft outside [0, vocab) is rejected and reported.
+ *     status word says so.  There n_emitted is one less than the tokens that are kept:
+ *     a caller that goes on gives ls_gdn_decode n_use = keep - kv_len + n, which is
+ *     n_emitted for all other sequences that were not left out.  A draft outside [0, vocab) is rejected and reported.
  *   An acceptance within 2^-16 of its border (relative; twice that for each
  *     doubling of vocab beyond 2^17; about 2^-20 in practice) may fall either way.
  *     The weights of the draw are good to 2^-30 each (those below 2^-23 of the row to

@@ -12,6 +12,7 @@ import pytest
 import torch
 
 import long_context_grpo_replay_gb300.binding as ls
+from oracle import drafts as ref
 from test_gpu_verify import LOW, check, make, run
 
 pytestmark = pytest.mark.gpu
@@ -197,3 +198,49 @@ def test_draws_from_a_million_tokens(cuda_device, dtype, probs):
             continue
         assert int(out[r]) == int((upto <= edge).sum())
     assert left_out <= 3
+
+
+@pytest.mark.parametrize("value", [-math.inf, math.nan])
+def test_caches_go_on_together(cuda_device, value):
+    """keep - kv_len + n is how many of a sequence's n tokens have their keys kept, and how many the recurrent state takes:
+    also behind a row without a distribution, where it is one more than n_emitted."""
+    counts = [3, 2, 1, 0, 4]
+    m = make(counts, 1031, torch.float32, probs=False, seed=43)
+    m["u"][:] = 0.0                                    # every draft passes
+    m["wide"][2] = value                               # the first's last row, the second's first
+    m["wide"][3] = value
+    b, n, page = len(counts), sum(counts), 4
+    i32, i64 = torch.int32, torch.int64
+    dev = lambda t: t.cuda()  # noqa: E731
+    refs, table = torch.zeros(64, dtype=i32, device="cuda"), torch.zeros((b, 16), dtype=i32, device="cuda")
+    kv_len = torch.zeros(b, dtype=i64, device="cuda")
+    book = ls.page_book(refs, table, kv_len, page)
+    pws = torch.zeros(ls.ls_pages_workspace_size(book), dtype=torch.uint8, device="cuda")
+    slots, copies = torch.empty(5 * b + n, dtype=i64, device="cuda"), torch.empty((b, 3), dtype=i32, device="cuda")
+    grown = torch.tensor([5 + c for c in counts])
+    starts = torch.cat([torch.zeros(1, dtype=i64), grown.cumsum(0)]).to(i32)
+    ls.ls_pages_advance(book, dev(starts), slots, copies, pws)
+    logits, q_start = dev(m["wide"]), torch.tensor(m["q_start"], dtype=i32, device="cuda")
+    desc = ls.verify_desc(logits, b, max(counts))
+    ws = torch.zeros(ls.ls_draft_verify_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    count, out, keep = torch.empty(b, dtype=i32, device="cuda"), torch.empty(n, dtype=i64, device="cuda"), torch.empty(b, dtype=i64, device="cuda")
+    ls.ls_draft_verify(desc, logits, dev(m["tokens"]), q_start, dev(m["u"]), dev(m["u_next"]), count, out, None, ws, kv_len=kv_len, keep=keep)
+    with pytest.raises(ls.LsError):
+        ls.ls_read_device_status(ws)
+    n_use = (keep - kv_len + torch.tensor(counts, device="cuda")).to(i32)
+    assert n_use.tolist() == [3, 1, 1, 0, 4] and count.tolist() == [2, 0, 1, 0, 4]
+    g = torch.Generator().manual_seed(44)
+    q, k, v = (torch.randn(n, 1, 128, generator=g) * s for s in (0.1, 0.1, 1.0))
+    decay, beta = -0.1 * torch.rand(n, 1, generator=g), torch.rand(n, 1, generator=g)
+    states = torch.randn(b, 1, 128, 128, generator=g)
+    d = [dev(t) for t in (states, q, k, v, decay, beta)]
+    own = torch.arange(b, dtype=i32, device="cuda")
+    ls.ls_gdn_decode(ls.gdn_decode_desc(*d[1:4], d[0], b, max(counts)), *d, q_start, own, own, None, pws, n_use=n_use)
+    ls.ls_pages_advance(book, None, None, None, pws, keep=keep)
+    ls.ls_read_device_status(pws)
+    for i in range(b):
+        used = int(n_use[i])
+        assert int(kv_len[i]) == 5 + used
+        at = slice(m["q_start"][i], m["q_start"][i] + used)
+        _, want, _, mag = ref.state_step(states[i], q[at], k[at], v[at], decay[at], beta[at])
+        assert ((d[0][i].double().cpu() - want).abs() <= 28 * used * 2.0 ** -24 * mag).all()
