@@ -649,8 +649,9 @@ LS_API ls_status ls_draft_verify_workspace_size(const ls_verify_desc* desc, size
  * float32 [total_q] or NULL; kv_len and keep int64 [batch], or keep NULL.  max_q is an
  * upper bound of a sequence's rows (max_q <= total_q <= batch * max_q); a sequence with
  * more, or with rows outside [0, total_q), is left out (n_emitted 0, its rows of emitted
- * and logp as they were, keep its kv_len) and reported.  emitted must not overlap tokens,
- * nor logp u; keep may be kv_len. */
+ * and logp as they were, keep its kv_len) and reported.  The results must not overlap
+ * the inputs; but keep may be kv_len (not a book's: ls_pages_advance has to see the
+ * length before as well, or the pages between stay taken). */
 LS_API ls_status ls_draft_verify(const ls_verify_desc* desc, const void* logits,
                                  const float* draft_probs, const int64_t* tokens,
                                  const int32_t* q_start, const float* u, const float* u_next,

@@ -6,6 +6,7 @@
 
 #include <climits>
 #include <cmath>
+#include <initializer_list>
 
 #include "ls_internal.h"
 
@@ -13,10 +14,21 @@ namespace ls {
 namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-// Bytes a .. a+na-1 and b .. b+nb-1 (NULL: none).
-bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x && y && x < y + nb && y < x + na;
+// A run of bytes (NULL: none).
+struct Run {
+  const void* at;
+  uint64_t bytes;
+};
+bool overlap(const Run& a, const Run& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return x && y && x < y + b.bytes && y < x + a.bytes;
+}
+// What a block writes, none of what others still read.
+bool apart(std::initializer_list<Run> written, std::initializer_list<Run> read) {
+  for (const Run& a : written)
+    for (const Run& b : read)
+      if (overlap(a, b)) return false;
+  return true;
 }
 bool known_dtype(int32_t t) { return t == LS_DTYPE_F32 || t == LS_DTYPE_BF16; }
 
@@ -247,9 +259,12 @@ ls_status ls_draft_verify(const ls_verify_desc* desc, const void* logits, const 
       !aligned(q_start, 4) || !aligned(u, 4) || !aligned(u_next, 4) || !aligned(kv_len, 8) || !aligned(n_emitted, 4) ||
       !aligned(emitted, 8) || !aligned(logp, 4) || !aligned(keep, 8))
     return fail(LS_ERR_INVALID_ARGUMENT, "buffers must be aligned to their elements");
-  // one block of a sequence writes while the others read on
-  if (overlap(emitted, 8 * desc->total_q, tokens, 8 * desc->total_q) || overlap(logp, 4 * desc->total_q, u, 4 * desc->total_q))
-    return fail(LS_ERR_INVALID_ARGUMENT, "emitted and logp must not overlap tokens and u");
+  // one block of a sequence writes while others, and those of other sequences, read on
+  const uint64_t n = desc->total_q, b = desc->batch;
+  if (!apart({{n_emitted, 4 * b}, {emitted, 8 * n}, {logp, 4 * n}, {keep, 8 * b}},
+             {{tokens, 8 * n}, {q_start, 4 * (b + 1)}, {u, 4 * n}, {u_next, 4 * b}}) ||
+      (keep && !apart({{n_emitted, 4 * b}, {emitted, 8 * n}, {logp, 4 * n}, {keep == kv_len ? nullptr : keep, 8 * b}}, {{kv_len, 8 * b}})))
+    return fail(LS_ERR_INVALID_ARGUMENT, "the results must not overlap the inputs (but keep may be kv_len)");
   LS_CHECK(check_ws(ws, ws_bytes, verify_need(*desc)));
   VerifyParams p{};
   p.d = *desc;
@@ -292,9 +307,9 @@ ls_status ls_gdn_decode(const ls_gdn_decode_desc* desc, float* states, const voi
   // a block writes its rows of o while others read on
   const uint64_t size = desc->dtype == LS_DTYPE_F32 ? 4 : 2, n = desc->total_q, key = (uint64_t)desc->key_heads * desc->dk,
                  val = (uint64_t)desc->heads * desc->dv;
-  if (n > 0 && (overlap(o, size * n * val, q, size * ((n - 1) * desc->q_stride + key)) ||
-                overlap(o, size * n * val, k, size * ((n - 1) * desc->k_stride + key)) ||
-                overlap(o, size * n * val, v, size * ((n - 1) * desc->v_stride + val))))
+  if (n > 0 && !apart({{o, size * n * val}}, {{q, size * ((n - 1) * desc->q_stride + key)},
+                                              {k, size * ((n - 1) * desc->k_stride + key)},
+                                              {v, size * ((n - 1) * desc->v_stride + val)}}))
     return fail(LS_ERR_INVALID_ARGUMENT, "o must not overlap q, k or v");
   GdnDecodeParams p{};
   LS_CHECK(status_word(ws, ws_bytes, &p.status));

@@ -123,6 +123,28 @@ def test_verify_calls(ls):
     assert call(verify(ls, draft_stride=99)) == 1 and call(nb=need - 1) == 3 and call(ws=None) == 1 and call(ws=A + 16) == 1
 
 
+def test_results_of_a_verification_over_its_inputs(ls):
+    """Blocks write results while others still read: every result against every small input, touching ends aside."""
+    L = ls.lib()
+    desc = verify(ls)                                        # 5 rows of 3 sequences
+    need = ls.ls_draft_verify_workspace_size(desc)
+    names = ("logits", "probs", "tokens", "q_start", "u", "u_next", "kv_len", "count", "out", "logp", "keep")
+    size = dict(tokens=40, q_start=16, u=20, u_next=12, kv_len=24, count=12, out=40, logp=20, keep=24)
+
+    def call(**kw):
+        d = {n: A + (i << 40) for i, n in enumerate(names)} | kw  # apart
+        return L.ls_draft_verify(ctypes.byref(desc), *(d[n] for n in names), None, need, None)
+
+    assert call() == 1 and b"overlap" not in L.ls_last_error()  # ws is NULL: nothing is launched here
+    for result in ("count", "out", "logp", "keep"):
+        for given in ("tokens", "q_start", "u", "u_next", "kv_len"):
+            for off, bad in ((0, (result, given) != ("keep", "kv_len")), (8 * ((size[given] - 1) // 8), True), (-8 * ((size[result] - 1) // 8), True),
+                             (8 * (size[given] // 8 + 1), False), (-8 * (size[result] // 8 + 1), False)):
+                assert call(**{result: 2 * A + off, given: 2 * A}) == 1
+                assert (b"overlap" in L.ls_last_error()) == bad, (result, given, off)
+    assert call(keep=None, kv_len=2 * A, out=2 * A) == 1 and b"overlap" not in L.ls_last_error()  # kv_len is not read then
+
+
 @pytest.mark.parametrize("bad,status", [
     (dict(dtype=2), 1), (dict(heads=0), 1), (dict(key_heads=3), 1), (dict(key_heads=0), 1), (dict(dk=64), 2), (dict(dv=256), 2),
     (dict(heads=131072), 2), (dict(batch=-1), 1), (dict(batch=65536), 2), (dict(total_q=9), 1), (dict(max_q=6), 1), (dict(n_states=0), 1),
