@@ -675,8 +675,8 @@ LS_API ls_status ls_draft_verify(const ls_verify_desc* desc, const void* logits,
  *   key_heads divides heads: value head h takes q and k of head
  *     h / (heads / key_heads).  q, k [total_q][key_heads][dk], v [total_q][heads][dv],
  *     token strides in elements, multiples of 8 (rows of one projection as they
- *     lie); g, beta [total_q][heads] and o [total_q][heads][dv] contiguous, o apart
- *     from q, k and v.
+ *     lie); g, beta [total_q][heads] and o [total_q][heads][dv] contiguous.  o and
+ *     the states must not overlap each other or anything that the call reads.
  *   states [n_states][heads][dv][dk].  dk = dv = 128.
  *   max_q: upper bound of a sequence's tokens (max_q <= total_q <= batch * max_q). */
 typedef struct {

@@ -14,14 +14,14 @@ namespace ls {
 namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-// A run of bytes (NULL: none).
+// A run of bytes (none of them, or NULL: nothing).
 struct Run {
   const void* at;
   uint64_t bytes;
 };
 bool overlap(const Run& a, const Run& b) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
-  return x && y && x < y + b.bytes && y < x + a.bytes;
+  return x && y && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
 }
 // What a block writes, none of what others still read.
 bool apart(std::initializer_list<Run> written, std::initializer_list<Run> read) {
@@ -304,13 +304,21 @@ ls_status ls_gdn_decode(const ls_gdn_decode_desc* desc, float* states, const voi
   if (!aligned(g, 4) || !aligned(beta, 4) || !aligned(q_start, 4) || !aligned(n_use, 4) || !aligned(state_in, 4) ||
       !aligned(state_out, 4))
     return fail(LS_ERR_INVALID_ARGUMENT, "buffers must be aligned to their elements");
-  // a block writes its rows of o while others read on
-  const uint64_t size = desc->dtype == LS_DTYPE_F32 ? 4 : 2, n = desc->total_q, key = (uint64_t)desc->key_heads * desc->dk,
-                 val = (uint64_t)desc->heads * desc->dv;
-  if (n > 0 && !apart({{o, size * n * val}}, {{q, size * ((n - 1) * desc->q_stride + key)},
-                                              {k, size * ((n - 1) * desc->k_stride + key)},
-                                              {v, size * ((n - 1) * desc->v_stride + val)}}))
-    return fail(LS_ERR_INVALID_ARGUMENT, "o must not overlap q, k or v");
+  // a block writes its rows of o and of the states while others read on
+  const uint64_t size = desc->dtype == LS_DTYPE_F32 ? 4 : 2, n = desc->total_q, b = desc->batch, h = desc->heads,
+                 key = (uint64_t)desc->key_heads * desc->dk, val = h * desc->dv, last = n > 0 ? n - 1 : 0;
+  const Run results[] = {{o, size * n * val}, {states, 4 * desc->n_states * val * desc->dk}};
+  if (overlap(results[0], results[1]) ||
+      !apart({results[0], results[1]}, {{q, n ? size * (last * desc->q_stride + key) : 0},
+                                        {k, n ? size * (last * desc->k_stride + key) : 0},
+                                        {v, n ? size * (last * desc->v_stride + val) : 0},
+                                        {g, 4 * n * h},
+                                        {beta, 4 * n * h},
+                                        {q_start, 4 * (b + 1)},
+                                        {n_use, 4 * b},
+                                        {state_in, 4 * b},
+                                        {state_out, 4 * b}}))
+    return fail(LS_ERR_INVALID_ARGUMENT, "o and states must not overlap each other or what the call reads");
   GdnDecodeParams p{};
   LS_CHECK(status_word(ws, ws_bytes, &p.status));
   p.d = *desc;

@@ -175,6 +175,28 @@ def test_decode_calls(ls):
     assert call(ws=A, nb=255) == 3 and call(ws=A + 8, nb=256) == 1
 
 
+def test_results_of_a_recurrent_step_over_its_inputs(ls):
+    """Blocks write rows of o and of the states while others still read."""
+    L = ls.lib()
+    names = ("states", "q", "k", "v", "g", "beta", "q_start", "n_use", "state_in", "state_out", "o")
+    size = dict(states=6 * 4 * 128 * 128 * 4, q=2 * (4 * 1024 + 256), k=2 * (4 * 1024 + 256), v=2 * (4 * 1024 + 512), g=80, beta=80, q_start=16,
+                n_use=12, state_in=12, state_out=12, o=5 * 4 * 128 * 2)
+
+    def call(**kw):
+        d = {n: A + (i << 40) for i, n in enumerate(names)} | kw  # apart
+        return L.ls_gdn_decode(ctypes.byref(decode(ls)), *(d[n] for n in names), A + 8, 256, None)
+
+    assert call() == 1 and b"overlap" not in L.ls_last_error()  # ws is not aligned: nothing is launched here
+    for result in ("o", "states"):
+        for other in names:
+            if other == result:
+                continue
+            for off, bad in ((0, True), (16 * ((size[other] - 1) // 16), True), (-16 * ((size[result] - 1) // 16), True),
+                             (16 * (size[other] // 16 + 1), False), (-16 * (size[result] // 16 + 1), False)):
+                assert call(**{result: 2 * A + off, other: 2 * A}) == 1
+                assert (b"overlap" in L.ls_last_error()) == bad, (result, other, off)
+
+
 def test_binding_checks_tensors(ls):
     z = lambda *s, dt=I32: torch.zeros(*s, dtype=dt)  # noqa: E731
     with pytest.raises(TypeError):
