@@ -531,7 +531,9 @@ LS_API ls_status ls_vocab_logprob_bwd(const ls_vocab_desc* desc, const void* h, 
  * and reported.  A call whose lists are not valid (a sequence out of range or
  * named twice, a length out of range, q_start not rising from 0 to total_q)
  * changes nothing but the results for the caller (slots and copies all -1), and
- * is reported.  ws: ls_pages_workspace_size() bytes, for one call at a time. */
+ * is reported.  The book's tensors, the lists and the results must not overlap (but
+ * kv_len may be the list of lengths that are kept).  ws: ls_pages_workspace_size()
+ * bytes, for one call at a time. */
 typedef struct {
   int32_t page_size;
   int32_t n_seqs;

@@ -116,6 +116,20 @@ ls_status pages_params(const ls_page_book* b, int64_t n, void* ws, size_t ws_byt
   return LS_OK;
 }
 
+Run refs_of(const ls_page_book& b) { return {b.refs, 4 * (uint64_t)b.pool_pages}; }
+Run table_of(const ls_page_book& b) { return {b.page_table, 4 * (uint64_t)b.n_seqs * b.pages_per_seq}; }
+Run lengths_of(const ls_page_book& b) { return {b.kv_len, 8 * (uint64_t)b.n_seqs}; }
+// Lists that a kernel of pages reads in every block before, and beside, the first writes (of lengths as int64,
+// kv_len itself may be one: it is written when all have been read).
+ls_status check_lists(const ls_page_book& b, const Run& seqs, const Run& more, const Run& lengths, const Run& slots, const Run& copies) {
+  const Run len = lengths.at == b.kv_len ? Run{nullptr, 0} : lengths;
+  if (!apart({slots, copies, refs_of(b), table_of(b), lengths_of(b)}, {seqs, more, len}) ||
+      !apart({refs_of(b), table_of(b), slots, copies}, {lengths}) || !apart({slots, copies}, {refs_of(b), table_of(b), lengths_of(b)}) ||
+      overlap(slots, copies))
+    return fail(LS_ERR_INVALID_ARGUMENT, "slots, copies and the book must not overlap each other or the lists");
+  return LS_OK;
+}
+
 ls_status check_verify(const ls_verify_desc* d) {
   if (!d) return fail(LS_ERR_INVALID_ARGUMENT, "desc is NULL");
   if (!known_dtype(d->dtype))
@@ -167,6 +181,8 @@ ls_status ls_pages_advance(const ls_page_book* book, int32_t n, const int32_t* s
   PagesParams p{};
   LS_CHECK(pages_params(book, n, ws, ws_bytes, &p));
   if (n == 0) return LS_OK;
+  LS_CHECK(check_lists(*book, {seqs, 4 * (uint64_t)n}, {q_start, 4 * ((uint64_t)n + 1)}, {keep, 8 * (uint64_t)n},
+                       {slots, 8 * (uint64_t)total_q}, {copies, 12 * (uint64_t)n}));
   p.seqs = seqs;
   p.keep = keep;
   p.q_start = q_start;
@@ -184,6 +200,7 @@ ls_status ls_pages_release(const ls_page_book* book, int32_t n, const int32_t* s
   PagesParams p{};
   LS_CHECK(pages_params(book, seqs ? n : book->n_seqs, ws, ws_bytes, &p));
   if (p.n == 0) return LS_OK;
+  LS_CHECK(check_lists(*book, {seqs, 4 * (uint64_t)p.n}, {}, {}, {}, {}));
   p.seqs = seqs;
   p.drop_all = true;
   LS_CUDA(launch_pages_advance(p, static_cast<cudaStream_t>(stream)), "pages launch");
@@ -199,6 +216,7 @@ ls_status ls_pages_fork(const ls_page_book* book, int32_t n, const int32_t* src,
   LS_CHECK(pages_params(book, n, ws, ws_bytes, &p));
   if (n == 0) return LS_OK;
   if (!src || !dst) return fail(LS_ERR_INVALID_ARGUMENT, "src and dst must be non-NULL");
+  LS_CHECK(check_lists(*book, {src, 4 * (uint64_t)n}, {dst, 4 * (uint64_t)n}, {lens, 8 * (uint64_t)n}, {}, {}));
   p.src = src;
   p.seqs = dst;
   p.keep = lens;
@@ -215,6 +233,11 @@ ls_status ls_pages_compact(const ls_page_book* book, int32_t* table_out, int32_t
     return fail(LS_ERR_INVALID_ARGUMENT, "buffers must be aligned to their elements");
   PagesParams p{};
   LS_CHECK(pages_params(book, 0, ws, ws_bytes, &p));
+  const Run refs = refs_of(*book), table = table_of(*book), out_refs{refs_out, refs.bytes}, out_table{table_out, table.bytes},
+            moves{copies, 12 * (uint64_t)(book->pool_pages / 2)};
+  if (!apart({out_refs, moves}, {table, lengths_of(*book), out_table}) || !apart({out_table, moves}, {refs, lengths_of(*book), out_refs}) ||
+      (refs_out != book->refs && overlap(out_refs, refs)) || (table_out != book->page_table && overlap(out_table, table)))
+    return fail(LS_ERR_INVALID_ARGUMENT, "table_out, refs_out and copies must not overlap each other or the book (but each may be the book's own)");
   p.copies = copies;
   p.table_out = table_out;
   p.refs_out = refs_out;

@@ -84,6 +84,46 @@ def test_pages_calls(ls):
     assert ls.ls_status_string(7) == "LS_ERR_OUT_OF_PAGES"
 
 
+def test_results_of_the_pages_over_lists_and_book(ls):
+    """What is read while other blocks write, and the results among each other.  (Calls that are right are made by the GPU's
+    tests: nothing stops them before the launch.)"""
+    L = ls.lib()
+    at = lambda i: A + (i << 40)  # noqa: E731
+    size = dict(refs=128, page_table=128, kv_len=32, seqs=12, keep=24, q_start=16, slots=56, copies=36, src=12, dst=12, lens=24,
+                table_out=128, refs_out=128, moves=16 * 12)
+    need = ls.ls_pages_workspace_size(book(ls))
+
+    def call(kind, **kw):
+        d = {n: at(i) for i, n in enumerate(size)} | kw
+        bk = ctypes.byref(book(ls, refs=d["refs"], page_table=d["page_table"], kv_len=d["kv_len"]))
+        if kind == "advance":
+            st = L.ls_pages_advance(bk, 3, d["seqs"], d["keep"], d["q_start"], 7, d["slots"], d["copies"], at(20), need, None)
+        elif kind == "release":
+            st = L.ls_pages_release(bk, 3, d["seqs"], at(20), need, None)
+        elif kind == "fork":
+            st = L.ls_pages_fork(bk, 3, d["src"], d["dst"], d["lens"], at(20), need, None)
+        else:
+            st = L.ls_pages_compact(bk, d["table_out"], d["refs_out"], d["moves"], at(20), need, None)
+        assert st == 1 and b"overlap" in L.ls_last_error(), (kind, kw)
+
+    book_of = ("refs", "page_table", "kv_len")
+    pairs = dict(
+        advance=[(a, x) for a in ("slots", "copies") + book_of for x in ("seqs", "q_start", "keep") if (a, x) != ("kv_len", "keep")] +
+                [(a, x) for a in ("slots", "copies") for x in book_of] + [("slots", "copies")],
+        release=[(a, "seqs") for a in book_of],
+        fork=[(a, x) for a in book_of for x in ("src", "dst")] + [("refs", "lens"), ("page_table", "lens")],
+        compact=[("refs_out", x) for x in ("page_table", "kv_len", "table_out")] + [("table_out", x) for x in ("refs", "kv_len")] +
+                [("moves", x) for x in book_of + ("table_out", "refs_out")])
+    for kind, which in pairs.items():
+        for a, x in which:
+            for off in (0, 8 * ((size[x] - 1) // 8), -8 * ((size[a] - 1) // 8)):
+                call(kind, **{a: 2 * A + off, x: 2 * A})
+    call("advance", kv_len=2 * A, keep=2 * A + 8)            # a part of it
+    call("fork", kv_len=2 * A, lens=2 * A + 8)
+    call("compact", refs=2 * A, refs_out=2 * A + 4)
+    call("compact", page_table=2 * A, table_out=2 * A - 4)
+
+
 @pytest.mark.parametrize("bad,status", [
     (dict(dtype=2), 1), (dict(vocab=0), 1), (dict(vocab=(1 << 30) + 1, logits_stride=1 << 31), 2), (dict(batch=-1), 1),
     (dict(batch=70000, max_q=1), 2), (dict(total_q=-1), 1), (dict(total_q=7), 1), (dict(max_q=6), 1), (dict(max_q=1), 1),
