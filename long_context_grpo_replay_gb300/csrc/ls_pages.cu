@@ -500,15 +500,24 @@ size_t pages_scratch(const ls_page_book& b) {
   return 4 * (3 * (size_t)b.pool_pages + 8 * (size_t)b.n_seqs * (b.n_seqs > kListed ? 1 + kListArrays : 1));
 }
 
+// One block or eight, measured in a graph.  A step of three tokens a sequence (one block / eight, us): 64 sequences over
+// 8192 pages 4.4 / 6.6, over 40,960 6.4 / 6.8, over 65,536 7.6 / 6.8; 384 over 8192 6.4 / 6.9, 512 7.3 / 6.7.  So a step
+// that drops little goes on being faster on one block up to some 35,000 pages or 400 sequences; but a call does not say
+// how many entries it drops: a release of 4096 takes 9.6 / 9.5 with the fork before it, of 8192 12.7 / 9.6.  The limits
+// stand where all pages of the pool, each named once, may go.  (Entries of pages that many share and slots are not looked
+// at: 64 x 4000 of the first take 197 / 35, 65,536 of the second for one sequence 22.9 / 9.4.)
 cudaError_t launch_pages_advance(const PagesParams& p, cudaStream_t s) {
   return launch_team(pages_advance_kernel<1>, pages_advance_kernel<8>, p.b.pool_pages > 4096 || p.n > 64, p, s);
 }
+// By the entries that may be copied: 1024 take 2.8 to 3.1 us on one block and 3.1 to 3.3 on eight, 1200 to 2000 3.5 to 3.9
+// and 3.1 to 3.5, 4096 4.8 to 5.1 and 3.3 to 3.6 (1 to 64 sequences).
 cudaError_t launch_pages_fork(const PagesParams& p, cudaStream_t s) {
-  return launch_team(pages_fork_kernel<1>, pages_fork_kernel<8>, (int64_t)p.n * p.b.pages_per_seq > 4096, p, s);
+  return launch_team(pages_fork_kernel<1>, pages_fork_kernel<8>, (int64_t)p.n * p.b.pages_per_seq > 1024, p, s);
 }
+// By pages and entries together: 6144 take 6.4 us on one block and 8.1 on eight, 8192 7.6 and 7.8, 16,384 12.6 and 8.3.
 cudaError_t launch_pages_compact(const PagesParams& p, cudaStream_t s) {
   return launch_team(pages_compact_kernel<1>, pages_compact_kernel<8>,
-                     p.b.pool_pages + (int64_t)p.b.n_seqs * p.b.pages_per_seq > 4096, p, s);
+                     p.b.pool_pages + (int64_t)p.b.n_seqs * p.b.pages_per_seq > 8192, p, s);
 }
 
 cudaError_t launch_page_copy(const ls_kv_cache& c, const int32_t* copies, int64_t n, uint32_t* status, cudaStream_t s) {
