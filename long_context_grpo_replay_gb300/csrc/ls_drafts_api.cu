@@ -237,7 +237,7 @@ ls_status ls_pages_compact(const ls_page_book* book, int32_t* table_out, int32_t
             moves{copies, 12 * (uint64_t)(book->pool_pages / 2)};
   if (!apart({out_refs, moves}, {table, lengths_of(*book), out_table}) || !apart({out_table, moves}, {refs, lengths_of(*book), out_refs}) ||
       (refs_out != book->refs && overlap(out_refs, refs)) || (table_out != book->page_table && overlap(out_table, table)))
-    return fail(LS_ERR_INVALID_ARGUMENT, "table_out, refs_out and copies must not overlap each other or the book (but each may be the book's own)");
+    return fail(LS_ERR_INVALID_ARGUMENT, "table_out, refs_out and copies must not overlap each other or the book (but the first two may be its own)");
   p.copies = copies;
   p.table_out = table_out;
   p.refs_out = refs_out;

@@ -31,7 +31,7 @@
 // within about 2^-20 of it (2^-17 at most up to 2^17 tokens), each partial sum is put
 // right afterwards by (Z - Z0) times the sum of its q where e > q Z0 (tokens as near
 // that border weigh 2^-20 of theirs, so that their side does not matter).
-//   Measured: 64 sequences of up to 5 rows x 128,000 (54 MB) 29.5 us: the rows' pass 8
+//   Measured: 64 sequences of up to 5 rows x 128,000 (54 MB) 29.2 us: the rows' pass 8
 // (4.3 TB/s with cold caches), the draw 20, of which half is the weights' arithmetic
 // (34 instructions an element, three issued a cycle on the SMs that hold four blocks)
 // and half the chain of a block's loads, barriers and scans.  Packed pairs with a copy
