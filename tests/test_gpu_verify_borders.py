@@ -244,3 +244,23 @@ def test_caches_go_on_together(cuda_device, value):
         at = slice(m["q_start"][i], m["q_start"][i] + used)
         _, want, _, mag = ref.state_step(states[i], q[at], k[at], v[at], decay[at], beta[at])
         assert ((d[0][i].double().cpu() - want).abs() <= 28 * used * 2.0 ** -24 * mag).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("behind", [0, 600])
+def test_nothing_to_draw_in_the_last_segments(cuda_device, dtype, behind):
+    """The rejected draft alone behind all other tokens, in the last segment or with masked ones behind it, and a random
+    number of 1, which asks for the last token: the last that is left comes out."""
+    n = 64
+    m = make([2] * n, 8191, dtype, False, seed=47)
+    m["u"][:] = 1.0
+    m["u_next"][:] = 1.0
+    for b in range(n):
+        r, d = m["q_start"][b], 8180 - behind - b
+        m["wide"][r] = -math.inf
+        m["wide"][r, d] = -7.0 - 0.13 * b
+        m["wide"][r, 4000:4011] = torch.linspace(0, 1, 11).to(dtype)
+        m["tokens"][r + 1] = d
+    got = run(m)
+    assert got[0].tolist() == [1] * n
+    assert got[1][::2].tolist() == [4010] * n
